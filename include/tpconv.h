@@ -602,6 +602,135 @@ tp_status tp_conv_sph_harm_backward(int32_t lmax, const float* r, int32_t n_edge
                                     const float* grad_Y, const float* grad_rlen, float* grad_r,
                                     hipStream_t stream);
 
+/* ---- layers around the convolution: norm, dropout, attention ------------------
+ * What a potential trains next to the convolution: a layer norm of (the scalar
+ * block of) the node rows, dropout onto the residual, and attention between all
+ * the atoms of a structure, with a learned bias by interatomic distance.  The
+ * pages describe none of these; the formulas below are the definitions.
+ *
+ * Element types: TP_F32 or TP_BF16 for the arrays marked T below.  Sums, row
+ * statistics and softmax statistics are held in 32 bits; each T output is
+ * rounded once.  Arrays marked T need the alignment of their element only,
+ * except where a comment asks for 16 bytes.  Deterministic: no atomics, fixed
+ * summation order. */
+#define TP_F32 0
+#define TP_BF16 1
+
+/* Dropout with probability p (0 <= p < 1) from a counter-based generator
+ * (Philox 4x32 with 10 rounds; Salmon, Moraes, Dror and Shaw, "Parallel Random
+ * Numbers: As Easy as 1, 2, 3", SC 2011): element e (row-major index of the
+ * logical rows x cols array, whatever the strides) is kept when 32-bit word
+ * e % 4 of block (key = seed, counter = (e / 4, offset), 64 bits each, low word
+ * first) is at least floor(p 2^32); a kept value is multiplied by 1 / (1 - p)
+ * (rounded to float32), a dropped one is 0 whatever it held.  No mask is
+ * stored: the backward draws the same words again. */
+typedef struct {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+} tp_dropout;
+
+/* out[e] = dropout(x[e]) + residual[e] (residual NULL: dropout(x)), n elements
+ * of T, contiguous.  out may alias x or residual.  The backward of x is
+ * tp_dropout applied to the upstream gradient (residual NULL); that of the
+ * residual is the identity. */
+tp_status tp_dropout_apply(int32_t dtype, int64_t n, const void* x, const void* residual,
+                           const tp_dropout* drop, void* out, hipStream_t stream);
+
+/* Layer norm of n_rows rows of n_cols values (1..8192), row strides in elements
+ * (>= n_cols), e.g. the 0e block of node rows:
+ *   mu = mean(h), rstd = 1 / sqrt(mean((h - mu)^2) + eps), eps >= 0
+ *   y = (h - mu) rstd gamma + beta
+ * with h = x, or, where residual is given, h = T(dropout(x) + residual)
+ * (contiguous rows, written to h; drop NULL: no dropout).  Without a residual,
+ * drop and h must be NULL.  gamma, beta float32 [n_cols]; mean, rstd float32
+ * [n_rows] (kept for the backward); x, y, h, residual T. */
+tp_status tp_layer_norm_forward(int32_t dtype, int64_t n_rows, int32_t n_cols, const void* x,
+                                int64_t x_stride, const void* residual, const tp_dropout* drop,
+                                const float* gamma, const float* beta, float eps, void* y,
+                                int64_t y_stride, void* h, float* mean, float* rstd,
+                                hipStream_t stream);
+
+/* Workspace bytes of tp_layer_norm_backward (partial sums of the weight
+ * gradients; 0 for few rows). */
+tp_status tp_layer_norm_workspace(int32_t dtype, int64_t n_rows, int32_t n_cols, size_t* bytes);
+
+/* Backward, with z = (h - mu) rstd and t = gamma grad_y:
+ *   grad_h = rstd (t - mean(t) - z mean(t z)) + grad_res   (grad_res: the
+ *            gradient that reaches h past the norm, contiguous, or NULL)
+ *   grad_x = dropout(grad_h)       (NULL: skipped; needs drop)
+ *   grad_gamma = sum_rows grad_y z,  grad_beta = sum_rows grad_y  (both or none NULL)
+ * h with h_stride is the normalised input (x itself without a residual),
+ * grad_y with gy_stride; grad_h (also the residual's gradient) and grad_x
+ * contiguous.  ws: tp_layer_norm_workspace bytes. */
+tp_status tp_layer_norm_backward(int32_t dtype, int64_t n_rows, int32_t n_cols, const void* grad_y,
+                                 int64_t gy_stride, const void* h, int64_t h_stride,
+                                 const float* gamma, const float* mean, const float* rstd,
+                                 const void* grad_res, const tp_dropout* drop, void* grad_h,
+                                 void* grad_x, float* grad_gamma, float* grad_beta, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/* Attention between the atoms of each structure of a packed batch.  Structure b
+ * owns nodes seg_ptr[b] .. seg_ptr[b+1]-1 (n_segments + 1 int32 on the device,
+ * ascending from 0 to n_nodes; entries are clamped into [0, n_nodes], so a wrong
+ * array gives meaningless results but no access out of bounds).  For query i and
+ * key j of one structure, head h, key head g = h / (n_heads / n_kv_heads):
+ *   s_ij = scale q_ih . k_jg + bias[h][bucket(i, j)]
+ *   p_ij = softmax over the unmasked j;  out_ih = sum_j p_ij v_jg
+ *   lse[h][i] = ln sum_j exp s_ij
+ * Rows without any key left get out = 0, lse = -inf and zero gradients; scores at or
+ * below -1e30 count as masked (a bias of -inf or of the type's lowest value
+ * masks its bucket).  Masked keys' rows of k and v are never multiplied: what
+ * they hold, NaN included, reaches no output.
+ * The bucket is a geometric step of the distance (positions as given, no
+ * periodic images): with float32 dx = x_i - x_j, ..., d2 = (dx dx + dy dy) + dz dz,
+ * every operation rounded once, and bits() the float's representation,
+ *   bucket = clamp((bits(d2) >> s) - (bits(r_min r_min) >> s), 0, n_buckets - 1),
+ * s = 23 - log2(steps): `steps` linear steps in each octave of d2, all below r_min in
+ * bucket 0, all beyond the range in the last.  pos NULL: no bias (bias NULL,
+ * n_buckets 0).  The bias has no gradient with respect to the positions (it is
+ * piecewise constant). */
+typedef struct {
+  int32_t dtype;        /* of q, k, v, out, bias and their gradients */
+  int32_t n_nodes, n_segments;
+  int32_t n_heads, n_kv_heads, head_dim; /* n_heads a multiple of n_kv_heads; head_dim a
+                                            multiple of 8, 8..128 */
+  const int32_t* seg_ptr;
+  const uint8_t* key_mask;  /* [n_nodes], 0 = masked key; NULL: none masked */
+  const float* pos;         /* [n_nodes][3] */
+  const void* bias;         /* T [n_heads][n_buckets] */
+  int32_t n_buckets;        /* 1..64 */
+  int32_t steps;            /* 1, 2, 4 or 8 */
+  float r_min;              /* > 0 */
+  float scale;
+} tp_attn;
+
+/* Forward.  q, out [n_nodes] rows of n_heads x head_dim, k, v of n_kv_heads x
+ * head_dim, T, each with its row stride in elements (views of one projected row
+ * are fine); base pointers and strides in bytes must be multiples of 16 (TP_ERR_ARG).
+ * lse float32 [n_heads][n_nodes]. */
+tp_status tp_attn_forward(const tp_attn* a, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, void* out,
+                          int64_t out_stride, float* lse, hipStream_t stream);
+
+/* Workspace bytes of tp_attn_backward for this description (pointers unused). */
+tp_status tp_attn_backward_workspace(const tp_attn* a, size_t* bytes);
+
+/* Backward: recomputes the probabilities from q, k and lse (no pair-sized array
+ * is read or written):
+ *   dp_ij = grad_out_i . v_j,  ds_ij = p_ij (dp_ij - grad_out_i . out_i)
+ *   grad_q_i = scale sum_j ds_ij k_j;  grad_k_j, grad_v_j summed over the query
+ *   heads that share the key head;  grad_bias[h][c] = sum of ds over bucket c.
+ * out and lse are tp_attn_forward's.  grad_out, grad_q [n_nodes][n_heads][head_dim]
+ * and grad_k, grad_v [n_nodes][n_kv_heads][head_dim] with their strides (16-byte
+ * multiples as above), grad_bias T [n_heads][n_buckets] (NULL: skipped). */
+tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, const void* k,
+                           int64_t k_stride, const void* v, int64_t v_stride, const void* out,
+                           int64_t out_stride, const float* lse, const void* grad_out,
+                           int64_t go_stride, void* grad_q, int64_t gq_stride, void* grad_k,
+                           int64_t gk_stride, void* grad_v, int64_t gv_stride, void* grad_bias,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Thread-local description of the last failure on this thread (helper for
  * error reporting; valid until the next failing call on the thread). */
 const char* tp_conv_last_error(void);

@@ -38,6 +38,8 @@ EXPORTS = (
     "tp_conv_forward_fc", "tp_conv_fc_backward_workspace", "tp_conv_backward_fc", "tp_conv_fc_double_workspace",
     "tp_conv_double_backward_fc", "tp_conv_gaunt_dims", "tp_conv_forward_gaunt", "tp_conv_backward_gaunt",
     "tp_conv_gaunt_double_workspace", "tp_conv_double_backward_gaunt",
+    "tp_dropout_apply", "tp_layer_norm_forward", "tp_layer_norm_workspace", "tp_layer_norm_backward",
+    "tp_attn_forward", "tp_attn_backward_workspace", "tp_attn_backward",
     "tp_conv_last_error",
 )
 
@@ -127,6 +129,15 @@ def lib():
         "tp_conv_radial_workspace": (I32, [P, I32, I32, ctypes.POINTER(SZ)]),
         "tp_conv_double_backward_radial": (I32, [P, ctypes.POINTER(_Graph)] + [VP] * 18 + [SZ, VP]),
         "tp_conv_radial_double_workspace": (I32, [P, I32, I32, ctypes.POINTER(SZ)]),
+        "tp_dropout_apply": (I32, [I32, I64, VP, VP, VP, VP, VP]),
+        "tp_layer_norm_forward": (I32, [I32, I64, I32, VP, I64, VP, VP, VP, VP, ctypes.c_float, VP, I64, VP, VP, VP,
+                                        VP]),
+        "tp_layer_norm_workspace": (I32, [I32, I64, I32, ctypes.POINTER(SZ)]),
+        "tp_layer_norm_backward": (I32, [I32, I64, I32, VP, I64, VP, I64, VP, VP, VP, VP, VP, VP, VP, VP, VP, VP, SZ,
+                                         VP]),
+        "tp_attn_forward": (I32, [VP] + [VP, I64] * 4 + [VP, VP]),
+        "tp_attn_backward_workspace": (I32, [VP, ctypes.POINTER(SZ)]),
+        "tp_attn_backward": (I32, [VP] + [VP, I64] * 4 + [VP] + [VP, I64] * 4 + [VP, VP, SZ, VP]),
         "tp_conv_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -939,3 +950,8 @@ def radial_workspace(plan, n_nodes, with_mix):
     b = ctypes.c_size_t()
     _check(lib().tp_conv_radial_workspace(plan.handle, n_nodes, int(bool(with_mix)), ctypes.byref(b)))
     return b.value
+
+
+from .layers import (Dropout, attn_backward, attn_forward, dropout_backward, dropout_forward,  # noqa: E402,F401
+                     layer_norm_backward, layer_norm_forward, layer_norm_residual_backward,
+                     layer_norm_residual_forward)

@@ -1,0 +1,411 @@
+// Pieces shared by the attention kernels (attn_fwd.hip, attn_dq.hip, attn_dkv.hip).
+//
+// A wave owns 32 rows (queries, or keys in the key-side backward) and walks the
+// other side in tiles of 32 rows staged in LDS.  Products run on
+// v_mfma_f32_32x32x16_bf16 with the staged tile as the A operand, so a score tile
+// comes out transposed: lane l holds column l % 32 (its own row) and tile rows
+// 8 (i / 4) + 4 (l / 32) + i % 4, i = 0..15.  Softmax statistics are then one
+// value per lane, and the tile is already the B operand of the next product
+// (the order of a contraction index is free as long as A uses the same one),
+// with the A operand read column-wise through the LDS transpose loads.
+//
+// float32 operands are split exactly into three bfloat16 pieces, x = hi + mid + lo
+// (8 + 8 + 8 significand bits, taken by truncation), and a product is the six
+// partial products down to 2^-16 relative; what is left out is below 2^-23, the
+// size of float32's own rounding.  Six bfloat16 MFMA cost 192 cycles per 32x32x16
+// against 512 for the float32 MFMA.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "internal.hpp"
+#include "rows.hpp"
+
+namespace tpc {
+
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4 lds_s4;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLowest = -1e30f;         // scores at or below count as masked
+constexpr int kTile = 32;
+constexpr int kMaxBuckets = 64;
+
+template <typename T>
+constexpr int kPlanes = std::is_same<T, float>::value ? 3 : 1;
+
+// geometry of a staged tile: 32 rows of KS * 16 values (zero-filled from head_dim
+// on), rows padded by 16 bytes so that 16-byte reads of 32 rows spread over
+// the banks (the row length in 16-byte units is odd)
+template <typename T, int KS>
+struct Tile {
+  static constexpr int P = kPlanes<T>;
+  static constexpr int MT = (KS + 1) / 2;            // 32-row blocks of the head dimension
+  static constexpr int kRow = 32 * MT + 8;           // 16-bit elements per row
+  static constexpr int kPlane = kTile * kRow;
+  static constexpr int kElems = P * kPlane;
+};
+
+template <int P>
+struct Frag {
+  b8 p[P];
+};
+
+__device__ __forceinline__ f16v mma(const Frag<1>& a, const Frag<1>& b, f16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
+}
+// smallest partial products first
+__device__ __forceinline__ f16v mma(const Frag<3>& a, const Frag<3>& b, f16v c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float flt(uint32_t x) { return __builtin_bit_cast(float, x); }
+// the upper halves of two words, the first in the low half
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+}
+
+// eight float32 values as an operand: one rounding (bfloat16) or the exact split
+__device__ __forceinline__ void to_frag(const float* x, Frag<1>& f) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.p[0][j] = (__bf16)x[j];
+}
+__device__ __forceinline__ void to_frag(const float* x, Frag<3>& f) {
+  u4 h, m, l;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = x[2 * j], b = x[2 * j + 1];
+    const float ra = a - flt(bits(a) & 0xffff0000u), rb = b - flt(bits(b) & 0xffff0000u);
+    const float sa = ra - flt(bits(ra) & 0xffff0000u), sb = rb - flt(bits(rb) & 0xffff0000u);
+    h[j] = high_halves(bits(a), bits(b));
+    m[j] = high_halves(bits(ra), bits(rb));
+    l[j] = high_halves(bits(sa), bits(sb));          // at most 8 bits left: exact
+  }
+  f.p[0] = __builtin_bit_cast(b8, h);
+  f.p[1] = __builtin_bit_cast(b8, m);
+  f.p[2] = __builtin_bit_cast(b8, l);
+}
+
+// eight consecutive values of a row, as loaded from memory
+template <typename T>
+struct Raw;
+template <>
+struct Raw<bf16_t> {
+  u4 v;
+  __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const u4*>(p); }
+  __device__ __forceinline__ void keep(bool k) { v = k ? v : u4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void frag(Frag<1>& f) const { f.p[0] = __builtin_bit_cast(b8, v); }
+  __device__ __forceinline__ float at(int j) const { return (float)__builtin_bit_cast(b8, v)[j]; }
+};
+template <>
+struct Raw<float> {
+  f4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const f4*>(p);
+    b = *reinterpret_cast<const f4*>(p + 4);
+  }
+  __device__ __forceinline__ void keep(bool k) {
+    a = k ? a : f4{0.f, 0.f, 0.f, 0.f};
+    b = k ? b : f4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void frag(Frag<3>& f) const {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    to_frag(x, f);
+  }
+  __device__ __forceinline__ float at(int j) const { return j < 4 ? a[j] : b[j - 4]; }
+};
+
+// row operand: tile row l % 32, contraction elements 16 kk + 8 (l / 32) + 0..7
+template <typename T, int KS>
+__device__ __forceinline__ Frag<kPlanes<T>> row_frag(const uint16_t* tile, int kk, int lane) {
+  using G = Tile<T, KS>;
+  Frag<G::P> f;
+#pragma unroll
+  for (int p = 0; p < G::P; ++p)
+    f.p[p] = *reinterpret_cast<const b8*>(tile + p * G::kPlane + (lane & 31) * G::kRow + 16 * kk + 8 * (lane >> 5));
+  return f;
+}
+
+// column operand: element 32 mt + l % 32 of the head dimension, tile rows
+// 16 kb + 4 (l / 32) + {0..3, 8..11}: the rows whose scores the lane holds.  The
+// transpose load hands lane i of a group of 16 the i-th column of the 4 rows x 16
+// columns that the group addresses (4 lanes a row).
+template <typename T, int KS>
+__device__ __forceinline__ Frag<kPlanes<T>> col_frag(const uint16_t* tile, int mt, int kb, int lane) {
+  using G = Tile<T, KS>;
+  Frag<G::P> f;
+  const int row = 16 * kb + 4 * (lane >> 5) + ((lane & 15) >> 2), col = 32 * mt + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+#pragma unroll
+  for (int p = 0; p < G::P; ++p) {
+    const uint16_t* at = tile + p * G::kPlane + row * G::kRow + col;
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 8 * G::kRow));
+    f.p[p] = __builtin_bit_cast(b8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  return f;
+}
+
+// store eight consecutive values into a staged tile
+template <typename T, int KS>
+__device__ __forceinline__ void put(uint16_t* tile, int row, int col8, const Raw<T>& r) {
+  using G = Tile<T, KS>;
+  Frag<G::P> f;
+  r.frag(f);
+#pragma unroll
+  for (int p = 0; p < G::P; ++p)
+    *reinterpret_cast<b8*>(tile + p * G::kPlane + row * G::kRow + 8 * col8) = f.p[p];
+}
+
+// the larger of a lane's value and that of the lane 32 away (which holds the other
+// half of the same row), and the same for sums
+__device__ __forceinline__ float pair_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+  return fmaxf(flt(r[0]), flt(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+  return flt(r[0]) + flt(r[1]);
+}
+
+// Tile t of the packed batch in tiles of `rows` rows: structure b's tiles start at
+// number seg[b] / rows + b, which never overlap and leave at most one unused
+// number per structure, so a grid of n_nodes / rows + n_segments tiles covers every
+// batch without the host knowing the lengths.  The wave looks b up 64 entries
+// at a time (1 step up to 64 structures, 2 up to 4,096).  False: an unused number.
+__device__ __forceinline__ bool find_tile(const tp_attn& d, int rows, int t, int& lo, int& hi, int& first) {
+  const int lane = threadIdx.x & 63, N = d.n_nodes;
+  int b = 0, n = d.n_segments;
+  while (n > 1) {
+    const int step = (n + 63) >> 6;
+    const int at = b + lane * step;
+    bool le = false;
+    if (lane * step < n) {
+      const int s = min(max(d.seg_ptr[at], 0), N);
+      le = s / rows + at <= t;
+    }
+    const int cnt = __popcll(__ballot(le));
+    if (cnt == 0) return false;            // not a valid seg_ptr
+    b += (cnt - 1) * step;
+    n = min(step, n - (cnt - 1) * step);
+  }
+  b = __builtin_amdgcn_readfirstlane(b);
+  lo = min(max(d.seg_ptr[b], 0), N);
+  hi = min(max(d.seg_ptr[b + 1], 0), N);
+  const int64_t q = (int64_t)lo + (int64_t)(t - (lo / rows + b)) * rows;
+  first = (int)q;
+  return q >= lo && q < hi;
+}
+
+// LDS bias table of HG heads, [entry][HG][32], base-2 units; 32 copies of every value,
+// so that the lanes of a half wave, each with a bucket of its own, read 32 different
+// banks.  The entry after the last bucket masks.
+__device__ __forceinline__ float bias_at(const tp_attn& d, int h, int b) {
+  const size_t i = (size_t)h * d.n_buckets + b;
+  return d.dtype == TP_F32 ? static_cast<const float*>(d.bias)[i] : (float)static_cast<const bf16_t*>(d.bias)[i];
+}
+template <int HG>
+__device__ __forceinline__ void fill_table(const tp_attn& d, int h0, float* tbl, int threads) {
+  const int ne = d.n_buckets > 0 ? d.n_buckets : 1;
+  for (int i = threadIdx.x; i < (ne + 1) * HG * 32; i += threads) {
+    const int hh = (i >> 5) % HG, b = (i >> 5) / HG;
+    tbl[i] = b == ne ? -INFINITY : d.n_buckets > 0 ? bias_at(d, h0 + hh, b) * kLog2e : 0.f;
+  }
+}
+
+// bucket -> byte offset of this lane's copy in the table
+template <int HG>
+struct Buckets {
+  int shift, lo, hi, add, first, masked;   // first: the only entry where there is no bias
+  __device__ __forceinline__ explicit Buckets(const tp_attn& d, int lane) {
+    int lg = 0;
+    while ((1 << lg) < d.steps) ++lg;
+    shift = 23 - lg;
+    const int base = (int)(bits(d.r_min * d.r_min) >> shift), nb = d.n_buckets > 0 ? d.n_buckets : 1;
+    lo = base << shift;
+    hi = ((base + nb) << shift) - 1;
+    first = (lane & 31) * 4;
+    add = first - base * HG * 128;
+    masked = first + nb * HG * 128;
+  }
+  // the squared distance, every operation rounded once (no fused multiply-add)
+  __device__ __forceinline__ int offset(float ax, float ay, float az, float bx, float by, float bz) const {
+#pragma clang fp contract(off)
+    const float dx = ax - bx, dy = ay - by, dz = az - bz;
+    const float xx = dx * dx, yy = dy * dy, zz = dz * dz;
+    const float d2 = (xx + yy) + zz;
+    const int c = min(max((int)bits(d2), lo), hi);
+    return (c >> shift) * (HG * 128) + add;
+  }
+};
+
+__device__ __forceinline__ float table(const float* tbl, int off, int hh) {
+  return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(tbl) + off + hh * 128);
+}
+
+// table offsets of the 16 tile rows that a lane holds: bucket of (own position, row's
+// position), masked rows sent to the masking entry.  pos: LDS [3][np] rows of the
+// tile from `at`; valid: bit r set where tile row r counts.
+template <int HG>
+__device__ __forceinline__ void tile_offsets(const Buckets<HG>& bk, bool biased, const float* pos, int np, int at, int half,
+                                             float x, float y, float z, uint32_t valid, int off[16]) {
+  if (biased) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int r = at + 8 * g + 4 * half;
+      const f4 px = *reinterpret_cast<const f4*>(pos + r), py = *reinterpret_cast<const f4*>(pos + np + r),
+               pz = *reinterpret_cast<const f4*>(pos + 2 * np + r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) off[4 * g + j] = bk.offset(x, y, z, px[j], py[j], pz[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) off[i] = bk.first;
+  }
+  if (valid != 0xffffffffu) {
+    const uint32_t m = valid >> (4 * half);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) off[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? off[i] : bk.masked;
+  }
+}
+
+// Staging of W tiles of 32 rows side by side (rows r0 + 32 w ..), NS head slots of two
+// arrays each (tile number (w NS + slot) 2 + array): every thread fetches its
+// 8-value chunks into registers while the previous step computes, then puts
+// them into LDS.  Rows past the end or masked are staged as zeros.
+template <typename T, int KS, int NT, int W, int NS>
+struct Stager {
+  using G = Tile<T, KS>;
+  static constexpr int kTiles = W * NS * 2;
+  static constexpr int kChunks = (kTiles * kTile * 2 * KS + NT - 1) / NT;
+  static constexpr int kBytes = kTiles * G::kElems * 2;
+  Raw<T> raw[kChunks];
+  bool live[kChunks];
+
+  template <typename Head>
+  __device__ __forceinline__ void fetch(const void* p0, int64_t s0, const void* p1, int64_t s1, int r0, int end, int D,
+                                        const uint8_t* mask, Head&& head) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = threadIdx.x + i * NT, col = c % (2 * KS), row = c / (2 * KS) % kTile, t = c / (2 * KS * kTile);
+      const int r = r0 + 32 * ((t >> 1) / NS) + row;
+      live[i] = t < kTiles && r < end && 8 * col < D;
+      if (live[i]) {
+        const T* p = t & 1 ? static_cast<const T*>(p1) + (size_t)r * s1 : static_cast<const T*>(p0) + (size_t)r * s0;
+        raw[i].load(p + (size_t)head((t >> 1) % NS) * D + 8 * col);
+        if (mask) live[i] = mask[r] != 0;
+      }
+    }
+  }
+  __device__ __forceinline__ void stage(uint16_t* tiles) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = threadIdx.x + i * NT, col = c % (2 * KS), row = c / (2 * KS) % kTile, t = c / (2 * KS * kTile);
+      raw[i].keep(live[i]);
+      if (t < kTiles) put<T, KS>(tiles + t * G::kElems, row, col, raw[i]);
+    }
+  }
+};
+
+// positions of NP rows, one per thread of the first NP
+template <int NP>
+struct PosStager {
+  float x = 0.f, y = 0.f, z = 0.f;
+  __device__ __forceinline__ void fetch(const float* pos, int r0, int end) {
+    if ((int)threadIdx.x < NP) {
+      const int r = min(r0 + (int)threadIdx.x, end - 1);
+      x = pos[3 * (size_t)r];
+      y = pos[3 * (size_t)r + 1];
+      z = pos[3 * (size_t)r + 2];
+    }
+  }
+  __device__ __forceinline__ void stage(float* lds) const {
+    if ((int)threadIdx.x < NP) {
+      lds[threadIdx.x] = x;
+      lds[NP + threadIdx.x] = y;
+      lds[2 * NP + threadIdx.x] = z;
+    }
+  }
+};
+
+// the wave's own rows as B operands: row `r`, contraction elements 16 kk + 8 half ..
+template <typename T, int KS>
+__device__ __forceinline__ void own_rows(const void* p, int64_t stride, int r, int head, int D, int half, bool keep,
+                                         Frag<kPlanes<T>> f[KS]) {
+#pragma unroll
+  for (int kk = 0; kk < KS; ++kk) {
+    const int c = 16 * kk + 8 * half;
+    Raw<T> w;
+    w.load(static_cast<const T*>(p) + (size_t)r * stride + (size_t)head * D + (c < D ? c : 0));
+    w.keep(keep && c < D);
+    w.frag(f[kk]);
+  }
+}
+
+// a transposed accumulator (lane: own row; registers: head dimension) times `by` to memory
+template <typename T, int MT>
+__device__ __forceinline__ void store_rows(void* p, int64_t stride, int r, int head, int D, int half, const f16v acc[MT],
+                                           float by, bool zero) {
+  T* o = static_cast<T*>(p) + (size_t)r * stride + (size_t)head * D;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int e = 32 * mt + 8 * g + 4 * half;
+      if (e < D) {
+        T v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (T)(zero ? 0.f : acc[mt][4 * g + j] * by);
+        __builtin_memcpy(__builtin_assume_aligned(o + e, 4 * sizeof(T)), v, sizeof(v));
+      }
+    }
+}
+
+// accumulators of one wave to LDS, and added to another wave's
+template <int MT>
+__device__ __forceinline__ void park(float* at, const f16v acc[MT]) {
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) at[64 * (16 * mt + i)] = acc[mt][i];
+}
+template <int MT>
+__device__ __forceinline__ void add_parked(const float* at, float mine, float theirs, f16v acc[MT]) {
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[mt][i] = acc[mt][i] * mine + at[64 * (16 * mt + i)] * theirs;
+}
+
+template <int MT>
+__device__ __forceinline__ void clear(f16v acc[MT]) {
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[mt][i] = 0.f;
+}
+
+constexpr size_t kLdsMax = 160 * 1024;
+
+// a kernel that may use all of a CU's LDS, launched with `bytes` of it
+template <typename K, typename... A>
+hipError_t launch_lds(K kernel, dim3 grid, int threads, size_t bytes, hipStream_t st, A... args) {
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)kLdsMax);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, grid, dim3(threads), bytes, st, args...);
+  return hipGetLastError();
+}
+
+}  // namespace tpc

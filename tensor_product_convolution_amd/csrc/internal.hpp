@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "../../include/tpconv.h"
+#include "philox.hpp"
 
 namespace tpc {
 
@@ -186,5 +187,53 @@ tp_status uvw_forward(int n_nodes, int U, int outdim, const UvwIrreps& irr, cons
                       const float* X, float* Z, bool trans_w, hipStream_t st);
 tp_status uvw_grad_w(int n_nodes, int U, int outdim, const UvwIrreps& irr, const float* X,
                      const float* G, float* gradW, void* ws, hipStream_t st);
+
+
+// ---- layers around the convolution (norm.hip, attn*.hip) ----------------------
+struct NormArgs {
+  int dtype = TP_F32, n_cols = 0;
+  int64_t n_rows = 0, x_stride = 0, y_stride = 0;
+  const void *x = nullptr, *residual = nullptr;   // residual null: h is x
+  bool has_drop = false;
+  DropArgs drop;
+  const float *gamma = nullptr, *beta = nullptr;
+  float eps = 0.f;
+  void *y = nullptr, *h = nullptr;
+  float *mean = nullptr, *rstd = nullptr;
+  hipStream_t stream = nullptr;
+};
+struct NormBwdArgs {
+  int dtype = TP_F32, n_cols = 0;
+  int64_t n_rows = 0, gy_stride = 0, h_stride = 0;
+  const void *grad_y = nullptr, *h = nullptr, *grad_res = nullptr;
+  const float *gamma = nullptr, *mean = nullptr, *rstd = nullptr;
+  DropArgs drop;                                  // used where grad_x is set
+  void *grad_h = nullptr, *grad_x = nullptr;
+  float *grad_gamma = nullptr, *grad_beta = nullptr, *part = nullptr;
+  hipStream_t stream = nullptr;
+};
+constexpr int kNormMaxCols = 8192;
+size_t norm_workspace_bytes(int dtype, int64_t n_rows, int n_cols);
+hipError_t norm_forward(const NormArgs& a);
+hipError_t norm_backward(const NormBwdArgs& a);
+hipError_t dropout_apply(int dtype, int64_t n, const void* x, const void* r, const DropArgs& d, void* out,
+                         hipStream_t st);
+
+struct AttnArgs {
+  tp_attn d;
+  const void *q = nullptr, *k = nullptr, *v = nullptr, *out_in = nullptr, *go = nullptr;
+  int64_t qs = 0, ks = 0, vs = 0, os = 0, gos = 0, gqs = 0, gks = 0, gvs = 0;   // row strides, elements
+  void *out = nullptr, *gq = nullptr, *gk = nullptr, *gv = nullptr, *gbias = nullptr;
+  float* lse = nullptr;
+  const float* lse_in = nullptr;
+  float *delta = nullptr, *part = nullptr;        // workspace of the backward
+  hipStream_t stream = nullptr;
+};
+hipError_t attn_forward(const AttnArgs& a);
+hipError_t attn_backward(const AttnArgs& a);
+hipError_t attn_backward_q(const AttnArgs& a);   // its query side (attn_dq.hip)
+// floats of the workspace: delta [n_heads][n_nodes], then the bias gradient's parts
+size_t attn_delta_floats(const tp_attn& d);
+size_t attn_part_floats(const tp_attn& d);
 
 }  // namespace tpc
