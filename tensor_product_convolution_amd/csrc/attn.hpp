@@ -255,11 +255,10 @@ __device__ __forceinline__ float table(const float* tbl, int off, int hh) {
 }
 
 // table offsets of the 16 tile rows that a lane holds: bucket of (own position, row's
-// position), masked rows sent to the masking entry.  pos: LDS [3][np] rows of the
-// tile from `at`; valid: bit r set where tile row r counts.
+// position).  pos: LDS [3][np], the tile's rows from `at`.
 template <int HG>
 __device__ __forceinline__ void tile_offsets(const Buckets<HG>& bk, bool biased, const float* pos, int np, int at, int half,
-                                             float x, float y, float z, uint32_t valid, int off[16]) {
+                                             float x, float y, float z, int off[16]) {
   if (biased) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -273,11 +272,13 @@ __device__ __forceinline__ void tile_offsets(const Buckets<HG>& bk, bool biased,
 #pragma unroll
     for (int i = 0; i < 16; ++i) off[i] = bk.first;
   }
-  if (valid != 0xffffffffu) {
-    const uint32_t m = valid >> (4 * half);
+}
+// tile rows that do not count (bit r of valid clear) to the masking entry
+template <int HG>
+__device__ __forceinline__ void mask_offsets(const Buckets<HG>& bk, uint32_t valid, int half, int off[16]) {
+  const uint32_t m = valid >> (4 * half);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) off[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? off[i] : bk.masked;
-  }
+  for (int i = 0; i < 16; ++i) off[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? off[i] : bk.masked;
 }
 
 // Staging of W tiles of 32 rows side by side (rows r0 + 32 w ..), NS head slots of two

@@ -1,12 +1,15 @@
-// Attention backward, query side: grad_q and the bias gradient.
+// Attention backward, query side: grad_q, and delta for the key side.
 //
-//   p = exp(s - lse),  dp = grad_out v^T,  ds = p (dp - delta),
-//   grad_q = scale ds k,  grad_bias[bucket] += ds,  delta = grad_out . out
+//   p = exp(s - lse),  dp = grad_out v^T,  ds = p (dp - delta),  grad_q = scale ds k,
+//   delta = grad_out . out
 //
-// A wave owns 32 queries and walks the keys as the forward does.  delta is formed
-// from the wave's own rows and kept for the key side.  The bias gradient goes
-// into LDS columns private to the lane (no two lanes add to one word, so the
-// order of the sums is fixed), summed per workgroup and joined by a second kernel.
+// A wave owns 32 queries and walks the keys as the forward does, with delta formed
+// from its own rows.  That delta carries the rounding of out (and the products
+// theirs), so a row of ds does not quite sum to zero.  grad_q does not notice, but
+// the bias gradient of a bucket that holds most pairs is a sum of millions of
+// terms that nearly cancel: it came out 5e-3 (bfloat16) and 2e-5 (float32) off at
+// 1,536 atoms.  So the row sums r = sum_j ds_ij are kept too, and the key side, which
+// forms ds again, takes delta + r.
 #include "attn.hpp"
 
 #include <algorithm>
@@ -19,13 +22,11 @@ struct DqShape {
   using G = Tile<T, KS>;
   static constexpr int kThreads = 64 * QW * KW, kRows = kTile * KW;
   using Stage = Stager<T, KS, kThreads, KW, NKV>;
-  static constexpr int kPart = G::MT * 16 * 64;
+  static constexpr int kPart = (G::MT * 16 + 1) * 64;
   static constexpr int kJoin = QW * (KW - 1) * HG * kPart * 4;
   static constexpr int kTileBytes = Stage::kBytes > kJoin ? Stage::kBytes : kJoin;
-  static size_t entries(int nb) { return (size_t)(nb > 0 ? nb : 1) + 1; }
-  static size_t lds_bytes(int nb, bool grad) {
-    return (size_t)kTileBytes + 12 * kRows + 16 * KW + entries(nb) * HG * 128 +
-           (grad ? (size_t)QW * KW * entries(nb) * HG * 256 : 0);
+  static size_t lds_bytes(int nb) {
+    return (size_t)kTileBytes + 12 * kRows + 16 * KW + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128;
   }
   static constexpr int kRegs = HG * (2 * KS * G::P * 4 + G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 4 : 8);
 };
@@ -35,33 +36,22 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     k_attn_dq(AttnArgs a) {
   using S = DqShape<T, KS, HG, NKV, QW, KW>;
   using G = Tile<T, KS>;
-  constexpr int P = G::P, MT = G::MT, NP = S::kRows, NW = QW * KW;
+  constexpr int P = G::P, MT = G::MT, NP = S::kRows;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   uint16_t* tiles = reinterpret_cast<uint16_t*>(lds);
   float* pos = reinterpret_cast<float*>(lds + S::kTileBytes);
   uint32_t* valid = reinterpret_cast<uint32_t*>(pos + 3 * NP);
   float* tbl = reinterpret_cast<float*>(valid + 4 * KW);
   const tp_attn& d = a.d;
-  const int nb = d.n_buckets, ne = (nb > 0 ? nb : 1) + 1;
-  float* gcol = tbl + ne * HG * 32;        // [NW][ne][HG][64] bias gradient columns
   const int h0 = blockIdx.y * HG;
   int lo, hi, q0;
-  if (!find_tile(d, kTile * QW, blockIdx.x, lo, hi, q0)) {
-    if (a.gbias)
-      for (int i = threadIdx.x; i < HG * nb; i += S::kThreads)
-        a.part[((size_t)(h0 + i / nb) * gridDim.x + blockIdx.x) * nb + i % nb] = 0.f;
-    return;
-  }
+  if (!find_tile(d, kTile * QW, blockIdx.x, lo, hi, q0)) return;
   const int lane = threadIdx.x & 63, half = lane >> 5, wv = threadIdx.x >> 6;
   const int kw = wv % KW, qw = wv / KW;
   const int rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
-  const bool biased = nb > 0;
+  const bool biased = d.n_buckets > 0;
   fill_table<HG>(d, h0, tbl, S::kThreads);
-  if (a.gbias)
-    for (int i = threadIdx.x; i < NW * ne * HG * 64; i += S::kThreads) gcol[i] = 0.f;
   const Buckets<HG> bk(d, lane);
-  // table offset -> byte offset of the lane's column of the same entry (twice as wide)
-  char* mycol = reinterpret_cast<char*>(gcol + (size_t)wv * ne * HG * 64) + 4 * lane - 8 * (lane & 31);
 
   const int q = q0 + 32 * qw + (lane & 31), qc = q < hi ? q : hi - 1;
   float x = 0.f, y = 0.f, z = 0.f;
@@ -93,7 +83,6 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     const float e = a.lse_in[at];
     // a row without keys has lse = -inf: p = exp2(s - inf) = 0
     lse[hh] = q < hi && e != -INFINITY ? e * kLog2e : INFINITY;
-    if (kw == 0 && half == 0 && q < hi) a.delta[at] = delta[hh];
   }
 
   typename S::Stage st;
@@ -109,8 +98,12 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
   };
 
   f16v dQ[HG][MT];
+  float r[HG];
 #pragma unroll
-  for (int hh = 0; hh < HG; ++hh) clear<MT>(dQ[hh]);
+  for (int hh = 0; hh < HG; ++hh) {
+    r[hh] = 0.f;
+    clear<MT>(dQ[hh]);
+  }
   const float c = d.scale * kLog2e;
 
   fetch(lo);
@@ -126,7 +119,8 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     const uint32_t vm = __builtin_amdgcn_readfirstlane(valid[4 * kw]);
     if (vm == 0) continue;
     int off[16];
-    tile_offsets<HG>(bk, biased, pos, NP, 32 * kw, half, x, y, z, vm, off);
+    tile_offsets<HG>(bk, biased, pos, NP, 32 * kw, half, x, y, z, off);
+    if (vm != 0xffffffffu) mask_offsets<HG>(bk, vm, half, off);
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
       const uint16_t* kt = tiles + (size_t)((kw * NKV + (NKV == 1 ? 0 : hh)) * 2) * G::kElems;
@@ -142,12 +136,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
       for (int i = 0; i < 16; ++i) {
         const float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, table(tbl, off[i], hh)) - lse[hh]);
         ds[i] = p * (dp[i] - delta[hh]);
-      }
-      if (a.gbias) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          __hip_atomic_fetch_add(reinterpret_cast<float*>(mycol + 2 * off[i] + hh * 256), ds[i], __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_WORKGROUP);
+        r[hh] += ds[i];
       }
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
@@ -159,81 +148,52 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     }
   }
 
-  float* join = reinterpret_cast<float*>(lds) + (size_t)qw * (KW - 1) * HG * S::kPart + lane;
-  __syncthreads();
-  if (KW > 1 && kw > 0) {
-#pragma unroll
-    for (int hh = 0; hh < HG; ++hh) park<MT>(join + ((kw - 1) * HG + hh) * S::kPart, dQ[hh]);
-  }
-  if (a.gbias) {
-    // an entry's 64 columns of every wave; lanes start at different columns so that they
-    // read different banks
-    for (int i = threadIdx.x; i < nb * HG; i += S::kThreads) {
-      const int b = i / HG, hh = i % HG;
-      float s = 0.f;
-      for (int w = 0; w < NW; ++w)
-#pragma unroll 8
-        for (int j = 0; j < 64; ++j) s += gcol[((size_t)(w * ne + b) * HG + hh) * 64 + ((j + lane) & 63)];
-      a.part[((size_t)(h0 + hh) * gridDim.x + blockIdx.x) * nb + b] = s;
-    }
-  }
   if (KW > 1) {
+    float* join = reinterpret_cast<float*>(lds) + (size_t)qw * (KW - 1) * HG * S::kPart + lane;
+    __syncthreads();
+    if (kw > 0) {
+#pragma unroll
+      for (int hh = 0; hh < HG; ++hh) {
+        float* w = join + ((kw - 1) * HG + hh) * S::kPart;
+        w[0] = r[hh];
+        park<MT>(w + 64, dQ[hh]);
+      }
+    }
     __syncthreads();
     if (kw > 0) return;
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh)
-      for (int o = 0; o < KW - 1; ++o) add_parked<MT>(join + (o * HG + hh) * S::kPart, 1.f, 1.f, dQ[hh]);
+      for (int o = 0; o < KW - 1; ++o) {
+        const float* w = join + (o * HG + hh) * S::kPart;
+        r[hh] += w[0];
+        add_parked<MT>(w + 64, 1.f, 1.f, dQ[hh]);
+      }
   }
-  if (q < hi) {
 #pragma unroll
-    for (int hh = 0; hh < HG; ++hh) store_rows<T, MT>(a.gq, a.gqs, q, h0 + hh, D, half, dQ[hh], d.scale, false);
+  for (int hh = 0; hh < HG; ++hh) {
+    const float sum = pair_sum(r[hh]);
+    if (q < hi) {
+      if (half == 0) a.delta[(size_t)(h0 + hh) * d.n_nodes + q] = delta[hh] + sum;
+      store_rows<T, MT>(a.gq, a.gqs, q, h0 + hh, D, half, dQ[hh], d.scale, false);
+    }
   }
-}
-
-// grad_bias[h][b] = sum over the tiles' parts, in a fixed order.
-constexpr int kJoinThreads = 1024;
-template <typename T>
-__global__ void __launch_bounds__(kJoinThreads)
-    k_attn_join_bias(const float* __restrict__ part, int n, int nb, T* __restrict__ out) {
-  __shared__ float lds[kJoinThreads];
-  const int h = blockIdx.x, b = threadIdx.x & 63, g = threadIdx.x >> 6;
-  float s = 0.f;
-  if (b < nb) {
-#pragma unroll 8
-    for (int t = g; t < n; t += kJoinThreads / 64) s += part[((size_t)h * n + t) * nb + b];
-  }
-  lds[threadIdx.x] = s;
-#pragma unroll
-  for (int m = kJoinThreads / 2; m >= 64; m >>= 1) {
-    __syncthreads();
-    if ((int)threadIdx.x < m) lds[threadIdx.x] += lds[threadIdx.x + m];
-  }
-  if (g == 0 && b < nb) out[(size_t)h * nb + b] = (T)lds[b];
 }
 
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
 hipError_t launch(const AttnArgs& a) {
   using S = DqShape<T, KS, HG, NKV, QW, KW>;
-  const int tiles = a.d.n_nodes / (kTile * QW) + a.d.n_segments;
-  hipError_t e = launch_lds(k_attn_dq<T, KS, HG, NKV, QW, KW>, dim3(tiles, a.d.n_heads / HG), S::kThreads,
-                            S::lds_bytes(a.d.n_buckets, a.gbias != nullptr), a.stream, a);
-  if (e != hipSuccess || !a.gbias) return e;
-  hipLaunchKernelGGL(k_attn_join_bias<T>, dim3(a.d.n_heads), dim3(kJoinThreads), 0, a.stream, a.part, tiles,
-                     a.d.n_buckets, static_cast<T*>(a.gbias));
-  return hipGetLastError();
+  const dim3 grid((unsigned)(a.d.n_nodes / (kTile * QW) + a.d.n_segments), (unsigned)(a.d.n_heads / HG));
+  return launch_lds(k_attn_dq<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a.stream, a);
 }
 
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a) {
   constexpr int pair = Tile<T, KS>::kElems * 4 * NKV;
-  constexpr int KW = pair * 4 <= 64 * 1024 ? 4 : 2;
+  constexpr int KW = pair * 4 <= 96 * 1024 ? 4 : 2;
   const int64_t tiles = ((int64_t)a.d.n_nodes / kTile + a.d.n_segments) * (a.d.n_heads / HG);
   const int64_t mean = a.d.n_nodes / std::max(1, a.d.n_segments);
-  if constexpr (pair <= 64 * 1024) {
-    if (mean > 64 && tiles >= 4096) return launch<T, KS, HG, NKV, 4, 1>(a);
-    if (mean > 64 && DqShape<T, KS, HG, NKV, 1, KW>::lds_bytes(a.d.n_buckets, a.gbias != nullptr) <= kLdsMax)
-      return launch<T, KS, HG, NKV, 1, KW>(a);
-  }
+  if (mean > 64 && tiles >= 4096) return launch<T, KS, HG, NKV, 4, 1>(a);
+  if (mean > 64) return launch<T, KS, HG, NKV, 1, KW>(a);
   return launch<T, KS, HG, NKV, 1, 1>(a);
 }
 
@@ -242,10 +202,8 @@ hipError_t by_heads(const AttnArgs& a) {
   constexpr bool pairs = kPlanes<T> * KS <= 4;      // operands of two heads fit the registers
   const int rep = a.d.n_heads / a.d.n_kv_heads;
   if constexpr (pairs) {
-    if (!a.gbias || a.d.n_buckets <= 32) {          // and their gradient columns LDS
-      if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a);
-      if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a);
-    }
+    if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a);
+    if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a);
   }
   return by_waves<T, KS, 1, 1>(a);
 }
@@ -261,27 +219,8 @@ hipError_t by_width(const AttnArgs& a) {
   return by_heads<T, 8>(a);
 }
 
-// grad_bias of a batch without nodes
-template <typename T>
-hipError_t zero_bias(const AttnArgs& a) {
-  hipLaunchKernelGGL(k_attn_join_bias<T>, dim3(a.d.n_heads), dim3(kJoinThreads), 0, a.stream, a.part, 0, a.d.n_buckets,
-                     static_cast<T*>(a.gbias));
-  return hipGetLastError();
-}
-
 }  // namespace
 
-hipError_t attn_backward_q(const AttnArgs& a) {
-  if (a.d.n_nodes == 0) {
-    if (!a.gbias) return hipSuccess;
-    return a.d.dtype == TP_F32 ? zero_bias<float>(a) : zero_bias<bf16_t>(a);
-  }
-  return a.d.dtype == TP_F32 ? by_width<float>(a) : by_width<bf16_t>(a);
-}
-
-size_t attn_delta_floats(const tp_attn& d) { return ((size_t)d.n_heads * d.n_nodes + 3) / 4 * 4; }
-size_t attn_part_floats(const tp_attn& d) {
-  return ((size_t)d.n_nodes / kTile + d.n_segments) * d.n_heads * d.n_buckets;
-}
+hipError_t attn_backward_q(const AttnArgs& a) { return a.d.dtype == TP_F32 ? by_width<float>(a) : by_width<bf16_t>(a); }
 
 }  // namespace tpc

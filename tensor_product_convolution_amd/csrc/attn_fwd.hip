@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
     const uint32_t vm = __builtin_amdgcn_readfirstlane(valid[4 * kw]);
     if (vm == 0) continue;
     int off[16];
-    tile_offsets<HG>(bk, biased, pos, NP, 32 * kw, half, x, y, z, vm, off);
+    tile_offsets<HG>(bk, biased, pos, NP, 32 * kw, half, x, y, z, off);
+    if (vm != 0xffffffffu) mask_offsets<HG>(bk, vm, half, off);
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
       const uint16_t* kt = tiles + (size_t)((kw * NKV + (NKV == 1 ? 0 : hh)) * 2) * G::kElems;
