@@ -702,7 +702,7 @@ typedef struct {
   int32_t n_buckets;        /* 1..64 */
   int32_t steps;            /* 1, 2, 4 or 8 */
   float r_min;              /* > 0 */
-  float scale;
+  float scale;              /* 0, or 1e-8 to 1e8 in size */
 } tp_attn;
 
 /* Forward.  q, out [n_nodes] rows of n_heads x head_dim, k, v of n_kv_heads x

@@ -106,6 +106,7 @@ struct Raw<bf16_t> {
   u4 v;
   __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const u4*>(p); }
   __device__ __forceinline__ void keep(bool k) { v = k ? v : u4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void negate() { v ^= 0x80008000u; }
   __device__ __forceinline__ void frag(Frag<1>& f) const { f.p[0] = __builtin_bit_cast(b8, v); }
   __device__ __forceinline__ float at(int j) const { return (float)__builtin_bit_cast(b8, v)[j]; }
 };
@@ -119,6 +120,10 @@ struct Raw<float> {
   __device__ __forceinline__ void keep(bool k) {
     a = k ? a : f4{0.f, 0.f, 0.f, 0.f};
     b = k ? b : f4{0.f, 0.f, 0.f, 0.f};
+  }
+  __device__ __forceinline__ void negate() {
+    a = -a;
+    b = -b;
   }
   __device__ __forceinline__ void frag(Frag<3>& f) const {
     const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
@@ -208,7 +213,20 @@ __device__ __forceinline__ bool find_tile(const tp_attn& d, int rows, int t, int
   return q >= lo && q < hi;
 }
 
-// LDS bias table of HG heads, [entry][HG][32], base-2 units; 32 copies of every value,
+// Scores are formed as c S with S = sign q k + bias / |scale|, c = |scale| log2 e (base-2
+// units): the bias starts the accumulator of the product and costs no instruction,
+// and the running maximum is taken on S.  scale 0: sign 0, c = log2 e.
+struct Scale {
+  float sign, c, inv;
+  __device__ __forceinline__ explicit Scale(float scale) {
+    const float a = scale != 0.f ? fabsf(scale) : 1.f;
+    sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+    c = a * kLog2e;
+    inv = 1.f / a;
+  }
+};
+
+// LDS bias table of HG heads, [entry][HG][32], in units of S; 32 copies of every value,
 // so that the lanes of a half wave, each with a bucket of its own, read 32 different
 // banks.  The entry after the last bucket masks.
 __device__ __forceinline__ float bias_at(const tp_attn& d, int h, int b) {
@@ -216,140 +234,225 @@ __device__ __forceinline__ float bias_at(const tp_attn& d, int h, int b) {
   return d.dtype == TP_F32 ? static_cast<const float*>(d.bias)[i] : (float)static_cast<const bf16_t*>(d.bias)[i];
 }
 template <int HG>
-__device__ __forceinline__ void fill_table(const tp_attn& d, int h0, float* tbl, int threads) {
+__device__ __forceinline__ void fill_table(const tp_attn& d, float inv, int h0, float* tbl, int threads) {
   const int ne = d.n_buckets > 0 ? d.n_buckets : 1;
-  for (int i = threadIdx.x; i < (ne + 1) * HG * 32; i += threads) {
-    const int hh = (i >> 5) % HG, b = (i >> 5) / HG;
-    tbl[i] = b == ne ? -INFINITY : d.n_buckets > 0 ? bias_at(d, h0 + hh, b) * kLog2e : 0.f;
+  for (int i = threadIdx.x; i < (ne + 1) * HG * 8; i += threads) {
+    const int hh = (i >> 3) % HG, b = (i >> 3) / HG;
+    const float v = b == ne ? -INFINITY : d.n_buckets > 0 ? bias_at(d, h0 + hh, b) * inv : 0.f;
+    reinterpret_cast<f4*>(tbl)[i] = f4{v, v, v, v};
   }
 }
 
-// bucket -> byte offset of this lane's copy in the table
+typedef __attribute__((address_space(3))) float lds_f;
+__device__ __forceinline__ uint32_t lds_address(const float* p) { return (uint32_t)(uintptr_t)(lds_f*)p; }
+__device__ __forceinline__ lds_f* lds_at(uint32_t address) { return (lds_f*)(uintptr_t)address; }
+
+// bucket -> LDS address of this lane's copy in the table
 template <int HG>
 struct Buckets {
-  int shift, lo, hi, add, first, masked;   // first: the only entry where there is no bias
-  __device__ __forceinline__ explicit Buckets(const tp_attn& d, int lane) {
+  static constexpr int kEntry = HG * 128;
+  int shift;
+  float lo, hi;
+  uint32_t add, first, masked;             // first: the only entry where there is no bias
+  __device__ __forceinline__ Buckets(const tp_attn& d, const float* tbl, int lane) {
     int lg = 0;
     while ((1 << lg) < d.steps) ++lg;
     shift = 23 - lg;
     const int base = (int)(bits(d.r_min * d.r_min) >> shift), nb = d.n_buckets > 0 ? d.n_buckets : 1;
-    lo = base << shift;
-    hi = ((base + nb) << shift) - 1;
-    first = (lane & 31) * 4;
-    add = first - base * HG * 128;
-    masked = first + nb * HG * 128;
+    lo = flt((uint32_t)base << shift);
+    hi = flt(((uint32_t)(base + nb) << shift) - 1);
+    first = lds_address(tbl) + (lane & 31) * 4;
+    add = first - base * kEntry;
+    masked = first + nb * kEntry;
   }
-  // the squared distance, every operation rounded once (no fused multiply-add)
-  __device__ __forceinline__ int offset(float ax, float ay, float az, float bx, float by, float bz) const {
+  // the squared distance, every operation rounded once (no fused multiply-add).  It is
+  // clamped as a float: positive floats are ordered as their representations.
+  __device__ __forceinline__ uint32_t address(float ax, float ay, float az, float bx, float by, float bz) const {
 #pragma clang fp contract(off)
     const float dx = ax - bx, dy = ay - by, dz = az - bz;
     const float xx = dx * dx, yy = dy * dy, zz = dz * dz;
     const float d2 = (xx + yy) + zz;
-    const int c = min(max((int)bits(d2), lo), hi);
-    return (c >> shift) * (HG * 128) + add;
+    return (bits(__builtin_amdgcn_fmed3f(d2, lo, hi)) >> shift) * kEntry + add;
   }
 };
 
-__device__ __forceinline__ float table(const float* tbl, int off, int hh) {
-  return *reinterpret_cast<const float*>(reinterpret_cast<const char*>(tbl) + off + hh * 128);
-}
-
-// table offsets of the 16 tile rows that a lane holds: bucket of (own position, row's
-// position).  pos: LDS [3][np], the tile's rows from `at`.
+// table addresses of the 16 tile rows that a lane holds: bucket of (own position, row's
+// position).  pos: LDS [3][32].
 template <int HG>
-__device__ __forceinline__ void tile_offsets(const Buckets<HG>& bk, bool biased, const float* pos, int np, int at, int half,
-                                             float x, float y, float z, int off[16]) {
+__device__ __forceinline__ void tile_entries(const Buckets<HG>& bk, bool biased, const float* pos, int half, float x,
+                                             float y, float z, uint32_t ent[16]) {
   if (biased) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const int r = at + 8 * g + 4 * half;
-      const f4 px = *reinterpret_cast<const f4*>(pos + r), py = *reinterpret_cast<const f4*>(pos + np + r),
-               pz = *reinterpret_cast<const f4*>(pos + 2 * np + r);
+      const int r = 8 * g + 4 * half;
+      const f4 px = *reinterpret_cast<const f4*>(pos + r), py = *reinterpret_cast<const f4*>(pos + kTile + r),
+               pz = *reinterpret_cast<const f4*>(pos + 2 * kTile + r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) off[4 * g + j] = bk.offset(x, y, z, px[j], py[j], pz[j]);
+      for (int j = 0; j < 4; ++j) ent[4 * g + j] = bk.address(x, y, z, px[j], py[j], pz[j]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) off[i] = bk.first;
+    for (int i = 0; i < 16; ++i) ent[i] = bk.first;
   }
 }
 // tile rows that do not count (bit r of valid clear) to the masking entry
 template <int HG>
-__device__ __forceinline__ void mask_offsets(const Buckets<HG>& bk, uint32_t valid, int half, int off[16]) {
+__device__ __forceinline__ void mask_entries(const Buckets<HG>& bk, uint32_t valid, int half, uint32_t ent[16]) {
   const uint32_t m = valid >> (4 * half);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) off[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? off[i] : bk.masked;
+  for (int i = 0; i < 16; ++i) ent[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? ent[i] : bk.masked;
 }
 
-// Staging of W tiles of 32 rows side by side (rows r0 + 32 w ..), NS head slots of two
-// arrays each (tile number (w NS + slot) 2 + array): every thread fetches its
-// 8-value chunks into registers while the previous step computes, then puts
-// them into LDS.  Rows past the end or masked are staged as zeros.
-template <typename T, int KS, int NT, int W, int NS>
+// S of a tile: the bias of every pair, then the product of the staged tile's rows with
+// the wave's own rows
+template <typename T, int KS>
+__device__ __forceinline__ f16v scores(const uint16_t* tile, const Frag<kPlanes<T>> own[KS], const uint32_t ent[16], int hh,
+                                       int lane) {
+  f16v s;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = lds_at(ent[i])[hh * 32];
+#pragma unroll
+  for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<T, KS>(tile, kk, lane), own[kk], s);
+  return s;
+}
+
+// Staging of a tile of 32 rows, NS head slots of two arrays each (tile number 2 slot +
+// array), by the NT threads that share it: every thread fetches its 8-value chunks
+// into registers while an earlier tile is worked on, then puts them into LDS.  Rows
+// past the end or masked are staged as zeros.
+template <typename T, int KS, int NT, int NS>
 struct Stager {
   using G = Tile<T, KS>;
-  static constexpr int kTiles = W * NS * 2;
+  static constexpr int kTiles = NS * 2;
   static constexpr int kChunks = (kTiles * kTile * 2 * KS + NT - 1) / NT;
   static constexpr int kBytes = kTiles * G::kElems * 2;
   Raw<T> raw[kChunks];
   bool live[kChunks];
+  const T* at[kChunks];                    // this thread's chunk of the next tile, not read past the end
+  int64_t step0, step1;
+  int tid;
 
+  __device__ __forceinline__ int chunk(int i) const { return tid + i * NT; }
+  static __device__ __forceinline__ int col_of(int c) { return c % (2 * KS); }
+  static __device__ __forceinline__ int row_of(int c) { return c / (2 * KS) % kTile; }
+  static __device__ __forceinline__ int tile_of(int c) { return c / (2 * KS * kTile); }
+
+  // the tile of rows r0 .. is next, then every `stride` rows; head(slot): the head of a slot
   template <typename Head>
-  __device__ __forceinline__ void fetch(const void* p0, int64_t s0, const void* p1, int64_t s1, int r0, int end, int D,
-                                        const uint8_t* mask, Head&& head) {
+  __device__ __forceinline__ void aim(int thread, const void* p0, int64_t s0, const void* p1, int64_t s1, int r0,
+                                      int stride, int D, Head&& head) {
+    tid = thread;
+    step0 = s0 * stride;
+    step1 = s1 * stride;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const int c = threadIdx.x + i * NT, col = c % (2 * KS), row = c / (2 * KS) % kTile, t = c / (2 * KS * kTile);
-      const int r = r0 + 32 * ((t >> 1) / NS) + row;
-      live[i] = t < kTiles && r < end && 8 * col < D;
+      const int c = chunk(i), t = tile_of(c);
+      const int64_t r = r0 + row_of(c);
+      at[i] = (t & 1 ? static_cast<const T*>(p1) + r * s1 : static_cast<const T*>(p0) + r * s0) +
+              head((t >> 1) % NS) * D + 8 * col_of(c);
+    }
+  }
+  // loads the tile that aim (or the previous fetch) has come to, rows r0 ..
+  __device__ __forceinline__ void fetch(int r0, int end, int D, const uint8_t* mask) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = chunk(i), t = tile_of(c), r = r0 + row_of(c);
+      live[i] = t < kTiles && r < end && 8 * col_of(c) < D;
       if (live[i]) {
-        const T* p = t & 1 ? static_cast<const T*>(p1) + (size_t)r * s1 : static_cast<const T*>(p0) + (size_t)r * s0;
-        raw[i].load(p + (size_t)head((t >> 1) % NS) * D + 8 * col);
+        raw[i].load(at[i]);
         if (mask) live[i] = mask[r] != 0;
       }
+      at[i] += t & 1 ? step1 : step0;
     }
   }
   __device__ __forceinline__ void stage(uint16_t* tiles) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const int c = threadIdx.x + i * NT, col = c % (2 * KS), row = c / (2 * KS) % kTile, t = c / (2 * KS * kTile);
+      const int c = chunk(i);
       raw[i].keep(live[i]);
-      if (t < kTiles) put<T, KS>(tiles + t * G::kElems, row, col, raw[i]);
+      if (tile_of(c) < kTiles) put<T, KS>(tiles + tile_of(c) * G::kElems, row_of(c), col_of(c), raw[i]);
     }
   }
 };
 
-// positions of NP rows, one per thread of the first NP
-template <int NP>
-struct PosStager {
+// positions and validity of a tile's rows, one per thread of the first 32 that share it.
+// LDS: [3][32] positions and the validity bits.
+struct RowStager {
+  static constexpr int kBytes = 3 * kTile * 4 + 16;
   float x = 0.f, y = 0.f, z = 0.f;
-  __device__ __forceinline__ void fetch(const float* pos, int r0, int end) {
-    if ((int)threadIdx.x < NP) {
-      const int r = min(r0 + (int)threadIdx.x, end - 1);
-      x = pos[3 * (size_t)r];
-      y = pos[3 * (size_t)r + 1];
-      z = pos[3 * (size_t)r + 2];
+  bool live = false;
+  __device__ __forceinline__ void fetch(int tid, const tp_attn& d, bool biased, int r0, int end, const uint8_t* mask) {
+    if (tid < kTile) {
+      const int r = r0 + tid, rc = r < end ? r : end - 1;
+      live = r < end && (!mask || mask[rc] != 0);
+      if (biased) {
+        x = d.pos[3 * (size_t)rc];
+        y = d.pos[3 * (size_t)rc + 1];
+        z = d.pos[3 * (size_t)rc + 2];
+      }
     }
   }
-  __device__ __forceinline__ void stage(float* lds) const {
-    if ((int)threadIdx.x < NP) {
-      lds[threadIdx.x] = x;
-      lds[NP + threadIdx.x] = y;
-      lds[2 * NP + threadIdx.x] = z;
+  __device__ __forceinline__ void stage(int tid, float* lds) const {
+    const uint32_t bits_ = (uint32_t)__ballot(live);
+    if (tid < kTile) {
+      lds[tid] = x;
+      lds[kTile + tid] = y;
+      lds[2 * kTile + tid] = z;
     }
+    if (tid == 0) *reinterpret_cast<uint32_t*>(lds + 3 * kTile) = bits_;
+  }
+  static __device__ __forceinline__ uint32_t valid(const float* lds) {
+    return __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(lds + 3 * kTile));
   }
 };
 
-// the wave's own rows as B operands: row `r`, contraction elements 16 kk + 8 half ..
+// Walks the tiles of one group of waves: prepare(i) starts tile i's loads into registers,
+// stage(i, buffer) puts them into LDS, work(i, buffer) uses them.  A tile that several
+// waves share is staged one tile ahead into the other of two buffers, with one barrier
+// a tile, or, where LDS holds one buffer only, between two barriers.  A wave on its own
+// needs no barrier and one buffer (its LDS accesses are executed in order).  All groups
+// of the workgroup take the same n.
+template <bool SHARED, int BUFS, typename Prepare, typename Stage, typename Work>
+__device__ __forceinline__ void walk(int n, Prepare&& prepare, Stage&& stage, Work&& work) {
+  prepare(0);
+  if (SHARED && BUFS == 2) {
+    stage(0);
+    if (n > 1) prepare(1);
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+      if (i + 1 < n) stage((i + 1) & 1);
+      if (i + 2 < n) prepare(i + 2);
+      work(i & 1);
+      __syncthreads();
+    }
+  } else {
+    for (int i = 0; i < n; ++i) {
+      if (SHARED) __syncthreads();
+      else __builtin_amdgcn_wave_barrier();
+      stage(0);
+      if (SHARED) __syncthreads();
+      else __builtin_amdgcn_wave_barrier();
+      if (i + 1 < n) prepare(i + 1);
+      work(0);
+    }
+  }
+}
+// buffers of a tile that `share` waves share, `groups` of them side by side: LDS for two
+// workgroups a CU beside their tables
+constexpr int buffers(int bytes, int share, int groups) { return share > 1 && 2 * groups * bytes <= 60 * 1024 ? 2 : 1; }
+
+// the wave's own rows as B operands, times sign (1, -1 or 0: exact): row `r`,
+// contraction elements 16 kk + 8 half ..
 template <typename T, int KS>
 __device__ __forceinline__ void own_rows(const void* p, int64_t stride, int r, int head, int D, int half, bool keep,
-                                         Frag<kPlanes<T>> f[KS]) {
+                                         float sign, Frag<kPlanes<T>> f[KS]) {
 #pragma unroll
   for (int kk = 0; kk < KS; ++kk) {
     const int c = 16 * kk + 8 * half;
     Raw<T> w;
     w.load(static_cast<const T*>(p) + (size_t)r * stride + (size_t)head * D + (c < D ? c : 0));
-    w.keep(keep && c < D);
+    w.keep(keep && c < D && sign != 0.f);
+    if (sign < 0.f) w.negate();
     w.frag(f[kk]);
   }
 }
@@ -398,6 +501,13 @@ __device__ __forceinline__ void clear(f16v acc[MT]) {
 }
 
 constexpr size_t kLdsMax = 160 * 1024;
+
+// How many waves a call can use: 32-row tiles times heads, the mean length of a structure.
+struct Extent {
+  int64_t units, mean;
+  Extent(const tp_attn& d, int heads)
+      : units(((int64_t)d.n_nodes / kTile + d.n_segments) * heads), mean(d.n_nodes / (d.n_segments > 0 ? d.n_segments : 1)) {}
+};
 
 // a kernel that may use all of a CU's LDS, launched with `bytes` of it
 template <typename K, typename... A>

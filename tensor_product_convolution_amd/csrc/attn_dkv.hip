@@ -3,53 +3,53 @@
 //   grad_v = p^T grad_out,  grad_k = scale ds^T q,  summed over the query heads of a
 //   key head;  grad_bias[bucket] += ds;  p = exp(s - lse), ds = p (grad_out v^T - delta)
 //
-// A wave owns 32 keys of NKV key heads and walks the queries in tiles, HG query heads
-// at a time (HG heads of one key head, or HG key heads with one query head each).
-// KV x QS waves: KV own 32 keys each, QS split the queries and are joined through
-// LDS at the end.
+// A wave owns 32 keys of one key head and walks the queries in tiles, one query head
+// after another.  KV x QS waves: KV own 32 keys each and share staged queries, QS
+// split the queries and are joined through LDS at the end.  Where key heads are
+// shared and there are too few key tiles to fill the chip, every query head gets
+// workgroups of its own, whose float32 parts a second kernel adds up.
 //
 // The bias gradient goes into LDS columns private to the lane (no two lanes add to
-// one word, so the order of the sums is fixed), summed per workgroup and joined by
-// a second kernel.
+// one word, so plain reads and writes do and the order of the sums is fixed), two
+// elements at a time, summed per workgroup and joined by a second kernel.  An LDS
+// float atomic takes 190 cycles a wave on gfx950; a read, an addition and a write of
+// a pair take 150 cycles of latency that other waves fill.
 #include "attn.hpp"
-
-#include <algorithm>
 
 namespace tpc {
 namespace {
 
-template <typename T, int KS, int HG, int NKV, int KV, int QS>
+template <typename T, int KS, int KV, int QS>
 struct DkvShape {
   using G = Tile<T, KS>;
-  static constexpr int kThreads = 64 * KV * QS, kRows = kTile * QS;
-  using Stage = Stager<T, KS, kThreads, QS, HG>;
-  static constexpr int kPart = G::MT * 16 * 64 * 2;
-  static constexpr int kJoin = KV * (QS - 1) * NKV * kPart * 4;
-  static constexpr int kTileBytes = Stage::kBytes > kJoin ? Stage::kBytes : kJoin;
+  static constexpr int kThreads = 64 * KV * QS;
+  using Stage = Stager<T, KS, 64 * KV, 1>;
+  static constexpr int kBuf = Stage::kBytes + RowStager::kBytes + 2 * kTile * 4, kBufs = buffers(kBuf, KV, QS);
+  static constexpr int kPart = 2 * G::MT * 16 * 64;                  // floats of one wave to join
+  static constexpr int kJoin = KV * (QS - 1) * kPart * 4;
+  static constexpr int kWork = kBuf * kBufs * QS > kJoin ? kBuf * kBufs * QS : kJoin;
   static size_t lds_bytes(int nb, bool grad) {
     const size_t entries = (nb > 0 ? nb : 1) + 1;
-    return (size_t)kTileBytes + 12 * kRows + 8 * HG * kRows + entries * HG * 128 +
-           (grad ? (size_t)KV * QS * entries * HG * 256 : 0);
+    return kWork + entries * 128 + (grad ? KV * QS * entries * 256 : 0);
   }
-  static constexpr int kRegs = NKV * (2 * KS * G::P * 4 + 2 * G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 4 : 8);
+  static constexpr int kRegs = 2 * KS * G::P * 4 + 2 * G::MT * 16 + 90 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
-template <typename T, int KS, int HG, int NKV, int KV, int QS>
-__global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, HG, NKV, KV, QS>::kRegs > 220 ? 1 : 2))
+template <typename T, int KS, int KV, int QS>
+__global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs > 220 ? 1 : 2))
     k_attn_dkv(AttnArgs a) {
-  using S = DkvShape<T, KS, HG, NKV, KV, QS>;
+  using S = DkvShape<T, KS, KV, QS>;
   using G = Tile<T, KS>;
-  constexpr int P = G::P, MT = G::MT, NP = S::kRows, NW = KV * QS;
+  constexpr int P = G::P, MT = G::MT, NW = KV * QS;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  uint16_t* tiles = reinterpret_cast<uint16_t*>(lds);
-  float* pos = reinterpret_cast<float*>(lds + S::kTileBytes);       // [3][NP]
-  float* stat = pos + 3 * NP;                                       // [HG][2][NP]: lse (base 2), delta
-  float* tbl = stat + 2 * HG * NP;
+  float* tbl = reinterpret_cast<float*>(lds + S::kWork);
   const tp_attn& d = a.d;
   const int nb = d.n_buckets, ne = (nb > 0 ? nb : 1) + 1;
-  float* cols = tbl + ne * HG * 32;        // [NW][ne][HG][64] bias gradient columns
-  const int g0 = blockIdx.y * NKV, rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
-  const int h_lo = g0 * rep, h_hi = (g0 + NKV) * rep;
+  float* cols = tbl + ne * 32;             // [NW][ne][64] bias gradient columns
+  const int rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
+  // query heads h_lo .. h_hi - 1 of key head g
+  const int g = a.split ? blockIdx.y / rep : blockIdx.y;
+  const int h_lo = a.split ? blockIdx.y : g * rep, h_hi = a.split ? h_lo + 1 : h_lo + rep;
   int lo, hi, k0;
   if (!find_tile(d, kTile * KV, blockIdx.x, lo, hi, k0)) {
     if (a.gbias)
@@ -60,159 +60,171 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, HG, NKV, KV, QS
   const int lane = threadIdx.x & 63, half = lane >> 5, wv = threadIdx.x >> 6;
   const int qs = wv % QS, kv = wv / QS;
   const bool biased = nb > 0;
-  const Buckets<HG> bk(d, lane);
+  const Buckets<1> bk(d, tbl, lane);
+  const Scale scale(d.scale);
 
   // this lane's key; a masked one is held as zeros and gets zero gradients
   const int k = k0 + 32 * kv + (lane & 31), kc = k < hi ? k : hi - 1;
   const bool live = k < hi && (!d.key_mask || d.key_mask[kc] != 0);
   const bool some_dead = __any(!live);
-  // table offset -> byte offset of the lane's column of the same entry (twice as wide)
-  char* mycol = reinterpret_cast<char*>(cols + (size_t)wv * ne * HG * 64) + 4 * lane - 8 * (lane & 31);
+  // table address -> address of the lane's column of the same entry (twice as wide)
+  float* my_cols = cols + (size_t)wv * ne * 64;
+  const uint32_t col = lds_address(my_cols) + 4 * lane - 2 * bk.first;
   float x = 0.f, y = 0.f, z = 0.f;
   if (biased) {
     x = d.pos[3 * (size_t)kc];
     y = d.pos[3 * (size_t)kc + 1];
     z = d.pos[3 * (size_t)kc + 2];
   }
-  Frag<P> K[NKV][KS], V[NKV][KS];
-  f16v dK[NKV][MT], dV[NKV][MT];
-#pragma unroll
-  for (int s = 0; s < NKV; ++s) {
-    own_rows<T, KS>(a.k, a.ks, kc, g0 + s, D, half, live, K[s]);
-    own_rows<T, KS>(a.v, a.vs, kc, g0 + s, D, half, live, V[s]);
-    clear<MT>(dK[s]);
-    clear<MT>(dV[s]);
-  }
-  const float c = d.scale * kLog2e;
+  Frag<P> K[KS], V[KS];
+  own_rows<T, KS>(a.k, a.ks, kc, g, D, half, live, scale.sign, K);
+  own_rows<T, KS>(a.v, a.vs, kc, g, D, half, live, 1.f, V);
+  f16v dK[MT], dV[MT];
+  clear<MT>(dK);
+  clear<MT>(dV);
 
-  // steps: query heads of the key head, HG at a time, outside; query tiles inside
   typename S::Stage st;
-  PosStager<NP> ps;
-  float slse[HG], sdel[HG];
-  auto fetch = [&](int h0, int q0) {
-    st.fetch(a.q, a.qs, a.go, a.gos, q0, hi, D, nullptr, [&](int slot) { return h0 + slot; });
-    if (biased) ps.fetch(d.pos, q0, hi);
-    if ((int)threadIdx.x < NP) {
-      const int q = q0 + threadIdx.x;
-#pragma unroll
-      for (int hh = 0; hh < HG; ++hh) {
-        const size_t at = (size_t)(h0 + hh) * d.n_nodes + min(q, hi - 1);
-        const float e = a.lse_in[at];
-        slse[hh] = q < hi && e != -INFINITY ? e * kLog2e : INFINITY;
-        sdel[hh] = q < hi ? a.delta[at] : 0.f;
-      }
-    }
-  };
-  fetch(h_lo, lo);
-  for (int h0 = h_lo; h0 < h_hi; h0 += HG) {
-    __syncthreads();
-    fill_table<HG>(d, h0, tbl, S::kThreads);
+  RowStager rows;
+  float slse = INFINITY, sdel = 0.f;
+  const int tid = kv * 64 + lane;          // among the threads that share a tile
+  char* mine = lds + qs * S::kBufs * S::kBuf;
+  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
+  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
+  const auto stat_of = [&](int buf) { return rows_of(buf) + RowStager::kBytes / 4; };   // [2][32]: lse (base 2), delta
+  const int q_first = lo + 32 * qs, n = (hi - lo + 32 * QS - 1) / (32 * QS);
+  for (int h = h_lo; h < h_hi; ++h) {
+    if (h > h_lo) __syncthreads();         // the previous head's table and columns have been read
+    fill_table<1>(d, scale.inv, h, tbl, S::kThreads);
     if (a.gbias)
-      for (int i = threadIdx.x; i < NW * ne * HG * 64; i += S::kThreads) cols[i] = 0.f;
-    for (int q0 = lo; q0 < hi; q0 += NP) {
-      __syncthreads();
-      st.stage(tiles);
-      ps.stage(pos);
-      if ((int)threadIdx.x < NP) {
+      for (int i = lane; i < ne * 16; i += 64) reinterpret_cast<f4*>(my_cols)[i] = f4{0.f, 0.f, 0.f, 0.f};
+    st.aim(tid, a.q, a.qs, a.go, a.gos, q_first, 32 * QS, D, [&](int) { return h; });
+    const auto prepare = [&](int i) {
+      const int q0 = q_first + i * 32 * QS;
+      st.fetch(q0, hi, D, nullptr);
+      rows.fetch(tid, d, biased, q0, hi, nullptr);
+      if (tid < kTile) {
+        const size_t at = (size_t)h * d.n_nodes + min(q0 + tid, hi - 1);
+        const float e = a.lse_in[at];
+        // rows past the end or without keys: p = exp2(s - inf) = 0
+        slse = q0 + tid < hi && e != -INFINITY ? e * kLog2e : INFINITY;
+        sdel = q0 + tid < hi ? a.delta[at] : 0.f;
+      }
+    };
+    const auto stage = [&](int buf) {
+      st.stage(tiles_of(buf));
+      rows.stage(tid, rows_of(buf));
+      if (tid < kTile) {
+        stat_of(buf)[tid] = slse;
+        stat_of(buf)[kTile + tid] = sdel;
+      }
+    };
+    __syncthreads();                       // the table
+    walk<(KV > 1), S::kBufs>(n, prepare, stage, [&](int buf) {
+      if (RowStager::valid(rows_of(buf)) == 0) return;   // past the end
+      uint32_t ent[16];
+      tile_entries<1>(bk, biased, rows_of(buf), half, x, y, z, ent);
+      if (some_dead) mask_entries<1>(bk, live ? 0xffffffffu : 0u, half, ent);
+      const uint16_t* qt = tiles_of(buf);
+      const f16v s = scores<T, KS>(qt, K, ent, 0, lane);
+      f16v dp;
+      clear<1>(&dp);
 #pragma unroll
-        for (int hh = 0; hh < HG; ++hh) {
-          stat[(2 * hh) * NP + threadIdx.x] = slse[hh];
-          stat[(2 * hh + 1) * NP + threadIdx.x] = sdel[hh];
+      for (int kk = 0; kk < KS; ++kk) dp = mma(row_frag<T, KS>(qt + G::kElems, kk, lane), V[kk], dp);
+      float p[16], ds[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 8 * j + 4 * half;
+        const f4 le = *reinterpret_cast<const f4*>(stat_of(buf) + r);
+        const f4 de = *reinterpret_cast<const f4*>(stat_of(buf) + kTile + r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], scale.c, -le[e]));
+          ds[4 * j + e] = p[4 * j + e] * (dp[4 * j + e] - de[e]);
         }
       }
-      __syncthreads();
-      if (hi - q0 > NP) fetch(h0, q0 + NP);
-      else if (h0 + HG < h_hi) fetch(h0 + HG, lo);
-      if (32 * qs >= hi - q0) continue;
-      int off[16];
-      tile_offsets<HG>(bk, biased, pos, NP, 32 * qs, half, x, y, z, off);
-      if (some_dead) mask_offsets<HG>(bk, live ? 0xffffffffu : 0u, half, off);
+      if (a.gbias) {
 #pragma unroll
-      for (int hh = 0; hh < HG; ++hh) {
-        const int s_ = NKV == 1 ? 0 : hh;
-        const uint16_t* qt = tiles + (size_t)((qs * HG + hh) * 2) * G::kElems;
-        f16v s, dp;
-        clear<1>(&s);
-        clear<1>(&dp);
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<T, KS>(qt, kk, lane), K[s_][kk], s);
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) dp = mma(row_frag<T, KS>(qt + G::kElems, kk, lane), V[s_][kk], dp);
-        float p[16], ds[16];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int r = 32 * qs + 8 * g + 4 * half;
-          const f4 le = *reinterpret_cast<const f4*>(stat + (2 * hh) * NP + r);
-          const f4 de = *reinterpret_cast<const f4*>(stat + (2 * hh + 1) * NP + r);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = 4 * g + j;
-            p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, table(tbl, off[i], hh)) - le[j]);
-            ds[i] = p[i] * (dp[i] - de[j]);
-          }
-        }
-        if (a.gbias) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            __hip_atomic_fetch_add(reinterpret_cast<float*>(mycol + 2 * off[i] + hh * 256), ds[i], __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_WORKGROUP);
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          Frag<P> pf, df;
-          to_frag(p + 8 * kb, pf);
-          to_frag(ds + 8 * kb, df);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            dV[s_][mt] = mma(col_frag<T, KS>(qt + G::kElems, mt, kb, lane), pf, dV[s_][mt]);
-            dK[s_][mt] = mma(col_frag<T, KS>(qt, mt, kb, lane), df, dK[s_][mt]);
-          }
+        for (int e = 0; e < 16; e += 2) {
+          lds_f *u = lds_at(2 * ent[e] + col), *v = lds_at(2 * ent[e + 1] + col);
+          const float x0 = *u, x1 = *v, y0 = x0 + ds[e], y1 = (ent[e] == ent[e + 1] ? y0 : x1) + ds[e + 1];
+          *u = y0;
+          *v = y1;                         // the later of two sums into one word stands
         }
       }
-    }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        Frag<P> pf, df;
+        to_frag(p + 8 * kb, pf);
+        to_frag(ds + 8 * kb, df);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          dV[mt] = mma(col_frag<T, KS>(qt + G::kElems, mt, kb, lane), pf, dV[mt]);
+          dK[mt] = mma(col_frag<T, KS>(qt, mt, kb, lane), df, dK[mt]);
+        }
+      }
+    });
     if (a.gbias) {
-      // an entry's 64 columns of every wave; lanes start at different columns so that
-      // they read different banks
+      // an entry's 64 columns of every wave, 16 bytes at a time; lanes start at different
+      // columns so that they read different banks
       __syncthreads();
-      for (int i = threadIdx.x; i < nb * HG; i += S::kThreads) {
-        const int b = i / HG, hh = i % HG;
+      for (int b = threadIdx.x; b < nb; b += S::kThreads) {
         float s = 0.f;
-        for (int w = 0; w < NW; ++w)
-#pragma unroll 8
-          for (int j = 0; j < 64; ++j) s += cols[((size_t)(w * ne + b) * HG + hh) * 64 + ((j + lane) & 63)];
-        a.part[((size_t)(h0 + hh) * gridDim.x + blockIdx.x) * nb + b] = s;
+        for (int w = 0; w < NW; ++w) {
+          const f4* c4 = reinterpret_cast<const f4*>(cols + (size_t)(w * ne + b) * 64);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const f4 v = c4[(j + lane) & 15];
+            s += (v[0] + v[1]) + (v[2] + v[3]);
+          }
+        }
+        a.part[((size_t)h * gridDim.x + blockIdx.x) * nb + b] = s;
       }
     }
   }
 
   if (QS > 1) {
-    float* join = reinterpret_cast<float*>(lds) + (size_t)kv * (QS - 1) * NKV * S::kPart + lane;
+    float* join = reinterpret_cast<float*>(lds) + (size_t)kv * (QS - 1) * S::kPart + lane;
     __syncthreads();
     if (qs > 0) {
-#pragma unroll
-      for (int s = 0; s < NKV; ++s) {
-        float* w = join + ((qs - 1) * NKV + s) * S::kPart;
-        park<MT>(w, dK[s]);
-        park<MT>(w + S::kPart / 2, dV[s]);
-      }
+      park<MT>(join + (qs - 1) * S::kPart, dK);
+      park<MT>(join + (qs - 1) * S::kPart + S::kPart / 2, dV);
     }
     __syncthreads();
     if (qs > 0) return;
-#pragma unroll
-    for (int s = 0; s < NKV; ++s)
-      for (int o = 0; o < QS - 1; ++o) {
-        const float* w = join + (o * NKV + s) * S::kPart;
-        add_parked<MT>(w, 1.f, 1.f, dK[s]);
-        add_parked<MT>(w + S::kPart / 2, 1.f, 1.f, dV[s]);
-      }
-  }
-  if (k < hi) {
-#pragma unroll
-    for (int s = 0; s < NKV; ++s) {
-      store_rows<T, MT>(a.gk, a.gks, k, g0 + s, D, half, dK[s], d.scale, !live);
-      store_rows<T, MT>(a.gv, a.gvs, k, g0 + s, D, half, dV[s], 1.f, !live);
+    for (int o = 0; o < QS - 1; ++o) {
+      add_parked<MT>(join + o * S::kPart, 1.f, 1.f, dK);
+      add_parked<MT>(join + o * S::kPart + S::kPart / 2, 1.f, 1.f, dV);
     }
   }
+  if (k < hi) {
+    if (a.split) {
+      // [n_nodes][n_heads][2][D]
+      float* o = a.kv_part + ((size_t)k * d.n_heads + h_lo) * 2 * D;
+      store_rows<float, MT>(o, 0, 0, 0, D, half, dK, d.scale, !live);
+      store_rows<float, MT>(o, 0, 0, 1, D, half, dV, 1.f, !live);
+    } else {
+      store_rows<T, MT>(a.gk, a.gks, k, g, D, half, dK, d.scale, !live);
+      store_rows<T, MT>(a.gv, a.gvs, k, g, D, half, dV, 1.f, !live);
+    }
+  }
+}
+
+// grad_k, grad_v [n][g] = sum over the query heads of key head g, in their order
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_attn_join_kv(AttnArgs a) {
+  const int D = a.d.head_dim, rep = a.d.n_heads / a.d.n_kv_heads;
+  const int per = a.d.n_kv_heads * 2 * (D / 4);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t node = i / per;
+  if (node >= a.d.n_nodes) return;
+  const int e = (int)(i % per), c = e % (D / 4), which = e / (D / 4) % 2, g = e / (D / 4) / 2;
+  const float* p = a.kv_part + (((size_t)node * a.d.n_heads + g * rep) * 2 + which) * D + 4 * c;
+  f4 s = *reinterpret_cast<const f4*>(p);
+  for (int r = 1; r < rep; ++r) s += *reinterpret_cast<const f4*>(p + (size_t)r * 2 * D);
+  T* o = which ? static_cast<T*>(a.gv) + (size_t)node * a.gvs : static_cast<T*>(a.gk) + (size_t)node * a.gks;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[(size_t)g * D + 4 * c + j] = (T)s[j];
 }
 
 // grad_bias[h][b] = sum over the tiles' parts, in a fixed order.
@@ -243,63 +255,72 @@ hipError_t join_bias(const AttnArgs& a, int parts) {
   return hipGetLastError();
 }
 
-template <typename T, int KS, int HG, int NKV, int KV, int QS>
+// Query heads apart: where key heads are shared and one workgroup per 32 keys and key
+// head would leave most of the chip idle.
+bool split_heads(const tp_attn& d) {
+  return d.n_heads > d.n_kv_heads && ((int64_t)d.n_nodes / kTile + d.n_segments) * d.n_kv_heads < 512;
+}
+
+template <typename T, int KS, int KV, int QS>
 hipError_t launch(const AttnArgs& a) {
-  using S = DkvShape<T, KS, HG, NKV, KV, QS>;
+  using S = DkvShape<T, KS, KV, QS>;
   const int tiles = a.d.n_nodes / (kTile * KV) + a.d.n_segments;
-  hipError_t e = launch_lds(k_attn_dkv<T, KS, HG, NKV, KV, QS>, dim3(tiles, a.d.n_kv_heads / NKV), S::kThreads,
+  hipError_t e = launch_lds(k_attn_dkv<T, KS, KV, QS>, dim3(tiles, a.split ? a.d.n_heads : a.d.n_kv_heads), S::kThreads,
                             S::lds_bytes(a.d.n_buckets, a.gbias != nullptr), a.stream, a);
-  return e != hipSuccess || !a.gbias ? e : join_bias<T>(a, tiles);
-}
-
-template <typename T, int KS, int HG, int NKV>
-hipError_t by_waves(const AttnArgs& a) {
-  constexpr int pair = Tile<T, KS>::kElems * 4 * HG;
-  constexpr int QS = pair * 4 <= 64 * 1024 ? 4 : 2;
-  const int64_t tiles = ((int64_t)a.d.n_nodes / kTile + a.d.n_segments) * (a.d.n_kv_heads / NKV);
-  const int64_t mean = a.d.n_nodes / std::max(1, a.d.n_segments);
-  const auto fits = [&](size_t bytes) { return bytes <= kLdsMax; };
-  if (mean > 64 && tiles >= 4096 && fits(DkvShape<T, KS, HG, NKV, 4, 1>::lds_bytes(a.d.n_buckets, a.gbias != nullptr)))
-    return launch<T, KS, HG, NKV, 4, 1>(a);
-  if (mean > 64 && fits(DkvShape<T, KS, HG, NKV, 1, QS>::lds_bytes(a.d.n_buckets, a.gbias != nullptr)))
-    return launch<T, KS, HG, NKV, 1, QS>(a);
-  return launch<T, KS, HG, NKV, 1, 1>(a);
-}
-
-template <typename T, int KS>
-hipError_t by_heads(const AttnArgs& a) {
-  const int rep = a.d.n_heads / a.d.n_kv_heads;
-  if constexpr (kPlanes<T> * KS <= 4) {
-    if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a);
-    if constexpr (KS <= 2)
-      if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a);
+  if (e != hipSuccess) return e;
+  if (a.split) {
+    const int64_t n = (int64_t)a.d.n_nodes * a.d.n_kv_heads * 2 * (a.d.head_dim / 4);
+    hipLaunchKernelGGL(k_attn_join_kv<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, a.stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  return by_waves<T, KS, 1, 1>(a);
+  return a.gbias ? join_bias<T>(a, tiles) : hipSuccess;
+}
+
+// ---- which variant
+// As the query side, but the columns of the bias gradient bound the waves of a workgroup:
+// eight up to 32 buckets, four up to 64.  (us) 1,536 atoms, 8 heads of 32, bfloat16: 2x4 44,
+// 2x2 59, 4x1 100; 4,096 atoms: 4x2 145, 2x4 174; 512 molecules of 62 atoms: 2x1 130, 2x2 259.
+template <typename T, int KS>
+hipError_t by_waves(const AttnArgs& a) {
+  const Extent x(a.d, a.split ? a.d.n_heads : a.d.n_kv_heads);
+  const int nb = a.d.n_buckets;
+  const bool grad = a.gbias != nullptr;
+  if (x.mean <= kTile) return launch<T, KS, 1, 1>(a);
+  if (x.mean < 1024 && x.units >= 1024) return launch<T, KS, 2, 1>(a);
+  if (x.units >= 1024 && DkvShape<T, KS, 4, 2>::lds_bytes(nb, grad) <= kLdsMax) return launch<T, KS, 4, 2>(a);
+  if (x.units < 1024 && DkvShape<T, KS, 2, 4>::lds_bytes(nb, grad) <= kLdsMax) return launch<T, KS, 2, 4>(a);
+  if (DkvShape<T, KS, 2, 2>::lds_bytes(nb, grad) <= kLdsMax) return launch<T, KS, 2, 2>(a);
+  return launch<T, KS, 2, 1>(a);
 }
 
 template <typename T>
 hipError_t by_width(const AttnArgs& a) {
   const int ks = (a.d.head_dim + 15) / 16;
-  if (ks <= 1) return by_heads<T, 1>(a);
-  if (ks <= 2) return by_heads<T, 2>(a);
-  if (ks <= 3) return by_heads<T, 3>(a);
-  if (ks <= 4) return by_heads<T, 4>(a);
-  if (ks <= 6) return by_heads<T, 6>(a);
-  return by_heads<T, 8>(a);
+  if (ks <= 1) return by_waves<T, 1>(a);
+  if (ks <= 2) return by_waves<T, 2>(a);
+  if (ks <= 3) return by_waves<T, 3>(a);
+  if (ks <= 4) return by_waves<T, 4>(a);
+  if (ks <= 6) return by_waves<T, 6>(a);
+  return by_waves<T, 8>(a);
 }
 
 }  // namespace
 
-hipError_t attn_backward(const AttnArgs& a) {
+hipError_t attn_backward(const AttnArgs& args) {
+  AttnArgs a = args;
+  a.split = split_heads(a.d);
   if (a.d.n_nodes == 0) return a.d.dtype == TP_F32 ? join_bias<float>(a, 0) : join_bias<bf16_t>(a, 0);
   hipError_t e = attn_backward_q(a);       // also leaves delta for the key side
   if (e != hipSuccess) return e;
   return a.d.dtype == TP_F32 ? by_width<float>(a) : by_width<bf16_t>(a);
 }
 
-size_t attn_delta_floats(const tp_attn& d) { return ((size_t)d.n_heads * d.n_nodes + 3) / 4 * 4; }
-size_t attn_part_floats(const tp_attn& d) {
-  return ((size_t)d.n_nodes / kTile + d.n_segments) * d.n_heads * d.n_buckets;
+AttnWorkspace attn_workspace(const tp_attn& d) {
+  AttnWorkspace w;
+  w.part = ((size_t)d.n_heads * d.n_nodes + 3) / 4 * 4;
+  w.kv_part = w.part + (((size_t)d.n_nodes / kTile + d.n_segments) * d.n_heads * d.n_buckets + 3) / 4 * 4;
+  w.floats = w.kv_part + (split_heads(d) ? (size_t)d.n_nodes * d.n_heads * 2 * d.head_dim : 0);
+  return w;
 }
 
 }  // namespace tpc

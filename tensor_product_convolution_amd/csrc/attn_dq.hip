@@ -12,23 +12,20 @@
 // forms ds again, takes delta + r.
 #include "attn.hpp"
 
-#include <algorithm>
-
 namespace tpc {
 namespace {
 
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
 struct DqShape {
   using G = Tile<T, KS>;
-  static constexpr int kThreads = 64 * QW * KW, kRows = kTile * KW;
-  using Stage = Stager<T, KS, kThreads, KW, NKV>;
+  static constexpr int kThreads = 64 * QW * KW;
+  using Stage = Stager<T, KS, 64 * QW, NKV>;
+  static constexpr int kBuf = Stage::kBytes + RowStager::kBytes, kBufs = buffers(kBuf, QW, KW);
   static constexpr int kPart = (G::MT * 16 + 1) * 64;
   static constexpr int kJoin = QW * (KW - 1) * HG * kPart * 4;
-  static constexpr int kTileBytes = Stage::kBytes > kJoin ? Stage::kBytes : kJoin;
-  static size_t lds_bytes(int nb) {
-    return (size_t)kTileBytes + 12 * kRows + 16 * KW + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128;
-  }
-  static constexpr int kRegs = HG * (2 * KS * G::P * 4 + G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 4 : 8);
+  static constexpr int kWork = kBuf * kBufs * KW > kJoin ? kBuf * kBufs * KW : kJoin;
+  static size_t lds_bytes(int nb) { return kWork + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128; }
+  static constexpr int kRegs = HG * (2 * KS * G::P * 4 + G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
@@ -36,12 +33,9 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     k_attn_dq(AttnArgs a) {
   using S = DqShape<T, KS, HG, NKV, QW, KW>;
   using G = Tile<T, KS>;
-  constexpr int P = G::P, MT = G::MT, NP = S::kRows;
+  constexpr int P = G::P, MT = G::MT;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  uint16_t* tiles = reinterpret_cast<uint16_t*>(lds);
-  float* pos = reinterpret_cast<float*>(lds + S::kTileBytes);
-  uint32_t* valid = reinterpret_cast<uint32_t*>(pos + 3 * NP);
-  float* tbl = reinterpret_cast<float*>(valid + 4 * KW);
+  float* tbl = reinterpret_cast<float*>(lds + S::kWork);
   const tp_attn& d = a.d;
   const int h0 = blockIdx.y * HG;
   int lo, hi, q0;
@@ -50,8 +44,9 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
   const int kw = wv % KW, qw = wv / KW;
   const int rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
   const bool biased = d.n_buckets > 0;
-  fill_table<HG>(d, h0, tbl, S::kThreads);
-  const Buckets<HG> bk(d, lane);
+  const Scale scale(d.scale);
+  fill_table<HG>(d, scale.inv, h0, tbl, S::kThreads);
+  const Buckets<HG> bk(d, tbl, lane);
 
   const int q = q0 + 32 * qw + (lane & 31), qc = q < hi ? q : hi - 1;
   float x = 0.f, y = 0.f, z = 0.f;
@@ -64,8 +59,8 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
   float lse[HG], delta[HG];
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
-    own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, Q[hh]);
-    own_rows<T, KS>(a.go, a.gos, qc, h0 + hh, D, half, true, dO[hh]);
+    own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, scale.sign, Q[hh]);
+    own_rows<T, KS>(a.go, a.gos, qc, h0 + hh, D, half, true, 1.f, dO[hh]);
     float s = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
@@ -85,18 +80,6 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     lse[hh] = q < hi && e != -INFINITY ? e * kLog2e : INFINITY;
   }
 
-  typename S::Stage st;
-  PosStager<NP> ps;
-  bool live = false;
-  auto fetch = [&](int k0) {
-    st.fetch(a.k, a.ks, a.v, a.vs, k0, hi, D, d.key_mask, [&](int slot) { return (h0 + slot) / rep; });
-    if (biased) ps.fetch(d.pos, k0, hi);
-    if ((int)threadIdx.x < NP) {
-      const int k = k0 + threadIdx.x;
-      live = k < hi && (!d.key_mask || d.key_mask[k] != 0);
-    }
-  };
-
   f16v dQ[HG][MT];
   float r[HG];
 #pragma unroll
@@ -104,37 +87,42 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     r[hh] = 0.f;
     clear<MT>(dQ[hh]);
   }
-  const float c = d.scale * kLog2e;
 
-  fetch(lo);
-  for (int k0 = lo; k0 < hi; k0 += NP) {
-    __syncthreads();
-    st.stage(tiles);
-    ps.stage(pos);
-    const uint64_t vote = __ballot(live);
-    if ((int)threadIdx.x < NP && (lane & 31) == 0) valid[4 * (threadIdx.x >> 5)] = (uint32_t)(vote >> (32 * half));
-    __syncthreads();
-    if (hi - k0 > NP) fetch(k0 + NP);
-    if (32 * kw >= hi - k0) continue;
-    const uint32_t vm = __builtin_amdgcn_readfirstlane(valid[4 * kw]);
-    if (vm == 0) continue;
-    int off[16];
-    tile_offsets<HG>(bk, biased, pos, NP, 32 * kw, half, x, y, z, off);
-    if (vm != 0xffffffffu) mask_offsets<HG>(bk, vm, half, off);
+  typename S::Stage st;
+  RowStager rows;
+  const int tid = qw * 64 + lane;          // among the threads that share a tile
+  char* mine = lds + kw * S::kBufs * S::kBuf;
+  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
+  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
+  const int k_first = lo + 32 * kw;
+  st.aim(tid, a.k, a.ks, a.v, a.vs, k_first, 32 * KW, D, [&](int slot) { return (h0 + slot) / rep; });
+  const auto prepare = [&](int i) {
+    st.fetch(k_first + i * 32 * KW, hi, D, d.key_mask);
+    rows.fetch(tid, d, biased, k_first + i * 32 * KW, hi, d.key_mask);
+  };
+  const auto stage = [&](int buf) {
+    st.stage(tiles_of(buf));
+    rows.stage(tid, rows_of(buf));
+  };
+  __syncthreads();                         // the table
+  walk<(QW > 1), S::kBufs>((hi - lo + 32 * KW - 1) / (32 * KW), prepare, stage, [&](int buf) {
+    const uint32_t vm = RowStager::valid(rows_of(buf));
+    if (vm == 0) return;                   // past the end, or all masked
+    uint32_t ent[16];
+    tile_entries<HG>(bk, biased, rows_of(buf), half, x, y, z, ent);
+    if (vm != 0xffffffffu) mask_entries<HG>(bk, vm, half, ent);
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
-      const uint16_t* kt = tiles + (size_t)((kw * NKV + (NKV == 1 ? 0 : hh)) * 2) * G::kElems;
-      f16v s, dp;
-      clear<1>(&s);
+      const uint16_t* kt = tiles_of(buf) + (NKV == 1 ? 0 : hh * 2) * G::kElems;
+      const f16v s = scores<T, KS>(kt, Q[hh], ent, hh, lane);
+      f16v dp;
       clear<1>(&dp);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<T, KS>(kt, kk, lane), Q[hh][kk], s);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) dp = mma(row_frag<T, KS>(kt + G::kElems, kk, lane), dO[hh][kk], dp);
       float ds[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[i], c, table(tbl, off[i], hh)) - lse[hh]);
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale.c, -lse[hh]));
         ds[i] = p * (dp[i] - delta[hh]);
         r[hh] += ds[i];
       }
@@ -146,7 +134,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
         for (int mt = 0; mt < MT; ++mt) dQ[hh][mt] = mma(col_frag<T, KS>(kt, mt, kb, lane), f, dQ[hh][mt]);
       }
     }
-  }
+  });
 
   if (KW > 1) {
     float* join = reinterpret_cast<float*>(lds) + (size_t)qw * (KW - 1) * HG * S::kPart + lane;
@@ -186,26 +174,36 @@ hipError_t launch(const AttnArgs& a) {
   return launch_lds(k_attn_dq<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a.stream, a);
 }
 
+// ---- which variant
+// The waves of a workgroup: with enough query tiles to fill the chip, eight tiles share the
+// staged keys; with few, two tiles share them and the other waves split the keys, four
+// ways where LDS holds the tiles; short structures get one wave per tile.  (us) 4,096
+// atoms, 8 heads of 32, bfloat16: 2x4 84, 8x1 178; 512 molecules of 62 atoms: 2x1 57, 1x1 67.
 template <typename T, int KS, int HG, int NKV>
-hipError_t by_waves(const AttnArgs& a) {
-  constexpr int pair = Tile<T, KS>::kElems * 4 * NKV;
-  constexpr int KW = pair * 4 <= 96 * 1024 ? 4 : 2;
-  const int64_t tiles = ((int64_t)a.d.n_nodes / kTile + a.d.n_segments) * (a.d.n_heads / HG);
-  const int64_t mean = a.d.n_nodes / std::max(1, a.d.n_segments);
-  if (mean > 64 && tiles >= 4096) return launch<T, KS, HG, NKV, 4, 1>(a);
-  if (mean > 64) return launch<T, KS, HG, NKV, 1, KW>(a);
-  return launch<T, KS, HG, NKV, 1, 1>(a);
+hipError_t by_waves(const AttnArgs& a, const Extent& x) {
+  constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
+  constexpr int64_t fill = kPlanes<T> * KS <= 2 ? 4096 : 2048;       // waves a chip holds of this kernel
+  const int64_t waves = x.units / HG;
+  if (x.mean <= kTile) return launch<T, KS, HG, NKV, 1, 1>(a);
+  if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, 8, 1>(a);
+  if (x.mean >= 1024 || waves < 1024) return launch<T, KS, HG, NKV, 2, KX>(a);
+  return launch<T, KS, HG, NKV, 2, 1>(a);
 }
 
+// Two heads to a wave share distances and buckets, where their operands fit the registers
+// and half the waves still fill the chip (4,096 atoms, 8 heads of 32: 84 against 106 us;
+// 1,536 atoms: 38 against 34 us).
 template <typename T, int KS>
 hipError_t by_heads(const AttnArgs& a) {
-  constexpr bool pairs = kPlanes<T> * KS <= 4;      // operands of two heads fit the registers
-  const int rep = a.d.n_heads / a.d.n_kv_heads;
-  if constexpr (pairs) {
-    if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a);
-    if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a);
+  const Extent x(a.d, a.d.n_heads);
+  if constexpr (kPlanes<T> * KS <= 4) {
+    const int rep = a.d.n_heads / a.d.n_kv_heads;
+    if (x.units >= 1024) {
+      if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a, x);
+      if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a, x);
+    }
   }
-  return by_waves<T, KS, 1, 1>(a);
+  return by_waves<T, KS, 1, 1>(a, x);
 }
 
 template <typename T>

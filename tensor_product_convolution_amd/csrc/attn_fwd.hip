@@ -2,11 +2,9 @@
 // One pass over the keys with a running maximum and sum per query (see attn.hpp
 // for the tile layout); HG heads share the tile's distances and buckets.
 //
-// QW x KW waves: QW own 32 queries each, KW split the keys and are joined through
-// LDS at the end (for batches with few query tiles).
+// QW x KW waves: QW own 32 queries each and share staged keys, KW split the keys and
+// are joined through LDS at the end (for batches with few query tiles).
 #include "attn.hpp"
-
-#include <algorithm>
 
 namespace tpc {
 namespace {
@@ -14,16 +12,15 @@ namespace {
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
 struct FwdShape {
   using G = Tile<T, KS>;
-  static constexpr int kThreads = 64 * QW * KW, kRows = kTile * KW;
-  using Stage = Stager<T, KS, kThreads, KW, NKV>;
+  static constexpr int kThreads = 64 * QW * KW;
+  using Stage = Stager<T, KS, 64 * QW, NKV>;
+  static constexpr int kBuf = Stage::kBytes + RowStager::kBytes, kBufs = buffers(kBuf, QW, KW);
   static constexpr int kPart = (G::MT * 16 + 2) * 64;                // floats of one wave's head to join
   static constexpr int kJoin = QW * (KW - 1) * HG * kPart * 4;
-  static constexpr int kTileBytes = Stage::kBytes > kJoin ? Stage::kBytes : kJoin;
-  static size_t lds_bytes(int nb) {
-    return (size_t)kTileBytes + 12 * kRows + 16 * KW + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128;
-  }
+  static constexpr int kWork = kBuf * kBufs * KW > kJoin ? kBuf * kBufs * KW : kJoin;
+  static size_t lds_bytes(int nb) { return kWork + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128; }
   // operands, accumulators and scores beside what the fetch holds
-  static constexpr int kRegs = HG * (KS * G::P * 4 + G::MT * 16) + 60 + Stage::kChunks * (G::P == 1 ? 4 : 8);
+  static constexpr int kRegs = HG * (KS * G::P * 4 + G::MT * 16 + 16) + 60 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
@@ -31,12 +28,9 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
     k_attn_fwd(AttnArgs a) {
   using S = FwdShape<T, KS, HG, NKV, QW, KW>;
   using G = Tile<T, KS>;
-  constexpr int P = G::P, MT = G::MT, NP = S::kRows;
+  constexpr int P = G::P, MT = G::MT;
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  uint16_t* tiles = reinterpret_cast<uint16_t*>(lds);
-  float* pos = reinterpret_cast<float*>(lds + S::kTileBytes);        // [3][NP]
-  uint32_t* valid = reinterpret_cast<uint32_t*>(pos + 3 * NP);       // [KW], 16 bytes each
-  float* tbl = reinterpret_cast<float*>(valid + 4 * KW);
+  float* tbl = reinterpret_cast<float*>(lds + S::kWork);
   const tp_attn& d = a.d;
   int lo, hi, q0;
   if (!find_tile(d, kTile * QW, blockIdx.x, lo, hi, q0)) return;
@@ -44,8 +38,9 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   const int kw = wv % KW, qw = wv / KW;
   const int h0 = blockIdx.y * HG, rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
   const bool biased = d.n_buckets > 0;
-  fill_table<HG>(d, h0, tbl, S::kThreads);
-  const Buckets<HG> bk(d, lane);
+  const Scale scale(d.scale);
+  fill_table<HG>(d, scale.inv, h0, tbl, S::kThreads);
+  const Buckets<HG> bk(d, tbl, lane);
 
   // this lane's query
   const int q = q0 + 32 * qw + (lane & 31), qc = q < hi ? q : hi - 1;
@@ -57,19 +52,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   }
   Frag<P> Q[HG][KS];
 #pragma unroll
-  for (int hh = 0; hh < HG; ++hh) own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, Q[hh]);
-
-  typename S::Stage st;
-  PosStager<NP> ps;
-  bool live = false;
-  auto fetch = [&](int k0) {
-    st.fetch(a.k, a.ks, a.v, a.vs, k0, hi, D, d.key_mask, [&](int slot) { return (h0 + slot) / rep; });
-    if (biased) ps.fetch(d.pos, k0, hi);
-    if ((int)threadIdx.x < NP) {
-      const int k = k0 + threadIdx.x;
-      live = k < hi && (!d.key_mask || d.key_mask[k] != 0);
-    }
-  };
+  for (int hh = 0; hh < HG; ++hh) own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, scale.sign, Q[hh]);
 
   f16v O[HG][MT];
   float m[HG], l[HG];
@@ -79,62 +62,75 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
     l[hh] = 0.f;
     clear<MT>(O[hh]);
   }
-  const float c = d.scale * kLog2e;
 
-  fetch(lo);
-  for (int k0 = lo; k0 < hi; k0 += NP) {
-    __syncthreads();                       // the previous step's tiles have been read
-    st.stage(tiles);
-    ps.stage(pos);
-    const uint64_t vote = __ballot(live);
-    if ((int)threadIdx.x < NP && (lane & 31) == 0) valid[4 * (threadIdx.x >> 5)] = (uint32_t)(vote >> (32 * half));
-    __syncthreads();
-    if (hi - k0 > NP) fetch(k0 + NP);
-    if (32 * kw >= hi - k0) continue;      // this wave's tile lies past the end
-    const uint32_t vm = __builtin_amdgcn_readfirstlane(valid[4 * kw]);
-    if (vm == 0) continue;
-    int off[16];
-    tile_offsets<HG>(bk, biased, pos, NP, 32 * kw, half, x, y, z, off);
-    if (vm != 0xffffffffu) mask_offsets<HG>(bk, vm, half, off);
+  typename S::Stage st;
+  RowStager rows;
+  const int tid = qw * 64 + lane;          // among the threads that share a tile
+  char* mine = lds + kw * S::kBufs * S::kBuf;
+  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
+  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
+  const int k_first = lo + 32 * kw;
+  st.aim(tid, a.k, a.ks, a.v, a.vs, k_first, 32 * KW, D, [&](int slot) { return (h0 + slot) / rep; });
+  const auto prepare = [&](int i) {
+    st.fetch(k_first + i * 32 * KW, hi, D, d.key_mask);
+    rows.fetch(tid, d, biased, k_first + i * 32 * KW, hi, d.key_mask);
+  };
+  const auto stage = [&](int buf) {
+    st.stage(tiles_of(buf));
+    rows.stage(tid, rows_of(buf));
+  };
+  __syncthreads();                         // the table
+  walk<(QW > 1), S::kBufs>((hi - lo + 32 * KW - 1) / (32 * KW), prepare, stage, [&](int buf) {
+    const uint32_t vm = RowStager::valid(rows_of(buf));
+    if (vm == 0) return;                   // past the end, or all masked
+    uint32_t ent[16];
+    tile_entries<HG>(bk, biased, rows_of(buf), half, x, y, z, ent);
+    if (vm != 0xffffffffu) mask_entries<HG>(bk, vm, half, ent);
+    // every head's scores first: a head's products run while another's softmax does
+    const uint16_t* kt = tiles_of(buf);
+    f16v sc[HG];
+#pragma unroll
+    for (int hh = 0; hh < HG; ++hh) sc[hh] = scores<T, KS>(kt + (NKV == 1 ? 0 : hh * 2) * G::kElems, Q[hh], ent, hh, lane);
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
-      const uint16_t* kt = tiles + (size_t)((kw * NKV + (NKV == 1 ? 0 : hh)) * 2) * G::kElems;
-      f16v s;
-      clear<1>(&s);
+      const uint16_t* vt = kt + (NKV == 1 ? 1 : hh * 2 + 1) * G::kElems;
+      float p[16], sum = 0.f;
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<T, KS>(kt, kk, lane), Q[hh][kk], s);
-      float p[16];
+      for (int i = 0; i < 16; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -m[hh]));
+        sum += p[i];
+      }
+      // The running maximum is raised when the tile's sum shows that it has been passed by
+      // far: probabilities up to 2^9 lose nothing, most tiles need no maximum at all, and
+      // the accumulators are rescaled in few.  NaN takes this way in every tile.
+      if (__any(!(sum <= 512.f))) {
+        float tm = fmaxf(sc[hh][0], sc[hh][1]);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = fmaf(s[i], c, table(tbl, off[i], hh));
-      float tm = fmaxf(p[0], p[1]);
-#pragma unroll
-      for (int i = 2; i < 16; ++i) tm = fmaxf(tm, p[i]);
-      tm = pair_max(tm);
-      // the maximum follows in steps of at least 2^8: probabilities up to 2^8 lose nothing,
-      // and the accumulators are rescaled in few tiles
-      if (__any(tm > m[hh] + 8.f)) {
-        const float mn = fmaxf(m[hh], tm), f = __builtin_amdgcn_exp2f(m[hh] - mn);
+        for (int i = 2; i < 16; ++i) tm = fmaxf(tm, sc[hh][i]);
+        const float mn = fmaxf(m[hh], pair_max(tm) * scale.c), f = __builtin_amdgcn_exp2f(m[hh] - mn);
         m[hh] = mn;
         l[hh] *= f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) O[hh][mt][i] *= f;
-      }
+        sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(p[i] - m[hh]);
-        l[hh] += p[i];
+        for (int i = 0; i < 16; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -mn));
+          sum += p[i];
+        }
       }
+      l[hh] += sum;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         Frag<P> pf;
         to_frag(p + 8 * kb, pf);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) O[hh][mt] = mma(col_frag<T, KS>(kt + G::kElems, mt, kb, lane), pf, O[hh][mt]);
+        for (int mt = 0; mt < MT; ++mt) O[hh][mt] = mma(col_frag<T, KS>(vt, mt, kb, lane), pf, O[hh][mt]);
       }
     }
-  }
+  });
 
   if (KW > 1) {
     float* join = reinterpret_cast<float*>(lds) + (size_t)qw * (KW - 1) * HG * S::kPart + lane;
@@ -180,29 +176,37 @@ hipError_t launch(const AttnArgs& a) {
   return launch_lds(k_attn_fwd<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a.stream, a);
 }
 
+// ---- which variant
+// The waves of a workgroup: with enough query tiles to fill the chip, eight tiles share the
+// staged keys; with few, two tiles share them and the other waves split the keys, four
+// ways where LDS holds the tiles; short structures get one wave per tile.  Measured
+// (us): 16,384 atoms, 8 heads of 64, bfloat16: 8x1 1,003, 2x4 1,380; 4,096 atoms, 8 heads of
+// 32: 2x4 78, 8x1 158; 512 molecules of 62 atoms, 8 heads of 32: 2x1 45, 1x1 58, 2x4 110.
 template <typename T, int KS, int HG, int NKV>
-hipError_t by_waves(const AttnArgs& a) {
-  // tiles of 32 queries and heads: where they fill the chip, four query tiles share
-  // the staged keys; else the waves split the keys of one tile, as far as LDS holds
-  // the tiles
-  constexpr int pair = Tile<T, KS>::kElems * 4 * NKV;
-  constexpr int KW = pair * 4 <= 96 * 1024 ? 4 : 2;
-  const int64_t tiles = ((int64_t)a.d.n_nodes / kTile + a.d.n_segments) * (a.d.n_heads / HG);
-  const int64_t mean = a.d.n_nodes / std::max(1, a.d.n_segments);
-  if (mean > 64 && tiles >= 4096) return launch<T, KS, HG, NKV, 4, 1>(a);
-  if (mean > 64) return launch<T, KS, HG, NKV, 1, KW>(a);
-  return launch<T, KS, HG, NKV, 1, 1>(a);
+hipError_t by_waves(const AttnArgs& a, const Extent& x) {
+  constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
+  constexpr int64_t fill = kPlanes<T> * KS <= 2 ? 4096 : 2048;       // waves a chip holds of this kernel
+  const int64_t waves = x.units / HG;
+  if (x.mean <= kTile) return launch<T, KS, HG, NKV, 1, 1>(a);
+  if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, 8, 1>(a);
+  if (x.mean >= 1024 || waves < 1024) return launch<T, KS, HG, NKV, 2, KX>(a);
+  return launch<T, KS, HG, NKV, 2, 1>(a);
 }
 
+// Two heads to a wave share distances and buckets, where their operands fit the registers
+// and half the waves still fill the chip (16,384 atoms: 1,003 against 1,104 us; 1,536
+// atoms: 32 against 24 us).
 template <typename T, int KS>
 hipError_t by_heads(const AttnArgs& a) {
-  constexpr bool pairs = kPlanes<T> * KS <= 6;      // operands of two heads fit the registers
-  const int rep = a.d.n_heads / a.d.n_kv_heads;
-  if constexpr (pairs) {
-    if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a);
-    if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a);
+  const Extent x(a.d, a.d.n_heads);
+  if constexpr (kPlanes<T> * KS <= 4) {
+    const int rep = a.d.n_heads / a.d.n_kv_heads;
+    if (x.units >= 2048) {
+      if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a, x);
+      if (rep == 1 && a.d.n_heads % 2 == 0) return by_waves<T, KS, 2, 2>(a, x);
+    }
   }
-  return by_waves<T, KS, 1, 1>(a);
+  return by_waves<T, KS, 1, 1>(a, x);
 }
 
 template <typename T>

@@ -60,14 +60,18 @@ tp_status check_attn(const char* where, const tp_attn* a) {
   if (!known(a->dtype)) return fail(where, "unknown element type");
   if (a->n_nodes < 0 || a->n_segments < 0) return fail(where, "negative size");
   if (a->n_nodes > 0 && a->n_segments == 0) return fail(where, "nodes without a structure");
-  if ((int64_t)a->n_nodes / 32 + a->n_segments > std::numeric_limits<int32_t>::max())
-    return fail(where, "too many structures for one launch", TP_ERR_OVERFLOW);
+  // row numbers run up to eight tiles past the end, the grid has a tile for every 32 nodes
+  // and one for every structure
+  if (a->n_nodes > std::numeric_limits<int32_t>::max() - 4096 ||
+      (int64_t)a->n_nodes / 32 + a->n_segments > std::numeric_limits<int32_t>::max())
+    return fail(where, "too many nodes or structures for one launch", TP_ERR_OVERFLOW);
   if (a->n_heads < 1 || a->n_kv_heads < 1 || a->n_heads % a->n_kv_heads)
     return fail(where, "n_heads must be a positive multiple of n_kv_heads");
   if (a->n_heads > 1024) return fail(where, "at most 1024 heads", TP_ERR_UNSUPPORTED);
   if (a->head_dim < 8 || a->head_dim > 128 || a->head_dim % 8)
     return fail(where, "head_dim must be a multiple of 8 in 8..128", TP_ERR_UNSUPPORTED);
-  if (!std::isfinite(a->scale)) return fail(where, "scale must be finite");
+  const float size = std::fabs(a->scale);
+  if (!(size == 0.f || (size >= 1e-8f && size <= 1e8f))) return fail(where, "scale must be 0 or of size 1e-8 to 1e8");
   if (a->n_buckets < 0) return fail(where, "negative n_buckets");
   if (a->n_buckets > 64) return fail(where, "at most 64 buckets", TP_ERR_UNSUPPORTED);
   if (a->n_buckets > 0) {
@@ -257,7 +261,7 @@ tp_status tp_attn_backward_workspace(const tp_attn* a, size_t* bytes) {
   return guarded([&]() -> tp_status {
     if (!bytes) return fail("tp_attn_backward_workspace", "bytes is NULL");
     tp_status s = check_attn("tp_attn_backward_workspace", a);
-    if (s == TP_OK) *bytes = (tpc::attn_delta_floats(*a) + tpc::attn_part_floats(*a)) * sizeof(float);
+    if (s == TP_OK) *bytes = tpc::attn_workspace(*a).floats * sizeof(float);
     return s;
   });
 }
@@ -284,8 +288,8 @@ tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, co
       if (!lse) return fail(me, "lse is NULL");
       if ((s = check_attn_pointers(me, a)) != TP_OK) return s;
     }
-    const size_t nd = tpc::attn_delta_floats(*a), np = tpc::attn_part_floats(*a);
-    if (nd + np > 0 && (!ws || ws_bytes < (nd + np) * sizeof(float)))
+    const tpc::AttnWorkspace w = tpc::attn_workspace(*a);
+    if (w.floats > 0 && (!ws || ws_bytes < w.floats * sizeof(float)))
       return fail(me, "workspace missing or too small", TP_ERR_WORKSPACE);
     if (a->n_nodes == 0 && !grad_bias) return TP_OK;
     tpc::AttnArgs args;
@@ -309,7 +313,8 @@ tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, co
     args.gvs = gv_stride;
     args.lse_in = lse;
     args.delta = static_cast<float*>(ws);
-    args.part = args.delta + nd;
+    args.part = args.delta + w.part;
+    args.kv_part = args.delta + w.kv_part;
     args.stream = stream;
     hipError_t e = tpc::attn_backward(args);
     return e == hipSuccess ? TP_OK : tpc::hip_error(e, "tp_attn_backward launch");

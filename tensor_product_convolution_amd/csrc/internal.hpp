@@ -226,14 +226,18 @@ struct AttnArgs {
   void *out = nullptr, *gq = nullptr, *gk = nullptr, *gv = nullptr, *gbias = nullptr;
   float* lse = nullptr;
   const float* lse_in = nullptr;
-  float *delta = nullptr, *part = nullptr;        // workspace of the backward
+  float *delta = nullptr, *part = nullptr, *kv_part = nullptr;   // workspace of the backward
+  bool split = false;                             // query heads that share a key head apart
   hipStream_t stream = nullptr;
 };
 hipError_t attn_forward(const AttnArgs& a);
 hipError_t attn_backward(const AttnArgs& a);
 hipError_t attn_backward_q(const AttnArgs& a);   // its query side (attn_dq.hip)
-// floats of the workspace: delta [n_heads][n_nodes], then the bias gradient's parts
-size_t attn_delta_floats(const tp_attn& d);
-size_t attn_part_floats(const tp_attn& d);
+// workspace of the backward, in floats: delta [n_heads][n_nodes] from 0, the bias
+// gradient's parts, the parts of grad_k and grad_v
+struct AttnWorkspace {
+  size_t part = 0, kv_part = 0, floats = 0;
+};
+AttnWorkspace attn_workspace(const tp_attn& d);
 
 }  // namespace tpc
