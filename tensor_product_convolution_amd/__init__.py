@@ -952,6 +952,19 @@ def radial_workspace(plan, n_nodes, with_mix):
     return b.value
 
 
-from .layers import (Dropout, attn_backward, attn_forward, dropout_backward, dropout_forward,  # noqa: E402,F401
-                     layer_norm_backward, layer_norm_forward, layer_norm_residual_backward,
-                     layer_norm_residual_forward)
+# Attention, layer norm and dropout (layers.py), loaded on first use: plans and CG tables
+# need no torch.
+_LAYERS = ("Dropout", "attn_forward", "attn_backward", "layer_norm_forward", "layer_norm_backward",
+           "layer_norm_residual_forward", "layer_norm_residual_backward", "dropout_forward", "dropout_backward")
+
+
+def __getattr__(name):
+    if name in _LAYERS:
+        from . import layers
+        globals().update({n: getattr(layers, n) for n in _LAYERS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted({*globals(), *_LAYERS})

@@ -509,12 +509,14 @@ struct Extent {
       : units(((int64_t)d.n_nodes / kTile + d.n_segments) * heads), mean(d.n_nodes / (d.n_segments > 0 ? d.n_segments : 1)) {}
 };
 
-// a kernel that may use all of a CU's LDS, launched with `bytes` of it
+// a launch with `bytes` of LDS, which above 64 KiB have to be asked for
 template <typename K, typename... A>
 hipError_t launch_lds(K kernel, dim3 grid, int threads, size_t bytes, hipStream_t st, A... args) {
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kLdsMax);
-  if (e != hipSuccess) return e;
+  if (bytes > 64 * 1024) {
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kLdsMax);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(kernel, grid, dim3(threads), bytes, st, args...);
   return hipGetLastError();
 }

@@ -8,9 +8,13 @@ strided rows are taken as they are where the C entry point takes a stride.
 import ctypes
 from typing import NamedTuple
 
-from . import _check, _need, _ptr, _stream, _torch, lib
+import torch
+
+from . import TPError, lib
 
 TP_F32, TP_BF16 = 0, 1
+_CODES = {torch.float32: TP_F32, torch.bfloat16: TP_BF16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _Dropout(ctypes.Structure):
@@ -37,56 +41,81 @@ class Dropout(NamedTuple):
         return _Dropout(self.p, self.seed, self.offset)
 
 
+# The smallest calls are bound by the host, so the checks take one pass over the
+# attributes and pointers go to ctypes as plain integers.
 def _code(t, name):
-    torch = _torch()
+    """Element type code and device number of an operand."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.device.type != "cuda":
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must live on the GPU")
-    if t.dtype is torch.float32:
-        return TP_F32
-    if t.dtype is torch.bfloat16:
-        return TP_BF16
-    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return code, dev
 
 
-def _same(t, name, like):
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    return t
-
-
-def _rows(t, name, like, shape):
-    """A tensor of rows (dense but for the row stride) of the type and device of ``like``."""
-    if not isinstance(t, type(like)) and not isinstance(t, _torch().Tensor):
+def _refuse(t, name, dtype, shape, dev):
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype is not like.dtype:
-        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    _same(t, name, like)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this type, shape and device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() and t.shape == shape
+            and t.get_device() == dev):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+
+
+def _rows(t, name, dtype, shape, dev):
+    """(address, row stride) of a tensor whose rows are dense, whatever their stride."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev):
+        _refuse(t, name, dtype, shape, dev)
+    strides = t.stride()
     want = 1
-    for s, n in zip(t.stride()[:0:-1], shape[:0:-1]):
-        if n != 1 and s != want:
+    for i in range(len(shape) - 1, 0, -1):
+        if strides[i] != want and shape[i] != 1:
             raise ValueError(f"{name}: rows must be contiguous")
-        want *= n
-    if shape[0] <= 1:
-        return want                     # the stride of a single row says nothing
-    return t.stride(0)
+        want *= shape[i]
+    # the stride of a single row says nothing
+    return t.data_ptr(), strides[0] if shape[0] > 1 else want
+
+
+def _call(dev, f, *args):
+    """The C entry point on the current stream of device ``dev``."""
+    if torch._C._cuda_getDevice() == dev:
+        status = f(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, _raw_stream(dev))
+    if status:
+        raise TPError(status, lib().tp_conv_last_error().decode())
+
+
+def _check(status):
+    if status:
+        raise TPError(status, lib().tp_conv_last_error().decode())
 
 
 # ---- dropout -------------------------------------------------------------------
 def _dropout(x, drop, residual, out):
-    torch = _torch()
-    dt = _code(x, "x")
-    _need(x, "x", x.dtype)
-    if residual is not None:
-        _same(_need(residual, "residual", x.dtype, x.shape), "residual", x)
+    code, dev = _code(x, "x")
+    dtype, shape = x.dtype, x.shape
+    px = _need(x, "x", dtype, shape, dev)
+    pr = None if residual is None else _need(residual, "residual", dtype, shape, dev)
     if out is None:
         out = torch.empty_like(x)
-    _same(_need(out, "out", x.dtype, x.shape), "out", x)
-    _check(lib().tp_dropout_apply(dt, x.numel(), _ptr(x), _ptr(residual), ctypes.byref(drop.cstruct()), _ptr(out),
-                                  _stream(x.device)))
+    po = _need(out, "out", dtype, shape, dev)
+    _call(dev, lib().tp_dropout_apply, code, x.numel(), px, pr, ctypes.byref(drop.cstruct()), po)
     return out
 
 
@@ -102,24 +131,23 @@ def dropout_backward(grad_out, drop, out=None):
 
 # ---- layer norm ------------------------------------------------------------------
 def _norm_forward(x, residual, gamma, beta, drop, eps):
-    torch = _torch()
-    dt = _code(x, "x")
+    code, dev = _code(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [rows, columns]")
-    n, c = x.shape
-    xs = _rows(x, "x", x, (n, c))
-    _same(_need(gamma, "gamma", torch.float32, (c,)), "gamma", x)
-    _same(_need(beta, "beta", torch.float32, (c,)), "beta", x)
-    y = torch.empty((n, c), dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, n), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    h = None
+    dtype, shape = x.dtype, x.shape
+    n, c = shape
+    px, xs = _rows(x, "x", dtype, shape, dev)
+    pg = _need(gamma, "gamma", torch.float32, (c,), dev)
+    pb = _need(beta, "beta", torch.float32, (c,), dev)
+    y = x.new_empty(shape)
+    mean, rstd = x.new_empty((2, n), dtype=torch.float32).unbind(0)
+    h = pr = ph = None
     if residual is not None:
-        _same(_need(residual, "residual", x.dtype, (n, c)), "residual", x)
+        pr = _need(residual, "residual", dtype, shape, dev)
         h = torch.empty_like(y)
-    _check(lib().tp_layer_norm_forward(dt, n, c, _ptr(x), xs, _ptr(residual),
-                                       None if drop is None else ctypes.byref(drop.cstruct()), _ptr(gamma), _ptr(beta),
-                                       eps, _ptr(y), c, _ptr(h), _ptr(mean), _ptr(rstd), _stream(x.device)))
+        ph = h.data_ptr()
+    _call(dev, lib().tp_layer_norm_forward, code, n, c, px, xs, pr, None if drop is None else ctypes.byref(drop.cstruct()),
+          pg, pb, eps, y.data_ptr(), c, ph, mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd, h
 
 
@@ -137,33 +165,33 @@ def layer_norm_residual_forward(x, residual, gamma, beta, drop=None, eps=1e-5):
 
 
 def _norm_backward(grad_y, h, gamma, mean, rstd, grad_res, drop, want_x, want_weights):
-    torch = _torch()
-    dt = _code(h, "h")
+    code, dev = _code(h, "h")
     if h.dim() != 2:
         raise ValueError("h must be [rows, columns]")
-    n, c = h.shape
-    hs = _rows(h, "h", h, (n, c))
-    gs = _rows(grad_y, "grad_y", h, (n, c))
-    _same(_need(gamma, "gamma", torch.float32, (c,)), "gamma", h)
-    _same(_need(mean, "mean", torch.float32, (n,)), "mean", h)
-    _same(_need(rstd, "rstd", torch.float32, (n,)), "rstd", h)
-    if grad_res is not None:
-        _same(_need(grad_res, "grad_h", h.dtype, (n, c)), "grad_h", h)
-    gh = torch.empty((n, c), dtype=h.dtype, device=h.device)
+    dtype, shape = h.dtype, h.shape
+    n, c = shape
+    ph, hs = _rows(h, "h", dtype, shape, dev)
+    py, ys = _rows(grad_y, "grad_y", dtype, shape, dev)
+    pg = _need(gamma, "gamma", torch.float32, (c,), dev)
+    pm = _need(mean, "mean", torch.float32, (n,), dev)
+    ps = _need(rstd, "rstd", torch.float32, (n,), dev)
+    pr = None if grad_res is None else _need(grad_res, "grad_h", dtype, shape, dev)
+    gh = h.new_empty(shape)
     gx = torch.empty_like(gh) if want_x else None
-    gg = gb = ws = None
+    gg = gb = ws = pgg = pgb = pws = None
     nbytes = 0
     if want_weights:
         need = ctypes.c_size_t()
-        _check(lib().tp_layer_norm_workspace(dt, n, c, ctypes.byref(need)))
+        _check(lib().tp_layer_norm_workspace(code, n, c, ctypes.byref(need)))
         nbytes = need.value
-        gg = torch.empty(c, dtype=torch.float32, device=h.device)
-        gb = torch.empty(c, dtype=torch.float32, device=h.device)
+        gg, gb = h.new_empty((2, c), dtype=torch.float32).unbind(0)
+        pgg, pgb = gg.data_ptr(), gb.data_ptr()
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=h.device)
-    _check(lib().tp_layer_norm_backward(dt, n, c, _ptr(grad_y), gs, _ptr(h), hs, _ptr(gamma), _ptr(mean), _ptr(rstd),
-                                        _ptr(grad_res), None if drop is None else ctypes.byref(drop.cstruct()),
-                                        _ptr(gh), _ptr(gx), _ptr(gg), _ptr(gb), _ptr(ws), nbytes, _stream(h.device)))
+            ws = h.new_empty(nbytes, dtype=torch.uint8)
+            pws = ws.data_ptr()
+    _call(dev, lib().tp_layer_norm_backward, code, n, c, py, ys, ph, hs, pg, pm, ps, pr,
+          None if drop is None else ctypes.byref(drop.cstruct()), gh.data_ptr(), None if gx is None else gx.data_ptr(),
+          pgg, pgb, pws, nbytes)
     return gh, gx, gg, gb
 
 
@@ -184,37 +212,36 @@ def layer_norm_residual_backward(grad_y, h, gamma, mean, rstd, drop=None, grad_h
 
 # ---- attention -------------------------------------------------------------------
 def _describe(q, k, v, seg_ptr, pos, bias, r_min, steps, key_mask, scale):
-    """(tp_attn, strides of q, k, v) after the checks that need the tensors."""
-    torch = _torch()
-    dt = _code(q, "q")
+    """(tp_attn, device, addresses and strides of q, k, v) after the checks that need the tensors."""
+    code, dev = _code(q, "q")
     if q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("q must be [nodes, heads, head_dim], k and v [nodes, key heads, head_dim]")
+    dtype = q.dtype
     n, hq, d = q.shape
     hk = k.shape[1]
-    qs = _rows(q, "q", q, (n, hq, d))
-    ks = _rows(k, "k", q, (n, hk, d))
-    vs = _rows(v, "v", q, (n, hk, d))
-    _same(_need(seg_ptr, "seg_ptr", torch.int32), "seg_ptr", q)
-    if seg_ptr.dim() != 1 or seg_ptr.shape[0] < 1:
+    rows = (*_rows(q, "q", dtype, (n, hq, d), dev), *_rows(k, "k", dtype, (n, hk, d), dev),
+            *_rows(v, "v", dtype, (n, hk, d), dev))
+    if not isinstance(seg_ptr, torch.Tensor) or seg_ptr.dim() != 1 or seg_ptr.shape[0] < 1:
         raise ValueError("seg_ptr must hold the number of structures + 1 offsets")
+    m = seg_ptr.shape[0]
+    pseg = _need(seg_ptr, "seg_ptr", torch.int32, (m,), dev)
     nb = 0
+    pp = pb = pk = None
     if (pos is None) != (bias is None):
         raise ValueError("pos and bias go together")
     if bias is not None:
-        _same(_need(pos, "pos", torch.float32, (n, 3)), "pos", q)
+        pp = _need(pos, "pos", torch.float32, (n, 3), dev)
         if not isinstance(bias, torch.Tensor) or bias.dim() != 2 or bias.shape[1] < 1:
             raise ValueError("bias must be [heads, buckets]")
         nb = bias.shape[1]
-        _same(_need(bias, "bias", q.dtype, (hq, nb)), "bias", q)
+        pb = _need(bias, "bias", dtype, (hq, nb), dev)
     if key_mask is not None:
         if isinstance(key_mask, torch.Tensor) and key_mask.dtype is torch.bool:
             key_mask = key_mask.view(torch.uint8)
-        _same(_need(key_mask, "key_mask", torch.uint8, (n,)), "key_mask", q)
+        pk = _need(key_mask, "key_mask", torch.uint8, (n,), dev)
     if scale is None:
         scale = d ** -0.5 if d else 1.0
-    p = lambda t: None if t is None else t.data_ptr()
-    a = _Attn(dt, n, seg_ptr.shape[0] - 1, hq, hk, d, p(seg_ptr), p(key_mask), p(pos), p(bias), nb, steps, r_min, scale)
-    return a, qs, ks, vs
+    return _Attn(code, n, m - 1, hq, hk, d, pseg, pk, pp, pb, nb, steps, r_min, scale), dev, rows
 
 
 def attn_forward(q, k, v, seg_ptr, pos=None, bias=None, r_min=0.5, steps=4, key_mask=None, scale=None, out=None):
@@ -225,15 +252,12 @@ def attn_forward(q, k, v, seg_ptr, pos=None, bias=None, r_min=0.5, steps=4, key_
     projected row are fine); seg_ptr int32 [structures + 1] node offsets; pos [nodes, 3]
     and bias [heads, buckets]: learned bias by distance bucket; key_mask [nodes]
     (uint8 or bool, 0 = masked); scale defaults to head_dim ** -0.5."""
-    torch = _torch()
-    a, qs, ks, vs = _describe(q, k, v, seg_ptr, pos, bias, r_min, steps, key_mask, scale)
-    n, hq, d = q.shape
+    a, dev, rows = _describe(q, k, v, seg_ptr, pos, bias, r_min, steps, key_mask, scale)
+    shape = q.shape
     if out is None:
-        out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    os = _rows(out, "out", q, (n, hq, d))
-    lse = torch.empty((hq, n), dtype=torch.float32, device=q.device)
-    _check(lib().tp_attn_forward(ctypes.byref(a), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(out), os, _ptr(lse),
-                                 _stream(q.device)))
+        out = q.new_empty(shape)
+    lse = q.new_empty((shape[1], shape[0]), dtype=torch.float32)
+    _call(dev, lib().tp_attn_forward, ctypes.byref(a), *rows, *_rows(out, "out", q.dtype, shape, dev), lse.data_ptr())
     return out, lse
 
 
@@ -242,24 +266,20 @@ def attn_backward(q, k, v, seg_ptr, out, lse, grad_out, pos=None, bias=None, r_m
     """(grad_q, grad_k, grad_v, grad_bias) of attn_forward; grad_bias is None without a
     bias or with ``want_bias`` false.  ``outs``: (grad_q, grad_k, grad_v) to fill, e.g. the
     views of one projected row's gradient."""
-    torch = _torch()
-    a, qs, ks, vs = _describe(q, k, v, seg_ptr, pos, bias, r_min, steps, key_mask, scale)
+    a, dev, rows = _describe(q, k, v, seg_ptr, pos, bias, r_min, steps, key_mask, scale)
+    dtype = q.dtype
     n, hq, d = q.shape
     hk = k.shape[1]
-    os = _rows(out, "out", q, (n, hq, d))
-    gs = _rows(grad_out, "grad_out", q, (n, hq, d))
-    _same(_need(lse, "lse", torch.float32, (hq, n)), "lse", q)
     if outs is None:
-        outs = tuple(torch.empty((n, h, d), dtype=q.dtype, device=q.device) for h in (hq, hk, hk))
+        outs = [q.new_empty((n, h, d)) for h in (hq, hk, hk)]
     gq, gk, gv = outs
-    gqs = _rows(gq, "grad_q", q, (n, hq, d))
-    gks = _rows(gk, "grad_k", q, (n, hk, d))
-    gvs = _rows(gv, "grad_v", q, (n, hk, d))
     gb = torch.empty_like(bias) if bias is not None and want_bias else None
     need = ctypes.c_size_t()
     _check(lib().tp_attn_backward_workspace(ctypes.byref(a), ctypes.byref(need)))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=q.device) if need.value else None
-    _check(lib().tp_attn_backward(ctypes.byref(a), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(out), os, _ptr(lse),
-                                  _ptr(grad_out), gs, _ptr(gq), gqs, _ptr(gk), gks, _ptr(gv), gvs, _ptr(gb), _ptr(ws),
-                                  need.value, _stream(q.device)))
+    ws = q.new_empty(need.value, dtype=torch.uint8) if need.value else None
+    _call(dev, lib().tp_attn_backward, ctypes.byref(a), *rows, *_rows(out, "out", dtype, (n, hq, d), dev),
+          _need(lse, "lse", torch.float32, (hq, n), dev), *_rows(grad_out, "grad_out", dtype, (n, hq, d), dev),
+          *_rows(gq, "grad_q", dtype, (n, hq, d), dev), *_rows(gk, "grad_k", dtype, (n, hk, d), dev),
+          *_rows(gv, "grad_v", dtype, (n, hk, d), dev), None if gb is None else gb.data_ptr(),
+          None if ws is None else ws.data_ptr(), need.value)
     return gq, gk, gv, gb
