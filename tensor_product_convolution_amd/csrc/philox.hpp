@@ -38,22 +38,33 @@ __device__ __forceinline__ void philox4(const DropArgs& d, uint64_t blk, uint32_
   w[3] = c3;
 }
 
-// The words of elements e .. e + N - 1 (N a multiple of 4).  Where e is not a
-// multiple of 4 (odd row lengths) the run touches one block more and is
-// shifted into place.
-template <int N>
-__device__ __forceinline__ void philox_run(const DropArgs& d, uint64_t e, uint32_t w[N]) {
+// keep[j]: whether element e + j is kept, j < N (N a multiple of 4).  Where e is not a
+// multiple of 4 (odd row lengths, !ALIGNED) the run touches one block more.  A comparison's
+// result stays in scalar registers, one bit a lane.
+template <int N, bool ALIGNED>
+__device__ __forceinline__ void philox_keep(const DropArgs& d, uint64_t e, bool keep[N]) {
   const uint64_t blk = e >> 2;
-  const int s = (int)(e & 3);
+  if (ALIGNED) {
 #pragma unroll
-  for (int b = 0; b < N / 4; ++b) philox4(d, blk + b, w + 4 * b);
-  if (s == 0) return;
-  uint32_t v[N + 4];
+    for (int b = 0; b < N / 4; ++b) {
+      uint32_t w[4];
+      philox4(d, blk + b, w);
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = w[i];
-  philox4(d, blk + N / 4, v + N);
+      for (int j = 0; j < 4; ++j) keep[4 * b + j] = w[j] >= d.threshold;
+    }
+  } else {
+    uint32_t bits = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) w[i] = s == 1 ? v[i + 1] : s == 2 ? v[i + 2] : v[i + 3];
+    for (int b = 0; b < N / 4 + 1; ++b) {
+      uint32_t w[4];
+      philox4(d, blk + b, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bits |= (uint32_t)(w[j] >= d.threshold) << (4 * b + j);
+    }
+    bits >>= e & 3;
+#pragma unroll
+    for (int j = 0; j < N; ++j) keep[j] = (bits >> j) & 1;
+  }
 }
 
 }  // namespace tpc

@@ -38,6 +38,22 @@ __device__ __forceinline__ void load_chunk(const T* p, int left, float* o) {
   }
 }
 
+// the same as loaded: a chunk held for a row to come, widened when its turn comes
+template <typename T>
+struct RawChunk {
+  typename Chunk<T>::vec v;
+  __device__ __forceinline__ void load(const T* p, int left) {
+    constexpr int N = Chunk<T>::kN;
+    if (left >= N) {
+      v = *reinterpret_cast<const typename Chunk<T>::vec*>(p);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = j < left ? p[j] : (T)0.f;
+    }
+  }
+  __device__ __forceinline__ float at(int j) const { return (float)v[j]; }
+};
+
 template <typename T>
 __device__ __forceinline__ void store_chunk(T* p, int left, const float* o) {
   constexpr int N = Chunk<T>::kN;
