@@ -40,9 +40,9 @@ constexpr int kMaxBuckets = 64;
 template <typename T>
 constexpr int kPlanes = std::is_same<T, float>::value ? 3 : 1;
 
-// geometry of a staged tile: 32 rows of KS * 16 values (zero-filled from head_dim
-// on), rows padded by 16 bytes so that 16-byte reads of 32 rows spread over
-// the banks (the row length in 16-byte units is odd)
+// geometry of a staged tile: 32 rows of KS * 16 values (zero-filled from
+// head_dim on), rows padded by 16 bytes so that 16-byte reads of 32 rows spread over the
+// banks (the row length in 16-byte units is odd)
 template <typename T, int KS>
 struct Tile {
   static constexpr int P = kPlanes<T>;
@@ -132,10 +132,9 @@ struct Raw<float> {
   __device__ __forceinline__ float at(int j) const { return j < 4 ? a[j] : b[j - 4]; }
 };
 
-// row operand: tile row l % 32, contraction elements 16 kk + 8 (l / 32) + 0..7
-template <typename T, int KS>
-__device__ __forceinline__ Frag<kPlanes<T>> row_frag(const uint16_t* tile, int kk, int lane) {
-  using G = Tile<T, KS>;
+// row operand: row l % 32, contraction elements 16 kk + 8 (l / 32) + 0..7
+template <typename G>
+__device__ __forceinline__ Frag<G::P> row_frag(const uint16_t* tile, int kk, int lane) {
   Frag<G::P> f;
 #pragma unroll
   for (int p = 0; p < G::P; ++p)
@@ -147,9 +146,8 @@ __device__ __forceinline__ Frag<kPlanes<T>> row_frag(const uint16_t* tile, int k
 // 16 kb + 4 (l / 32) + {0..3, 8..11}: the rows whose scores the lane holds.  The
 // transpose load hands lane i of a group of 16 the i-th column of the 4 rows x 16
 // columns that the group addresses (4 lanes a row).
-template <typename T, int KS>
-__device__ __forceinline__ Frag<kPlanes<T>> col_frag(const uint16_t* tile, int mt, int kb, int lane) {
-  using G = Tile<T, KS>;
+template <typename G>
+__device__ __forceinline__ Frag<G::P> col_frag(const uint16_t* tile, int mt, int kb, int lane) {
   Frag<G::P> f;
   const int row = 16 * kb + 4 * (lane >> 5) + ((lane & 15) >> 2), col = 32 * mt + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
 #pragma unroll
@@ -163,9 +161,8 @@ __device__ __forceinline__ Frag<kPlanes<T>> col_frag(const uint16_t* tile, int m
 }
 
 // store eight consecutive values into a staged tile
-template <typename T, int KS>
+template <typename G, typename T>
 __device__ __forceinline__ void put(uint16_t* tile, int row, int col8, const Raw<T>& r) {
-  using G = Tile<T, KS>;
   Frag<G::P> f;
   r.frag(f);
 #pragma unroll
@@ -228,7 +225,7 @@ struct Scale {
 
 // LDS bias table of HG heads, [entry][HG][32], in units of S; 32 copies of every value,
 // so that the lanes of a half wave, each with a bucket of its own, read 32 different
-// banks.  The entry after the last bucket masks.
+// banks.
 __device__ __forceinline__ float bias_at(const tp_attn& d, int h, int b) {
   const size_t i = (size_t)h * d.n_buckets + b;
   return d.dtype == TP_F32 ? static_cast<const float*>(d.bias)[i] : (float)static_cast<const bf16_t*>(d.bias)[i];
@@ -236,9 +233,9 @@ __device__ __forceinline__ float bias_at(const tp_attn& d, int h, int b) {
 template <int HG>
 __device__ __forceinline__ void fill_table(const tp_attn& d, float inv, int h0, float* tbl, int threads) {
   const int ne = d.n_buckets > 0 ? d.n_buckets : 1;
-  for (int i = threadIdx.x; i < (ne + 1) * HG * 8; i += threads) {
+  for (int i = threadIdx.x; i < ne * HG * 8; i += threads) {
     const int hh = (i >> 3) % HG, b = (i >> 3) / HG;
-    const float v = b == ne ? -INFINITY : d.n_buckets > 0 ? bias_at(d, h0 + hh, b) * inv : 0.f;
+    const float v = d.n_buckets > 0 ? bias_at(d, h0 + hh, b) * inv : 0.f;
     reinterpret_cast<f4*>(tbl)[i] = f4{v, v, v, v};
   }
 }
@@ -253,7 +250,7 @@ struct Buckets {
   static constexpr int kEntry = HG * 128;
   int shift;
   float lo, hi;
-  uint32_t add, first, masked;             // first: the only entry where there is no bias
+  uint32_t add, first;                     // first: the only entry where there is no bias
   __device__ __forceinline__ Buckets(const tp_attn& d, const float* tbl, int lane) {
     int lg = 0;
     while ((1 << lg) < d.steps) ++lg;
@@ -263,7 +260,6 @@ struct Buckets {
     hi = flt(((uint32_t)(base + nb) << shift) - 1);
     first = lds_address(tbl) + (lane & 31) * 4;
     add = first - base * kEntry;
-    masked = first + nb * kEntry;
   }
   // the squared distance, every operation rounded once (no fused multiply-add).  It is
   // clamped as a float: positive floats are ordered as their representations.
@@ -279,104 +275,121 @@ struct Buckets {
 // table addresses of the 16 tile rows that a lane holds: bucket of (own position, row's
 // position).  pos: LDS [3][32].
 template <int HG>
-__device__ __forceinline__ void tile_entries(const Buckets<HG>& bk, bool biased, const float* pos, int half, float x,
-                                             float y, float z, uint32_t ent[16]) {
-  if (biased) {
+__device__ __forceinline__ void tile_entries(const Buckets<HG>& bk, const float* pos, int half, float x, float y,
+                                             float z, uint32_t ent[16]) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int r = 8 * g + 4 * half;
-      const f4 px = *reinterpret_cast<const f4*>(pos + r), py = *reinterpret_cast<const f4*>(pos + kTile + r),
-               pz = *reinterpret_cast<const f4*>(pos + 2 * kTile + r);
+  for (int g = 0; g < 4; ++g) {
+    const int r = 8 * g + 4 * half;
+    const f4 px = *reinterpret_cast<const f4*>(pos + r), py = *reinterpret_cast<const f4*>(pos + kTile + r),
+             pz = *reinterpret_cast<const f4*>(pos + 2 * kTile + r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ent[4 * g + j] = bk.address(x, y, z, px[j], py[j], pz[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) ent[i] = bk.first;
+    for (int j = 0; j < 4; ++j) ent[4 * g + j] = bk.address(x, y, z, px[j], py[j], pz[j]);
   }
 }
-// tile rows that do not count (bit r of valid clear) to the masking entry
-template <int HG>
-__device__ __forceinline__ void mask_entries(const Buckets<HG>& bk, uint32_t valid, int half, uint32_t ent[16]) {
+// scores of tile rows that do not count (bit r of valid clear)
+__device__ __forceinline__ void mask_scores(uint32_t valid, int half, f16v& s) {
   const uint32_t m = valid >> (4 * half);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ent[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? ent[i] : bk.masked;
+  for (int i = 0; i < 16; ++i) s[i] = (m >> (8 * (i / 4) + i % 4)) & 1 ? s[i] : -INFINITY;
 }
 
-// S of a tile: the bias of every pair, then the product of the staged tile's rows with
-// the wave's own rows
-template <typename T, int KS>
-__device__ __forceinline__ f16v scores(const uint16_t* tile, const Frag<kPlanes<T>> own[KS], const uint32_t ent[16], int hh,
+// S of a tile: the bias of every pair, then the product of the staged rows with the
+// wave's own rows
+template <typename G, int KS>
+__device__ __forceinline__ f16v scores(const uint16_t* tile, const Frag<G::P> own[KS], const uint32_t ent[16], int hh,
                                        int lane) {
   f16v s;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = lds_at(ent[i])[hh * 32];
 #pragma unroll
-  for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<T, KS>(tile, kk, lane), own[kk], s);
+  for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<G>(tile, kk, lane), own[kk], s);
+  return s;
+}
+// the same without a bias
+template <typename G, int KS>
+__device__ __forceinline__ f16v product(const uint16_t* tile, const Frag<G::P> own[KS], int lane) {
+  f16v s;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+  for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<G>(tile, kk, lane), own[kk], s);
   return s;
 }
 
-// Staging of a tile of 32 rows, NS head slots of two arrays each (tile number 2 slot +
-// array), by the NT threads that share it: every thread fetches its 8-value chunks
+// Staging of a tile, NS head slots of two arrays each (array number 2 slot +
+// which), by the NT threads that share it: every thread fetches its 8-value chunks
 // into registers while an earlier tile is worked on, then puts them into LDS.  Rows
 // past the end or masked are staged as zeros.
 template <typename T, int KS, int NT, int NS>
 struct Stager {
   using G = Tile<T, KS>;
-  static constexpr int kTiles = NS * 2;
-  static constexpr int kChunks = (kTiles * kTile * 2 * KS + NT - 1) / NT;
-  static constexpr int kBytes = kTiles * G::kElems * 2;
+  static constexpr int kArrays = NS * 2;
+  static constexpr int kChunks = (kArrays * kTile * 2 * KS + NT - 1) / NT;
+  static constexpr int kBytes = kArrays * G::kElems * 2;
   Raw<T> raw[kChunks];
   bool live[kChunks];
-  const T* at[kChunks];                    // this thread's chunk of the next tile, not read past the end
+  const T* at[kChunks];                    // this thread's chunk of the next tile
+  const T *safe0, *safe1;                  // what is loaded where a chunk does not exist
   int64_t step0, step1;
   int tid;
+  bool whole;                              // every chunk of the tile fetched last exists
 
   __device__ __forceinline__ int chunk(int i) const { return tid + i * NT; }
   static __device__ __forceinline__ int col_of(int c) { return c % (2 * KS); }
   static __device__ __forceinline__ int row_of(int c) { return c / (2 * KS) % kTile; }
-  static __device__ __forceinline__ int tile_of(int c) { return c / (2 * KS * kTile); }
+  static __device__ __forceinline__ int array_of(int c) { return c / (2 * KS * kTile); }
 
-  // the tile of rows r0 .. is next, then every `stride` rows; head(slot): the head of a slot
+  // the tile of rows r0 .. is next, then every `stride` rows, of a structure that starts at
+  // row lo; head(slot): the head of a slot
   template <typename Head>
-  __device__ __forceinline__ void aim(int thread, const void* p0, int64_t s0, const void* p1, int64_t s1, int r0,
+  __device__ __forceinline__ void aim(int thread, const void* p0, int64_t s0, const void* p1, int64_t s1, int lo, int r0,
                                       int stride, int D, Head&& head) {
     tid = thread;
     step0 = s0 * stride;
     step1 = s1 * stride;
+    safe0 = static_cast<const T*>(p0) + lo * s0;
+    safe1 = static_cast<const T*>(p1) + lo * s1;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
-      const int c = chunk(i), t = tile_of(c);
-      const int64_t r = r0 + row_of(c);
-      at[i] = (t & 1 ? static_cast<const T*>(p1) + r * s1 : static_cast<const T*>(p0) + r * s0) +
-              head((t >> 1) % NS) * D + 8 * col_of(c);
+      const int c = chunk(i), t = array_of(c);
+      const int64_t r = r0 + row_of(c) - lo;
+      at[i] = (t & 1 ? safe1 + r * s1 : safe0 + r * s0) + head((t >> 1) % NS) * D + 8 * col_of(c);
     }
   }
   // loads the tile that aim (or the previous fetch) has come to, rows r0 ..
   __device__ __forceinline__ void fetch(int r0, int end, int D, const uint8_t* mask) {
+    constexpr bool kEven = kArrays * kTile * 2 * KS % NT == 0;
+    whole = kEven && end - r0 >= kTile && D == 16 * KS && !mask;
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = chunk(i), t = tile_of(c), r = r0 + row_of(c);
-      live[i] = t < kTiles && r < end && 8 * col_of(c) < D;
-      if (live[i]) {
-        raw[i].load(at[i]);
-        if (mask) live[i] = mask[r] != 0;
+      for (int i = 0; i < kChunks; ++i) raw[i].load(at[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = chunk(i), t = array_of(c), r = r0 + row_of(c);
+        live[i] = t < kArrays && r < end && 8 * col_of(c) < D;
+        raw[i].load(live[i] ? at[i] : t & 1 ? safe1 : safe0);
+        if (mask && live[i]) live[i] = mask[r] != 0;
       }
-      at[i] += t & 1 ? step1 : step0;
     }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) at[i] += array_of(chunk(i)) & 1 ? step1 : step0;
   }
   __device__ __forceinline__ void stage(uint16_t* tiles) {
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) raw[i].keep(live[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int c = chunk(i);
-      raw[i].keep(live[i]);
-      if (tile_of(c) < kTiles) put<T, KS>(tiles + tile_of(c) * G::kElems, row_of(c), col_of(c), raw[i]);
+      if (array_of(c) < kArrays) put<G>(tiles + array_of(c) * G::kElems, row_of(c), col_of(c), raw[i]);
     }
   }
 };
 
 // positions and validity of a tile's rows, one per thread of the first 32 that share it.
-// LDS: [3][32] positions and the validity bits.
+// LDS: [3][32] positions, then the validity bits.
 struct RowStager {
   static constexpr int kBytes = 3 * kTile * 4 + 16;
   float x = 0.f, y = 0.f, z = 0.f;
@@ -393,13 +406,13 @@ struct RowStager {
     }
   }
   __device__ __forceinline__ void stage(int tid, float* lds) const {
-    const uint32_t bits_ = (uint32_t)__ballot(live);
+    const uint32_t vote = (uint32_t)__ballot(live);
     if (tid < kTile) {
       lds[tid] = x;
       lds[kTile + tid] = y;
       lds[2 * kTile + tid] = z;
     }
-    if (tid == 0) *reinterpret_cast<uint32_t*>(lds + 3 * kTile) = bits_;
+    if (tid == 0) *reinterpret_cast<uint32_t*>(lds + 3 * kTile) = vote;
   }
   static __device__ __forceinline__ uint32_t valid(const float* lds) {
     return __builtin_amdgcn_readfirstlane(*reinterpret_cast<const uint32_t*>(lds + 3 * kTile));
@@ -411,10 +424,9 @@ struct RowStager {
 // waves share is staged one tile ahead into the other of two buffers, with one barrier
 // a tile, or, where LDS holds one buffer only, between two barriers.  A wave on its own
 // needs no barrier and one buffer (its LDS accesses are executed in order).  All groups
-// of the workgroup take the same n.
+// of the workgroup take the same n.  The caller has done prepare(0), as early as it can.
 template <bool SHARED, int BUFS, typename Prepare, typename Stage, typename Work>
 __device__ __forceinline__ void walk(int n, Prepare&& prepare, Stage&& stage, Work&& work) {
-  prepare(0);
   if (SHARED && BUFS == 2) {
     stage(0);
     if (n > 1) prepare(1);
@@ -457,26 +469,24 @@ __device__ __forceinline__ void own_rows(const void* p, int64_t stride, int r, i
   }
 }
 
-// a transposed accumulator (lane: own row; registers: head dimension) times `by` to memory
-template <typename T, int MT>
-__device__ __forceinline__ void store_rows(void* p, int64_t stride, int r, int head, int D, int half, const f16v acc[MT],
-                                           float by, bool zero) {
-  T* o = static_cast<T*>(p) + (size_t)r * stride + (size_t)head * D;
+// four values of a row of a transposed accumulator (lane: own row; register 16 mt + 4 g + j:
+// element 32 mt + 8 g + 4 half + j of the head dimension) to memory
+template <typename T>
+__device__ __forceinline__ void store4(void* p, int64_t stride, int r, int head, int D, int half, int mt, int g,
+                                       const float v[4]) {
+  const int e = 32 * mt + 8 * g + 4 * half;
+  if (e < D) {
+    T w[4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int e = 32 * mt + 8 * g + 4 * half;
-      if (e < D) {
-        T v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = (T)(zero ? 0.f : acc[mt][4 * g + j] * by);
-        __builtin_memcpy(__builtin_assume_aligned(o + e, 4 * sizeof(T)), v, sizeof(v));
-      }
-    }
+    for (int j = 0; j < 4; ++j) w[j] = (T)v[j];
+    T* o = static_cast<T*>(p) + (size_t)r * stride + (size_t)head * D + e;
+    __builtin_memcpy(__builtin_assume_aligned(o, 4 * sizeof(T)), w, sizeof(w));
+  }
 }
 
-// accumulators of one wave to LDS, and added to another wave's
+// Accumulators of the waves that split the other side meet in LDS, [wave][part][register]
+// [lane]; each of them then adds up and stores its share of the registers, four at a
+// time.
 template <int MT>
 __device__ __forceinline__ void park(float* at, const f16v acc[MT]) {
 #pragma unroll
@@ -484,12 +494,15 @@ __device__ __forceinline__ void park(float* at, const f16v acc[MT]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) at[64 * (16 * mt + i)] = acc[mt][i];
 }
-template <int MT>
-__device__ __forceinline__ void add_parked(const float* at, float mine, float theirs, f16v acc[MT]) {
+// sum over W waves of factor[w] times register group gi (at: of wave 0, waves `stride` floats apart)
+template <int W>
+__device__ __forceinline__ void sum_parked(const float* at, int stride, int gi, const float* factor, float v[4]) {
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int j = 0; j < 4; ++j) {
+    v[j] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[mt][i] = acc[mt][i] * mine + at[64 * (16 * mt + i)] * theirs;
+    for (int w = 0; w < W; ++w) v[j] = fmaf(at[w * stride + 64 * (4 * gi + j)], factor ? factor[w] : 1.f, v[j]);
+  }
 }
 
 template <int MT>

@@ -13,11 +13,25 @@
 // one word, so plain reads and writes do and the order of the sums is fixed), two
 // elements at a time, summed per workgroup and joined by a second kernel.  An LDS
 // float atomic takes 190 cycles a wave on gfx950; a read, an addition and a write of
-// a pair take 150 cycles of latency that other waves fill.
+// a pair take 150 cycles of latency, which the distances of the next tile fill.
 #include "attn.hpp"
 
 namespace tpc {
 namespace {
+
+// Two sums into words of the lane's own column, which may be the same word: read both, add,
+// write in order (the later of two sums into one word stands).
+struct ColumnPair {
+  lds_f *u, *v;
+  float x, y;
+  bool same;
+  __device__ __forceinline__ ColumnPair(uint32_t a, uint32_t b) : u(lds_at(a)), v(lds_at(b)), x(*u), y(*v), same(a == b) {}
+  __device__ __forceinline__ void add(float a, float b) const {
+    const float s = x + a;
+    *u = s;
+    *v = (same ? s : y) + b;
+  }
+};
 
 template <typename T, int KS, int KV, int QS>
 struct DkvShape {
@@ -26,13 +40,13 @@ struct DkvShape {
   using Stage = Stager<T, KS, 64 * KV, 1>;
   static constexpr int kBuf = Stage::kBytes + RowStager::kBytes + 2 * kTile * 4, kBufs = buffers(kBuf, KV, QS);
   static constexpr int kPart = 2 * G::MT * 16 * 64;                  // floats of one wave to join
-  static constexpr int kJoin = KV * (QS - 1) * kPart * 4;
-  static constexpr int kWork = kBuf * kBufs * QS > kJoin ? kBuf * kBufs * QS : kJoin;
-  static size_t lds_bytes(int nb, bool grad) {
-    const size_t entries = (nb > 0 ? nb : 1) + 1;
-    return kWork + entries * 128 + (grad ? KV * QS * entries * 256 : 0);
+  static constexpr int kJoin = QS > 1 ? KV * QS * kPart * 4 : 0;
+  static constexpr int kWork = kBuf * kBufs * QS;
+  static size_t lds_bytes(int nb) {
+    const size_t walk = kWork + (nb > 0 ? (size_t)nb * (128 + KV * QS * 256) : 128);
+    return walk > kJoin ? walk : kJoin;    // the joined parts take the place of all else
   }
-  static constexpr int kRegs = 2 * KS * G::P * 4 + 2 * G::MT * 16 + 90 + Stage::kChunks * (G::P == 1 ? 6 : 10);
+  static constexpr int kRegs = 2 * KS * G::P * 4 + 2 * G::MT * 16 + 124 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
 template <typename T, int KS, int KV, int QS>
@@ -44,7 +58,7 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
   extern __shared__ __attribute__((aligned(16))) char lds[];
   float* tbl = reinterpret_cast<float*>(lds + S::kWork);
   const tp_attn& d = a.d;
-  const int nb = d.n_buckets, ne = (nb > 0 ? nb : 1) + 1;
+  const int nb = d.n_buckets, ne = nb > 0 ? nb : 1;
   float* cols = tbl + ne * 32;             // [NW][ne][64] bias gradient columns
   const int rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
   // query heads h_lo .. h_hi - 1 of key head g
@@ -69,7 +83,7 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
   const bool some_dead = __any(!live);
   // table address -> address of the lane's column of the same entry (twice as wide)
   float* my_cols = cols + (size_t)wv * ne * 64;
-  const uint32_t col = lds_address(my_cols) + 4 * lane - 2 * bk.first;
+  const uint32_t col = lds_address(my_cols) + 4 * lane - 2 * bk.first, col0 = lds_address(my_cols) + 4 * lane;
   float x = 0.f, y = 0.f, z = 0.f;
   if (biased) {
     x = d.pos[3 * (size_t)kc];
@@ -91,25 +105,39 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
   const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
   const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
   const auto stat_of = [&](int buf) { return rows_of(buf) + RowStager::kBytes / 4; };   // [2][32]: lse (base 2), delta
-  const int q_first = lo + 32 * qs, n = (hi - lo + 32 * QS - 1) / (32 * QS);
-  for (int h = h_lo; h < h_hi; ++h) {
+  const int q_first = lo + kTile * qs, step = kTile * QS, n = (hi - lo + step - 1) / step;
+  // table addresses of the present tile; ds and column addresses of the previous one, which
+  // wait to be added to the columns
+  uint32_t ent[16], due[16];
+  float ds[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ent[i] = bk.first;
+  int h = h_lo;
+  const auto prepare = [&](int i) {
+    const int q0 = q_first + i * step;
+    st.fetch(q0, hi, D, nullptr);
+    rows.fetch(tid, d, biased, q0, hi, nullptr);
+    if (tid < kTile) {
+      const size_t at = (size_t)h * d.n_nodes + min(q0 + tid, hi - 1);
+      const float e = a.lse_in[at];
+      // rows past the end or without keys: p = exp2(s - inf) = 0
+      slse = q0 + tid < hi && e != -INFINITY ? e * kLog2e : INFINITY;
+      sdel = q0 + tid < hi ? a.delta[at] : 0.f;
+    }
+  };
+  for (; h < h_hi; ++h) {
     if (h > h_lo) __syncthreads();         // the previous head's table and columns have been read
+    st.aim(tid, a.q, a.qs, a.go, a.gos, lo, q_first, step, D, [&](int) { return h; });
+    prepare(0);
     fill_table<1>(d, scale.inv, h, tbl, S::kThreads);
-    if (a.gbias)
+    if (biased) {
       for (int i = lane; i < ne * 16; i += 64) reinterpret_cast<f4*>(my_cols)[i] = f4{0.f, 0.f, 0.f, 0.f};
-    st.aim(tid, a.q, a.qs, a.go, a.gos, q_first, 32 * QS, D, [&](int) { return h; });
-    const auto prepare = [&](int i) {
-      const int q0 = q_first + i * 32 * QS;
-      st.fetch(q0, hi, D, nullptr);
-      rows.fetch(tid, d, biased, q0, hi, nullptr);
-      if (tid < kTile) {
-        const size_t at = (size_t)h * d.n_nodes + min(q0 + tid, hi - 1);
-        const float e = a.lse_in[at];
-        // rows past the end or without keys: p = exp2(s - inf) = 0
-        slse = q0 + tid < hi && e != -INFINITY ? e * kLog2e : INFINITY;
-        sdel = q0 + tid < hi ? a.delta[at] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        due[i] = col0;
+        ds[i] = 0.f;
       }
-    };
+    }
     const auto stage = [&](int buf) {
       st.stage(tiles_of(buf));
       rows.stage(tid, rows_of(buf));
@@ -120,35 +148,40 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
     };
     __syncthreads();                       // the table
     walk<(KV > 1), S::kBufs>(n, prepare, stage, [&](int buf) {
-      if (RowStager::valid(rows_of(buf)) == 0) return;   // past the end
-      uint32_t ent[16];
-      tile_entries<1>(bk, biased, rows_of(buf), half, x, y, z, ent);
-      if (some_dead) mask_entries<1>(bk, live ? 0xffffffffu : 0u, half, ent);
-      const uint16_t* qt = tiles_of(buf);
-      const f16v s = scores<T, KS>(qt, K, ent, 0, lane);
-      f16v dp;
-      clear<1>(&dp);
+      const float *pos = rows_of(buf), *stat = stat_of(buf);
+      if (RowStager::valid(pos) == 0) return;     // past the end
+      if (biased) {
+        // the latency of the column sums is filled with the distances of this tile
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) dp = mma(row_frag<T, KS>(qt + G::kElems, kk, lane), V[kk], dp);
-      float p[16], ds[16];
+        for (int j = 0; j < 4; ++j) {
+          const int r = 8 * j + 4 * half;
+          const f4 px = *reinterpret_cast<const f4*>(pos + r), py = *reinterpret_cast<const f4*>(pos + kTile + r),
+                   pz = *reinterpret_cast<const f4*>(pos + 2 * kTile + r);
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int i = 4 * j + e;
+            const ColumnPair u(due[i], due[i + 1]);
+            ent[i] = bk.address(x, y, z, px[e], py[e], pz[e]);
+            ent[i + 1] = bk.address(x, y, z, px[e + 1], py[e + 1], pz[e + 1]);
+            u.add(ds[i], ds[i + 1]);
+            due[i] = 2 * ent[i] + col;
+            due[i + 1] = 2 * ent[i + 1] + col;
+          }
+        }
+      }
+      const uint16_t* qt = tiles_of(buf);
+      f16v s = scores<G, KS>(qt, K, ent, 0, lane);
+      const f16v dp = product<G, KS>(qt + G::kElems, V, lane);
+      if (some_dead) mask_scores(live ? 0xffffffffu : 0u, half, s);   // p = 0: nothing for the bias
+      float p[16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = 8 * j + 4 * half;
-        const f4 le = *reinterpret_cast<const f4*>(stat_of(buf) + r);
-        const f4 de = *reinterpret_cast<const f4*>(stat_of(buf) + kTile + r);
+        const f4 le = *reinterpret_cast<const f4*>(stat + r), de = *reinterpret_cast<const f4*>(stat + kTile + r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           p[4 * j + e] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + e], scale.c, -le[e]));
           ds[4 * j + e] = p[4 * j + e] * (dp[4 * j + e] - de[e]);
-        }
-      }
-      if (a.gbias) {
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          lds_f *u = lds_at(2 * ent[e] + col), *v = lds_at(2 * ent[e + 1] + col);
-          const float x0 = *u, x1 = *v, y0 = x0 + ds[e], y1 = (ent[e] == ent[e + 1] ? y0 : x1) + ds[e + 1];
-          *u = y0;
-          *v = y1;                         // the later of two sums into one word stands
         }
       }
 #pragma unroll
@@ -158,11 +191,15 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
         to_frag(ds + 8 * kb, df);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          dV[mt] = mma(col_frag<T, KS>(qt + G::kElems, mt, kb, lane), pf, dV[mt]);
-          dK[mt] = mma(col_frag<T, KS>(qt, mt, kb, lane), df, dK[mt]);
+          dV[mt] = mma(col_frag<G>(qt + G::kElems, mt, kb, lane), pf, dV[mt]);
+          dK[mt] = mma(col_frag<G>(qt, mt, kb, lane), df, dK[mt]);
         }
       }
     });
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) ColumnPair(due[i], due[i + 1]).add(ds[i], ds[i + 1]);
+    }
     if (a.gbias) {
       // an entry's 64 columns of every wave, 16 bytes at a time; lanes start at different
       // columns so that they read different banks
@@ -182,29 +219,40 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
     }
   }
 
+  float* join = reinterpret_cast<float*>(lds) + (size_t)kv * QS * S::kPart + lane;
   if (QS > 1) {
-    float* join = reinterpret_cast<float*>(lds) + (size_t)kv * (QS - 1) * S::kPart + lane;
     __syncthreads();
-    if (qs > 0) {
-      park<MT>(join + (qs - 1) * S::kPart, dK);
-      park<MT>(join + (qs - 1) * S::kPart + S::kPart / 2, dV);
-    }
+    park<MT>(join + qs * S::kPart, dK);
+    park<MT>(join + qs * S::kPart + S::kPart / 2, dV);
     __syncthreads();
-    if (qs > 0) return;
-    for (int o = 0; o < QS - 1; ++o) {
-      add_parked<MT>(join + o * S::kPart, 1.f, 1.f, dK);
-      add_parked<MT>(join + o * S::kPart + S::kPart / 2, 1.f, 1.f, dV);
-    }
   }
-  if (k < hi) {
-    if (a.split) {
-      // [n_nodes][n_heads][2][D]
-      float* o = a.kv_part + ((size_t)k * d.n_heads + h_lo) * 2 * D;
-      store_rows<float, MT>(o, 0, 0, 0, D, half, dK, d.scale, !live);
-      store_rows<float, MT>(o, 0, 0, 1, D, half, dV, 1.f, !live);
-    } else {
-      store_rows<T, MT>(a.gk, a.gks, k, g, D, half, dK, d.scale, !live);
-      store_rows<T, MT>(a.gv, a.gvs, k, g, D, half, dV, 1.f, !live);
+  if (k >= hi) return;
+  // gi: register groups of dK, then of dV
+  const auto store = [&](int gi, float v[4]) {
+    const bool is_v = gi >= 4 * MT;
+    const int e = is_v ? gi - 4 * MT : gi;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = live ? (is_v ? v[j] : v[j] * d.scale) : 0.f;
+    if (a.split)                           // [n_nodes][n_heads][2][D]
+      store4<float>(a.kv_part, (int64_t)d.n_heads * 2 * D, k, 2 * h_lo + is_v, D, half, e / 4, e % 4, v);
+    else if (is_v)
+      store4<T>(a.gv, a.gvs, k, g, D, half, e / 4, e % 4, v);
+    else
+      store4<T>(a.gk, a.gks, k, g, D, half, e / 4, e % 4, v);
+  };
+  if (QS > 1) {
+    for (int gi = qs; gi < 8 * MT; gi += QS) {
+      float v[4];
+      sum_parked<QS>(join, S::kPart, gi, nullptr, v);
+      store(gi, v);
+    }
+  } else {
+#pragma unroll
+    for (int gi = 0; gi < 8 * MT; ++gi) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = (gi < 4 * MT ? dK : dV)[gi / 4 % MT][gi % 4 * 4 + j];
+      store(gi, v);
     }
   }
 }
@@ -266,7 +314,7 @@ hipError_t launch(const AttnArgs& a) {
   using S = DkvShape<T, KS, KV, QS>;
   const int tiles = a.d.n_nodes / (kTile * KV) + a.d.n_segments;
   hipError_t e = launch_lds(k_attn_dkv<T, KS, KV, QS>, dim3(tiles, a.split ? a.d.n_heads : a.d.n_kv_heads), S::kThreads,
-                            S::lds_bytes(a.d.n_buckets, a.gbias != nullptr), a.stream, a);
+                            S::lds_bytes(a.d.n_buckets), a.stream, a);
   if (e != hipSuccess) return e;
   if (a.split) {
     const int64_t n = (int64_t)a.d.n_nodes * a.d.n_kv_heads * 2 * (a.d.head_dim / 4);
@@ -284,12 +332,11 @@ template <typename T, int KS>
 hipError_t by_waves(const AttnArgs& a) {
   const Extent x(a.d, a.split ? a.d.n_heads : a.d.n_kv_heads);
   const int nb = a.d.n_buckets;
-  const bool grad = a.gbias != nullptr;
   if (x.mean <= kTile) return launch<T, KS, 1, 1>(a);
   if (x.mean < 1024 && x.units >= 1024) return launch<T, KS, 2, 1>(a);
-  if (x.units >= 1024 && DkvShape<T, KS, 4, 2>::lds_bytes(nb, grad) <= kLdsMax) return launch<T, KS, 4, 2>(a);
-  if (x.units < 1024 && DkvShape<T, KS, 2, 4>::lds_bytes(nb, grad) <= kLdsMax) return launch<T, KS, 2, 4>(a);
-  if (DkvShape<T, KS, 2, 2>::lds_bytes(nb, grad) <= kLdsMax) return launch<T, KS, 2, 2>(a);
+  if (x.units >= 1024 && DkvShape<T, KS, 4, 2>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 4, 2>(a);
+  if (x.units < 1024 && DkvShape<T, KS, 2, 4>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 2, 4>(a);
+  if (DkvShape<T, KS, 2, 2>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 2, 2>(a);
   return launch<T, KS, 2, 1>(a);
 }
 

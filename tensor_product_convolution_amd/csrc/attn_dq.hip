@@ -22,9 +22,12 @@ struct DqShape {
   using Stage = Stager<T, KS, 64 * QW, NKV>;
   static constexpr int kBuf = Stage::kBytes + RowStager::kBytes, kBufs = buffers(kBuf, QW, KW);
   static constexpr int kPart = (G::MT * 16 + 1) * 64;
-  static constexpr int kJoin = QW * (KW - 1) * HG * kPart * 4;
-  static constexpr int kWork = kBuf * kBufs * KW > kJoin ? kBuf * kBufs * KW : kJoin;
-  static size_t lds_bytes(int nb) { return kWork + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128; }
+  static constexpr int kJoin = KW > 1 ? QW * KW * HG * kPart * 4 : 0;
+  static constexpr int kWork = kBuf * kBufs * KW;
+  static size_t lds_bytes(int nb) {
+    const size_t walk = kWork + (size_t)(nb > 0 ? nb : 1) * HG * 128;
+    return walk > kJoin ? walk : kJoin;    // the joined parts take the place of all else
+  }
   static constexpr int kRegs = HG * (2 * KS * G::P * 4 + G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
@@ -44,6 +47,20 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
   const int kw = wv % KW, qw = wv / KW;
   const int rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
   const bool biased = d.n_buckets > 0;
+  typename S::Stage st;
+  RowStager rows;
+  const int tid = qw * 64 + lane;          // among the threads that share a tile
+  char* mine = lds + kw * S::kBufs * S::kBuf;
+  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
+  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
+  const int k_first = lo + kTile * kw, step = kTile * KW;
+  st.aim(tid, a.k, a.ks, a.v, a.vs, lo, k_first, step, D, [&](int slot) { return (h0 + slot) / rep; });
+  const auto prepare = [&](int i) {
+    st.fetch(k_first + i * step, hi, D, d.key_mask);
+    rows.fetch(tid, d, biased, k_first + i * step, hi, d.key_mask);
+  };
+  prepare(0);
+
   const Scale scale(d.scale);
   fill_table<HG>(d, scale.inv, h0, tbl, S::kThreads);
   const Buckets<HG> bk(d, tbl, lane);
@@ -88,37 +105,25 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     clear<MT>(dQ[hh]);
   }
 
-  typename S::Stage st;
-  RowStager rows;
-  const int tid = qw * 64 + lane;          // among the threads that share a tile
-  char* mine = lds + kw * S::kBufs * S::kBuf;
-  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
-  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
-  const int k_first = lo + 32 * kw;
-  st.aim(tid, a.k, a.ks, a.v, a.vs, k_first, 32 * KW, D, [&](int slot) { return (h0 + slot) / rep; });
-  const auto prepare = [&](int i) {
-    st.fetch(k_first + i * 32 * KW, hi, D, d.key_mask);
-    rows.fetch(tid, d, biased, k_first + i * 32 * KW, hi, d.key_mask);
-  };
   const auto stage = [&](int buf) {
     st.stage(tiles_of(buf));
     rows.stage(tid, rows_of(buf));
   };
   __syncthreads();                         // the table
-  walk<(QW > 1), S::kBufs>((hi - lo + 32 * KW - 1) / (32 * KW), prepare, stage, [&](int buf) {
-    const uint32_t vm = RowStager::valid(rows_of(buf));
+  uint32_t ent[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ent[i] = bk.first;
+  walk<(QW > 1), S::kBufs>((hi - lo + step - 1) / step, prepare, stage, [&](int buf) {
+    const float* pos = rows_of(buf);
+    const uint32_t vm = RowStager::valid(pos);
     if (vm == 0) return;                   // past the end, or all masked
-    uint32_t ent[16];
-    tile_entries<HG>(bk, biased, rows_of(buf), half, x, y, z, ent);
-    if (vm != 0xffffffffu) mask_entries<HG>(bk, vm, half, ent);
+    if (biased) tile_entries<HG>(bk, pos, half, x, y, z, ent);
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
       const uint16_t* kt = tiles_of(buf) + (NKV == 1 ? 0 : hh * 2) * G::kElems;
-      const f16v s = scores<T, KS>(kt, Q[hh], ent, hh, lane);
-      f16v dp;
-      clear<1>(&dp);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) dp = mma(row_frag<T, KS>(kt + G::kElems, kk, lane), dO[hh][kk], dp);
+      f16v s = scores<G, KS>(kt, Q[hh], ent, hh, lane);
+      const f16v dp = product<G, KS>(kt + G::kElems, dO[hh], lane);
+      if (vm != 0xffffffffu) mask_scores(vm, half, s);
       float ds[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -131,38 +136,52 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
         Frag<P> f;
         to_frag(ds + 8 * kb, f);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) dQ[hh][mt] = mma(col_frag<T, KS>(kt, mt, kb, lane), f, dQ[hh][mt]);
+        for (int mt = 0; mt < MT; ++mt) dQ[hh][mt] = mma(col_frag<G>(kt, mt, kb, lane), f, dQ[hh][mt]);
       }
     }
   });
 
+  float* join = reinterpret_cast<float*>(lds) + (size_t)qw * KW * HG * S::kPart + lane;
   if (KW > 1) {
-    float* join = reinterpret_cast<float*>(lds) + (size_t)qw * (KW - 1) * HG * S::kPart + lane;
     __syncthreads();
-    if (kw > 0) {
 #pragma unroll
-      for (int hh = 0; hh < HG; ++hh) {
-        float* w = join + ((kw - 1) * HG + hh) * S::kPart;
-        w[0] = r[hh];
-        park<MT>(w + 64, dQ[hh]);
-      }
+    for (int hh = 0; hh < HG; ++hh) {
+      float* w = join + (kw * HG + hh) * S::kPart;
+      w[0] = pair_sum(r[hh]);
+      park<MT>(w + 64, dQ[hh]);
     }
     __syncthreads();
-    if (kw > 0) return;
-#pragma unroll
-    for (int hh = 0; hh < HG; ++hh)
-      for (int o = 0; o < KW - 1; ++o) {
-        const float* w = join + (o * HG + hh) * S::kPart;
-        r[hh] += w[0];
-        add_parked<MT>(w + 64, 1.f, 1.f, dQ[hh]);
-      }
   }
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
-    const float sum = pair_sum(r[hh]);
-    if (q < hi) {
-      if (half == 0) a.delta[(size_t)(h0 + hh) * d.n_nodes + q] = delta[hh] + sum;
-      store_rows<T, MT>(a.gq, a.gqs, q, h0 + hh, D, half, dQ[hh], d.scale, false);
+    float sum = 0.f;
+    if (KW > 1) {
+#pragma unroll
+      for (int w = 0; w < KW; ++w) sum += join[(w * HG + hh) * S::kPart];
+    } else {
+      sum = pair_sum(r[hh]);
+    }
+    if (q < hi && half == 0 && kw == 0) a.delta[(size_t)(h0 + hh) * d.n_nodes + q] = delta[hh] + sum;
+  }
+  if (q >= hi) return;
+#pragma unroll
+  for (int hh = 0; hh < HG; ++hh) {
+    if (KW > 1) {
+      for (int gi = (kw + hh * 4 * MT) % KW; gi < 4 * MT; gi += KW) {
+        float v[4];
+        sum_parked<KW>(join + hh * S::kPart + 64, HG * S::kPart, gi, nullptr, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= d.scale;
+        store4<T>(a.gq, a.gqs, q, h0 + hh, D, half, gi / 4, gi % 4, v);
+      }
+    } else {
+#pragma unroll
+      for (int gi = 0; gi < 4 * MT; ++gi) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = dQ[hh][gi / 4][gi % 4 * 4 + j] * d.scale;
+        store4<T>(a.gq, a.gqs, q, h0 + hh, D, half, gi / 4, gi % 4, v);
+      }
     }
   }
 }

@@ -16,9 +16,12 @@ struct FwdShape {
   using Stage = Stager<T, KS, 64 * QW, NKV>;
   static constexpr int kBuf = Stage::kBytes + RowStager::kBytes, kBufs = buffers(kBuf, QW, KW);
   static constexpr int kPart = (G::MT * 16 + 2) * 64;                // floats of one wave's head to join
-  static constexpr int kJoin = QW * (KW - 1) * HG * kPart * 4;
-  static constexpr int kWork = kBuf * kBufs * KW > kJoin ? kBuf * kBufs * KW : kJoin;
-  static size_t lds_bytes(int nb) { return kWork + (size_t)((nb > 0 ? nb : 1) + 1) * HG * 128; }
+  static constexpr int kJoin = KW > 1 ? QW * KW * HG * kPart * 4 : 0;
+  static constexpr int kWork = kBuf * kBufs * KW;
+  static size_t lds_bytes(int nb) {
+    const size_t walk = kWork + (size_t)(nb > 0 ? nb : 1) * HG * 128;
+    return walk > kJoin ? walk : kJoin;    // the joined parts take the place of all else
+  }
   // operands, accumulators and scores beside what the fetch holds
   static constexpr int kRegs = HG * (KS * G::P * 4 + G::MT * 16 + 16) + 60 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
@@ -38,6 +41,20 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   const int kw = wv % KW, qw = wv / KW;
   const int h0 = blockIdx.y * HG, rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
   const bool biased = d.n_buckets > 0;
+  typename S::Stage st;
+  RowStager rows;
+  const int tid = qw * 64 + lane;          // among the threads that share a tile
+  char* mine = lds + kw * S::kBufs * S::kBuf;
+  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
+  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
+  const int k_first = lo + kTile * kw, step = kTile * KW;
+  st.aim(tid, a.k, a.ks, a.v, a.vs, lo, k_first, step, D, [&](int slot) { return (h0 + slot) / rep; });
+  const auto prepare = [&](int i) {
+    st.fetch(k_first + i * step, hi, D, d.key_mask);
+    rows.fetch(tid, d, biased, k_first + i * step, hi, d.key_mask);
+  };
+  prepare(0);
+
   const Scale scale(d.scale);
   fill_table<HG>(d, scale.inv, h0, tbl, S::kThreads);
   const Buckets<HG> bk(d, tbl, lane);
@@ -63,43 +80,41 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
     clear<MT>(O[hh]);
   }
 
-  typename S::Stage st;
-  RowStager rows;
-  const int tid = qw * 64 + lane;          // among the threads that share a tile
-  char* mine = lds + kw * S::kBufs * S::kBuf;
-  const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
-  const auto rows_of = [&](int buf) { return reinterpret_cast<float*>(mine + buf * S::kBuf + S::Stage::kBytes); };
-  const int k_first = lo + 32 * kw;
-  st.aim(tid, a.k, a.ks, a.v, a.vs, k_first, 32 * KW, D, [&](int slot) { return (h0 + slot) / rep; });
-  const auto prepare = [&](int i) {
-    st.fetch(k_first + i * 32 * KW, hi, D, d.key_mask);
-    rows.fetch(tid, d, biased, k_first + i * 32 * KW, hi, d.key_mask);
-  };
   const auto stage = [&](int buf) {
     st.stage(tiles_of(buf));
     rows.stage(tid, rows_of(buf));
   };
   __syncthreads();                         // the table
-  walk<(QW > 1), S::kBufs>((hi - lo + 32 * KW - 1) / (32 * KW), prepare, stage, [&](int buf) {
-    const uint32_t vm = RowStager::valid(rows_of(buf));
+  uint32_t ent[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) ent[i] = bk.first;
+  walk<(QW > 1), S::kBufs>((hi - lo + step - 1) / step, prepare, stage, [&](int buf) {
+    const float* pos = rows_of(buf);
+    const uint32_t vm = RowStager::valid(pos);
     if (vm == 0) return;                   // past the end, or all masked
-    uint32_t ent[16];
-    tile_entries<HG>(bk, biased, rows_of(buf), half, x, y, z, ent);
-    if (vm != 0xffffffffu) mask_entries<HG>(bk, vm, half, ent);
+    if (biased) tile_entries<HG>(bk, pos, half, x, y, z, ent);
     // every head's scores first: a head's products run while another's softmax does
     const uint16_t* kt = tiles_of(buf);
     f16v sc[HG];
 #pragma unroll
-    for (int hh = 0; hh < HG; ++hh) sc[hh] = scores<T, KS>(kt + (NKV == 1 ? 0 : hh * 2) * G::kElems, Q[hh], ent, hh, lane);
+    for (int hh = 0; hh < HG; ++hh) sc[hh] = scores<G, KS>(kt + (NKV == 1 ? 0 : hh * 2) * G::kElems, Q[hh], ent, hh, lane);
+    if (vm != 0xffffffffu) {
+#pragma unroll
+      for (int hh = 0; hh < HG; ++hh) mask_scores(vm, half, sc[hh]);
+    }
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
       const uint16_t* vt = kt + (NKV == 1 ? 1 : hh * 2 + 1) * G::kElems;
-      float p[16], sum = 0.f;
+      float p[16], sum;
+      const auto exponentials = [&]() {
+        sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -m[hh]));
-        sum += p[i];
-      }
+        for (int i = 0; i < 16; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -m[hh]));
+          sum += p[i];
+        }
+      };
+      exponentials();
       // The running maximum is raised when the tile's sum shows that it has been passed by
       // far: probabilities up to 2^9 lose nothing, most tiles need no maximum at all, and
       // the accumulators are rescaled in few.  NaN takes this way in every tile.
@@ -114,12 +129,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) O[hh][mt][i] *= f;
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -mn));
-          sum += p[i];
-        }
+        exponentials();
       }
       l[hh] += sum;
 #pragma unroll
@@ -127,44 +137,65 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
         Frag<P> pf;
         to_frag(p + 8 * kb, pf);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) O[hh][mt] = mma(col_frag<T, KS>(vt, mt, kb, lane), pf, O[hh][mt]);
+        for (int mt = 0; mt < MT; ++mt) O[hh][mt] = mma(col_frag<G>(vt, mt, kb, lane), pf, O[hh][mt]);
       }
     }
   });
 
+  // statistics of the row over all waves that share it
+  float factor[HG][KW], sum[HG];
+  float* join = reinterpret_cast<float*>(lds) + (size_t)qw * KW * HG * S::kPart + lane;
   if (KW > 1) {
-    float* join = reinterpret_cast<float*>(lds) + (size_t)qw * (KW - 1) * HG * S::kPart + lane;
     __syncthreads();
-    if (kw > 0) {
 #pragma unroll
-      for (int hh = 0; hh < HG; ++hh) {
-        float* w = join + ((kw - 1) * HG + hh) * S::kPart;
-        w[0] = m[hh];
-        w[64] = l[hh];
-        park<MT>(w + 128, O[hh]);
-      }
+    for (int hh = 0; hh < HG; ++hh) {
+      float* w = join + (kw * HG + hh) * S::kPart;
+      w[0] = m[hh];
+      w[64] = pair_sum(l[hh]);
+      park<MT>(w + 128, O[hh]);
     }
     __syncthreads();
-    if (kw > 0) return;
-#pragma unroll
-    for (int hh = 0; hh < HG; ++hh)
-      for (int o = 0; o < KW - 1; ++o) {
-        const float* w = join + (o * HG + hh) * S::kPart;
-        const float mn = fmaxf(m[hh], w[0]);
-        const float f = __builtin_amdgcn_exp2f(m[hh] - mn), g = __builtin_amdgcn_exp2f(w[0] - mn);
-        m[hh] = mn;
-        l[hh] = l[hh] * f + w[64] * g;
-        add_parked<MT>(w + 128, f, g, O[hh]);
-      }
   }
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
-    const float sum = pair_sum(l[hh]);
-    if (q < hi) {
-      const bool none = sum == 0.f;        // NaN is not none: it has to show
-      if (a.lse && half == 0)
-        a.lse[(size_t)(h0 + hh) * d.n_nodes + q] = none ? -INFINITY : (m[hh] + __builtin_amdgcn_logf(sum)) * kLn2;
-      store_rows<T, MT>(a.out, a.os, q, h0 + hh, D, half, O[hh], 1.f / sum, none);
+    if (KW > 1) {
+#pragma unroll
+      for (int w = 0; w < KW; ++w) m[hh] = fmaxf(m[hh], join[(w * HG + hh) * S::kPart]);
+      sum[hh] = 0.f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        factor[hh][w] = __builtin_amdgcn_exp2f(join[(w * HG + hh) * S::kPart] - m[hh]);
+        sum[hh] = fmaf(join[(w * HG + hh) * S::kPart + 64], factor[hh][w], sum[hh]);
+      }
+    } else {
+      sum[hh] = pair_sum(l[hh]);
+    }
+  }
+  if (q >= hi) return;
+#pragma unroll
+  for (int hh = 0; hh < HG; ++hh) {
+    const bool none = sum[hh] == 0.f;      // NaN is not none: it has to show
+    const float inv = 1.f / sum[hh];
+    if (a.lse && half == 0 && kw == 0)
+      a.lse[(size_t)(h0 + hh) * d.n_nodes + q] = none ? -INFINITY : (m[hh] + __builtin_amdgcn_logf(sum[hh])) * kLn2;
+    const auto store = [&](int gi, float v[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = none ? 0.f : v[j] * inv;
+      store4<T>(a.out, a.os, q, h0 + hh, D, half, gi / 4, gi % 4, v);
+    };
+    if (KW > 1) {
+      for (int gi = (kw + hh * 4 * MT) % KW; gi < 4 * MT; gi += KW) {
+        float v[4];
+        sum_parked<KW>(join + hh * S::kPart + 128, HG * S::kPart, gi, factor[hh], v);
+        store(gi, v);
+      }
+    } else {
+#pragma unroll
+      for (int gi = 0; gi < 4 * MT; ++gi) {
+        float v[4] = {O[hh][gi / 4][gi % 4 * 4], O[hh][gi / 4][gi % 4 * 4 + 1], O[hh][gi / 4][gi % 4 * 4 + 2],
+                      O[hh][gi / 4][gi % 4 * 4 + 3]};
+        store(gi, v);
+      }
     }
   }
 }
