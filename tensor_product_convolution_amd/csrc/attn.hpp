@@ -328,6 +328,7 @@ struct Stager {
   static constexpr int kBytes = kArrays * G::kElems * 2;
   Raw<T> raw[kChunks];
   bool live[kChunks];
+  uint8_t byte[kChunks];                   // the mask's
   const T* at[kChunks];                    // this thread's chunk of the next tile
   const T *safe0, *safe1;                  // what is loaded where a chunk does not exist
   int64_t step0, step1;
@@ -360,25 +361,28 @@ struct Stager {
   __device__ __forceinline__ void fetch(int r0, int end, int D, const uint8_t* mask) {
     constexpr bool kEven = kArrays * kTile * 2 * KS % NT == 0;
     whole = kEven && end - r0 >= kTile && D == 16 * KS && !mask;
-    if (whole) {
+    const T* p[kChunks];
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) raw[i].load(at[i]);
-    } else {
+    for (int i = 0; i < kChunks; ++i) p[i] = at[i];
+    if (!whole) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = chunk(i), t = array_of(c), r = r0 + row_of(c);
         live[i] = t < kArrays && r < end && 8 * col_of(c) < D;
-        raw[i].load(live[i] ? at[i] : t & 1 ? safe1 : safe0);
-        if (mask && live[i]) live[i] = mask[r] != 0;
+        if (!live[i]) p[i] = t & 1 ? safe1 : safe0;
+        byte[i] = mask ? mask[r < end ? r : end - 1] : 1;
       }
     }
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) at[i] += array_of(chunk(i)) & 1 ? step1 : step0;
+    for (int i = 0; i < kChunks; ++i) {
+      raw[i].load(p[i]);
+      at[i] += array_of(chunk(i)) & 1 ? step1 : step0;
+    }
   }
   __device__ __forceinline__ void stage(uint16_t* tiles) {
     if (!whole) {
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) raw[i].keep(live[i]);
+      for (int i = 0; i < kChunks; ++i) raw[i].keep(live[i] && byte[i] != 0);
     }
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -394,10 +398,12 @@ struct RowStager {
   static constexpr int kBytes = 3 * kTile * 4 + 16;
   float x = 0.f, y = 0.f, z = 0.f;
   bool live = false;
+  uint8_t byte = 1;                        // the mask's
   __device__ __forceinline__ void fetch(int tid, const tp_attn& d, bool biased, int r0, int end, const uint8_t* mask) {
     if (tid < kTile) {
       const int r = r0 + tid, rc = r < end ? r : end - 1;
-      live = r < end && (!mask || mask[rc] != 0);
+      live = r < end;
+      if (mask) byte = mask[rc];
       if (biased) {
         x = d.pos[3 * (size_t)rc];
         y = d.pos[3 * (size_t)rc + 1];
@@ -406,7 +412,7 @@ struct RowStager {
     }
   }
   __device__ __forceinline__ void stage(int tid, float* lds) const {
-    const uint32_t vote = (uint32_t)__ballot(live);
+    const uint32_t vote = (uint32_t)__ballot(live && byte != 0);
     if (tid < kTile) {
       lds[tid] = x;
       lds[kTile + tid] = y;
