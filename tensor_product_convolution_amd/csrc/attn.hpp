@@ -57,16 +57,21 @@ struct Frag {
   b8 p[P];
 };
 
+template <bool SWAPPED = false>
 __device__ __forceinline__ f16v mma(const Frag<1>& a, const Frag<1>& b, f16v c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
 }
-// smallest partial products first
+// Smallest partial products first.  SWAPPED takes the same products in the same order with
+// the operands exchanged, so that the key side of the backward forms bit for bit the
+// scores of the query side: its row sums then cancel.
+template <bool SWAPPED = false>
 __device__ __forceinline__ f16v mma(const Frag<3>& a, const Frag<3>& b, f16v c) {
-  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[2], c, 0, 0, 0);
-  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2], b.p[0], c, 0, 0, 0);
+  constexpr int f = SWAPPED ? 2 : 0, g = SWAPPED ? 1 : 0;
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[f], b.p[2 - f], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[2 - f], b.p[f], c, 0, 0, 0);
   c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[1], c, 0, 0, 0);
-  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[1], c, 0, 0, 0);
-  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1], b.p[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[g], b.p[1 - g], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[1 - g], b.p[g], c, 0, 0, 0);
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.p[0], b.p[0], c, 0, 0, 0);
 }
 
@@ -295,24 +300,24 @@ __device__ __forceinline__ void mask_scores(uint32_t valid, int half, f16v& s) {
 
 // S of a tile: the bias of every pair, then the product of the staged rows with the
 // wave's own rows
-template <typename G, int KS>
+template <typename G, int KS, bool SWAPPED = false>
 __device__ __forceinline__ f16v scores(const uint16_t* tile, const Frag<G::P> own[KS], const uint32_t ent[16], int hh,
                                        int lane) {
   f16v s;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = lds_at(ent[i])[hh * 32];
 #pragma unroll
-  for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<G>(tile, kk, lane), own[kk], s);
+  for (int kk = 0; kk < KS; ++kk) s = mma<SWAPPED>(row_frag<G>(tile, kk, lane), own[kk], s);
   return s;
 }
 // the same without a bias
-template <typename G, int KS>
+template <typename G, int KS, bool SWAPPED = false>
 __device__ __forceinline__ f16v product(const uint16_t* tile, const Frag<G::P> own[KS], int lane) {
   f16v s;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = 0.f;
 #pragma unroll
-  for (int kk = 0; kk < KS; ++kk) s = mma(row_frag<G>(tile, kk, lane), own[kk], s);
+  for (int kk = 0; kk < KS; ++kk) s = mma<SWAPPED>(row_frag<G>(tile, kk, lane), own[kk], s);
   return s;
 }
 

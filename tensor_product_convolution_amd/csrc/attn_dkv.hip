@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
         }
       }
       const uint16_t* qt = tiles_of(buf);
-      f16v s = scores<G, KS>(qt, K, ent, 0, lane);
-      const f16v dp = product<G, KS>(qt + G::kElems, V, lane);
+      f16v s = scores<G, KS, true>(qt, K, ent, 0, lane);
+      const f16v dp = product<G, KS, true>(qt + G::kElems, V, lane);
       if (some_dead) mask_scores(live ? 0xffffffffu : 0u, half, s);   // p = 0: nothing for the bias
       float p[16];
 #pragma unroll
@@ -276,24 +276,51 @@ __global__ void __launch_bounds__(256)
 }
 
 // grad_bias[h][b] = sum over the tiles' parts, in a fixed order.
+//
+// Every row of ds sums to zero, so a head's buckets do too.  What they sum to instead is
+// rounding, most of it in the buckets of most pairs: n additions to a sum that grows as
+// sqrt(n) round off about n.  It is taken off in proportion to n^2, n by the squares
+// of the parts (a bucket without pairs stays 0).  Two structures of 3,000 to 6,000 atoms,
+// 2 heads, 32 buckets, float32, 93 % of the pairs in the last: 4.4e-6 off without, 3.6e-7 with.
 constexpr int kJoinThreads = 1024;
 template <typename T>
 __global__ void __launch_bounds__(kJoinThreads)
     k_attn_join_bias(const float* __restrict__ part, int n, int nb, T* __restrict__ out) {
-  __shared__ float lds[kJoinThreads];
+  __shared__ float2 lds[kJoinThreads];
   const int h = blockIdx.x, b = threadIdx.x & 63, g = threadIdx.x >> 6;
-  float s = 0.f;
+  float2 s = make_float2(0.f, 0.f);
   if (b < nb) {
 #pragma unroll 8
-    for (int t = g; t < n; t += kJoinThreads / 64) s += part[((size_t)h * n + t) * nb + b];
+    for (int t = g; t < n; t += kJoinThreads / 64) {
+      const float v = part[((size_t)h * n + t) * nb + b];
+      s.x += v;
+      s.y = fmaf(v, v, s.y);
+    }
   }
   lds[threadIdx.x] = s;
 #pragma unroll
   for (int m = kJoinThreads / 2; m >= 64; m >>= 1) {
     __syncthreads();
-    if ((int)threadIdx.x < m) lds[threadIdx.x] += lds[threadIdx.x + m];
+    if ((int)threadIdx.x < m) {
+      lds[threadIdx.x].x += lds[threadIdx.x + m].x;
+      lds[threadIdx.x].y += lds[threadIdx.x + m].y;
+    }
   }
-  if (g == 0 && b < nb) out[(size_t)h * nb + b] = (T)lds[b];
+  if (g > 0) return;                       // one wave, a lane per bucket
+  s = lds[b];
+  float most = s.y;
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor(most, m, 64));
+  const float share = s.y / most;
+  float over = s.x, weight = share * share;
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) {
+    over += __shfl_xor(over, m, 64);
+    weight += __shfl_xor(weight, m, 64);
+  }
+  const float off = over * (share * share / weight);
+  // not where values are not finite, or so small or large that their squares are not
+  if (b < nb) out[(size_t)h * nb + b] = (T)(__builtin_isfinite(off) ? s.x - off : s.x);
 }
 
 template <typename T>

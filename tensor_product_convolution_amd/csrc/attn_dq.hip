@@ -5,11 +5,12 @@
 //
 // A wave owns 32 queries and walks the keys as the forward does, with delta formed
 // from its own rows.  That delta carries the rounding of out (and the products
-// theirs), so a row of ds does not quite sum to zero.  grad_q does not notice, but
-// the bias gradient of a bucket that holds most pairs is a sum of millions of
-// terms that nearly cancel: it came out 5e-3 (bfloat16) and 2e-5 (float32) off at
-// 1,536 atoms.  So the row sums r = sum_j ds_ij are kept too, and the key side, which
-// forms ds again, takes delta + r.
+// theirs), so a row of ds does not quite sum to zero.  The bias gradient of a bucket
+// that holds most pairs, a sum of millions of terms that nearly cancel, came out
+// 5e-3 (bfloat16) and 2e-5 (float32) off at 1,536 atoms.  So the row sums
+// r = sum_j ds_ij are kept too, and the key side, which forms ds again, takes
+// delta + r.  In bfloat16 grad_q of short rows notices as well (structures of 62 atoms:
+// 2.5e-3 off against 2.4e-3), so p k is summed beside ds k and r p k taken off at the end.
 #include "attn.hpp"
 
 namespace tpc {
@@ -28,7 +29,7 @@ struct DqShape {
     const size_t walk = kWork + (size_t)(nb > 0 ? nb : 1) * HG * 128;
     return walk > kJoin ? walk : kJoin;    // the joined parts take the place of all else
   }
-  static constexpr int kRegs = HG * (2 * KS * G::P * 4 + G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 6 : 10);
+  static constexpr int kRegs = HG * (2 * KS * G::P * 4 + (G::P == 1 ? 2 : 1) * G::MT * 16) + 76 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
@@ -97,12 +98,14 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     lse[hh] = q < hi && e != -INFINITY ? e * kLog2e : INFINITY;
   }
 
-  f16v dQ[HG][MT];
+  constexpr bool kCorrect = P == 1;
+  f16v dQ[HG][MT], PK[HG][kCorrect ? MT : 1];
   float r[HG];
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
     r[hh] = 0.f;
     clear<MT>(dQ[hh]);
+    if (kCorrect) clear<MT>(PK[hh]);
   }
 
   const auto stage = [&](int buf) {
@@ -124,32 +127,35 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
       f16v s = scores<G, KS>(kt, Q[hh], ent, hh, lane);
       const f16v dp = product<G, KS>(kt + G::kElems, dO[hh], lane);
       if (vm != 0xffffffffu) mask_scores(vm, half, s);
-      float ds[16];
+      float p[16], ds[16], sum = 0.f;      // a sum per tile first: few additions to the running one
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[i], scale.c, -lse[hh]));
-        ds[i] = p * (dp[i] - delta[hh]);
-        r[hh] += ds[i];
+        p[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale.c, -lse[hh]));
+        ds[i] = p[i] * (dp[i] - delta[hh]);
+        sum += ds[i];
       }
+      r[hh] += sum;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        Frag<P> f;
+        Frag<P> f, w;
         to_frag(ds + 8 * kb, f);
+        if (kCorrect) to_frag(p + 8 * kb, w);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) dQ[hh][mt] = mma(col_frag<G>(kt, mt, kb, lane), f, dQ[hh][mt]);
+        for (int mt = 0; mt < MT; ++mt) {
+          const Frag<P> k = col_frag<G>(kt, mt, kb, lane);
+          dQ[hh][mt] = mma(k, f, dQ[hh][mt]);
+          if (kCorrect) PK[hh][mt] = mma(k, w, PK[hh][mt]);
+        }
       }
     }
   });
 
+  // row sums over all waves that share the row: delta for the key side, and grad_q's part of it
   float* join = reinterpret_cast<float*>(lds) + (size_t)qw * KW * HG * S::kPart + lane;
   if (KW > 1) {
     __syncthreads();
 #pragma unroll
-    for (int hh = 0; hh < HG; ++hh) {
-      float* w = join + (kw * HG + hh) * S::kPart;
-      w[0] = pair_sum(r[hh]);
-      park<MT>(w + 64, dQ[hh]);
-    }
+    for (int hh = 0; hh < HG; ++hh) join[(kw * HG + hh) * S::kPart] = pair_sum(r[hh]);
     __syncthreads();
   }
 #pragma unroll
@@ -162,7 +168,15 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
       sum = pair_sum(r[hh]);
     }
     if (q < hi && half == 0 && kw == 0) a.delta[(size_t)(h0 + hh) * d.n_nodes + q] = delta[hh] + sum;
+    if (kCorrect) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dQ[hh][mt][i] = fmaf(-sum, PK[hh][mt][i], dQ[hh][mt][i]);
+    }
+    if (KW > 1) park<MT>(join + (kw * HG + hh) * S::kPart + 64, dQ[hh]);
   }
+  if (KW > 1) __syncthreads();
   if (q >= hi) return;
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
@@ -215,7 +229,7 @@ hipError_t by_waves(const AttnArgs& a, const Extent& x) {
 template <typename T, int KS>
 hipError_t by_heads(const AttnArgs& a) {
   const Extent x(a.d, a.d.n_heads);
-  if constexpr (kPlanes<T> * KS <= 4) {
+  if constexpr (KS <= (kPlanes<T> == 1 ? 2 : 1)) {
     const int rep = a.d.n_heads / a.d.n_kv_heads;
     if (x.units >= 1024) {
       if (rep % 2 == 0) return by_waves<T, KS, 2, 1>(a, x);
