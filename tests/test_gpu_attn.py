@@ -79,7 +79,7 @@ class Case:
         full = dict(pos=None, bias=None, key_mask=None, scale=None)
         full.update(kw)
         for sl, h, g, bk, live, q, k, v, p, lse, sc in ol._each(**c, **full):
-            n, d = q.shape
+            (n, d), sc = q.shape, abs(sc)
             smax = float((np.abs(q) @ np.abs(k).T).max() * sc) + np.abs(lse[np.isfinite(lse)]).max(initial=0.0)
             if bk is not None:
                 smax += np.abs(kw["bias"][h][np.isfinite(kw["bias"][h])]).max(initial=0.0)
@@ -206,6 +206,28 @@ def test_nan_in_a_live_row_shows(tpc, dtype):
     assert torch.isnan(c.out[:40, 0]).all() and not torch.isnan(c.out[40:]).any() and not torch.isnan(c.out[:, 1]).any()
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.5, 3.0])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scales(tpc, dtype, scale):
+    """A scale of zero (bias alone), a negative one, a large one."""
+    c = Case(dtype, [50, 70], 4, 2, 16, nb=16, masked=0.1)
+    c.kw["scale"] = scale
+    c.check(tpc)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bias_gradient_of_one_crowded_bucket(tpc, dtype):
+    """Nearly all pairs in the last bucket: its gradient is a sum of cancelling terms.  The
+    tolerance is that of the smaller buckets' own bound, far below n u of the terms."""
+    c = Case(dtype, [600, 500], 4, 2, 32, nb=8, seed=7).run(tpc)
+    h, kw, go = c.host()
+    ref = ol.attn_backward(**h, **kw, grad_out=go)[3]
+    got = c.grads[3].double().cpu().numpy()
+    # bfloat16: rounded once; float32: 2^-16 of the head's largest bucket
+    tol = (W if dtype == "bf16" else 2.0 ** -16) * np.abs(ref).max(axis=1, keepdims=True)
+    assert (np.abs(got - ref) <= tol).all(), np.abs(got - ref).max()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_large_scores(tpc, dtype):
     """Scores that overflow exp without the running maximum, growing along the keys."""
@@ -275,6 +297,27 @@ def test_other_stream_and_graph_replay(tpc):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, [out, *grads]))
         c.run(tpc)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_beyond_32_bits(tpc, dtype):
+    """Rows far apart: element offsets pass 2^31.  Bit for bit the results of dense rows."""
+    n, wide = 36000, 1 << 16
+    dt = DT[dtype]
+    big = torch.empty(n, wide, device="cuda", dtype=dt)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    big[:, -96:] = torch.randn(n, 96, device="cuda", generator=g).to(dt)
+    q, k, v = (big[:, -96 + 32 * i:wide - 64 + 32 * i].view(n, 2, 16) for i in range(3))
+    seg = torch.arange(0, n + 1, 60, device="cuda", dtype=torch.int32)
+    pos = 4 * torch.rand(n, 3, device="cuda", generator=g)
+    bias = torch.randn(2, 8, device="cuda", generator=g).to(dt)
+    go = torch.randn(n, 2, 16, device="cuda", generator=g).to(dt)
+    res = []
+    for a in ((q, k, v), tuple(t.contiguous() for t in (q, k, v))):
+        out, lse = tpc.attn_forward(*a, seg, pos=pos, bias=bias)
+        outs = [torch.empty(n, wide, device="cuda", dtype=dt)[:, -32:].view(n, 2, 16) for _ in range(3)] if a[0] is q else None
+        res.append([out, lse, *tpc.attn_backward(*a, seg, out, lse, go, pos=pos, bias=bias, outs=outs)])
+    assert all(torch.equal(x, y) for x, y in zip(*res))
 
 
 def test_empty_batches(tpc):

@@ -204,6 +204,21 @@ def test_element_numbers_beyond_32_bits(tpc):
         assert out[at:at + 8].float().cpu().tolist() == want, at
 
 
+def test_strides_beyond_32_bits(tpc):
+    """Rows far apart: element offsets pass 2^31.  Bit for bit the results of dense rows."""
+    n, wide, c = 36000, 1 << 16, 40
+    x = torch.empty(n, wide, device="cuda", dtype=torch.bfloat16)[:, -c:]
+    gy = torch.empty(n, wide, device="cuda", dtype=torch.bfloat16)[:, :c]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x[:], gy[:] = (torch.randn(n, c, device="cuda", generator=g) for _ in range(2))
+    w, b = torch.rand(c, device="cuda", generator=g), torch.rand(c, device="cuda", generator=g)
+    res = []
+    for a, d in ((x, gy), (x.contiguous(), gy.contiguous())):
+        y, mean, rstd = tpc.layer_norm_forward(a, w, b)
+        res.append([y, mean, rstd, *tpc.layer_norm_backward(d, a, w, mean, rstd)])
+    assert all(torch.equal(p, q) for p, q in zip(*res))
+
+
 def test_no_rows_and_refusals(tpc):
     e = torch.empty(0, 16, device="cuda")
     g = torch.ones(16, device="cuda")
