@@ -38,32 +38,16 @@ __device__ __forceinline__ void philox4(const DropArgs& d, uint64_t blk, uint32_
   w[3] = c3;
 }
 
-// keep[j]: whether element e + j is kept, j < N (N a multiple of 4).  Where e is not a
-// multiple of 4 (odd row lengths, !ALIGNED) the run touches one block more.  A comparison's
+// which of the N words (a multiple of 4) from block blk on keep their elements.  A comparison's
 // result stays in scalar registers, one bit a lane.
-template <int N, bool ALIGNED>
-__device__ __forceinline__ void philox_keep(const DropArgs& d, uint64_t e, bool keep[N]) {
-  const uint64_t blk = e >> 2;
-  if (ALIGNED) {
+template <int N>
+__device__ __forceinline__ void philox_keep(const DropArgs& d, uint64_t blk, bool keep[N]) {
 #pragma unroll
-    for (int b = 0; b < N / 4; ++b) {
-      uint32_t w[4];
-      philox4(d, blk + b, w);
+  for (int b = 0; b < N / 4; ++b) {
+    uint32_t w[4];
+    philox4(d, blk + b, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) keep[4 * b + j] = w[j] >= d.threshold;
-    }
-  } else {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int b = 0; b < N / 4 + 1; ++b) {
-      uint32_t w[4];
-      philox4(d, blk + b, w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bits |= (uint32_t)(w[j] >= d.threshold) << (4 * b + j);
-    }
-    bits >>= e & 3;
-#pragma unroll
-    for (int j = 0; j < N; ++j) keep[j] = (bits >> j) & 1;
+    for (int j = 0; j < 4; ++j) keep[4 * b + j] = w[j] >= d.threshold;
   }
 }
 
