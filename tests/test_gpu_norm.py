@@ -266,3 +266,13 @@ def test_graph_replay(tpc):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
         step()
+
+
+# rows that end inside a chunk, on either side of every change of layout, and so many rows that
+# a workgroup takes several
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(50, 3), (50, 5), (50, 9), (40, 19), (40, 43), (33, 61), (33, 86), (30, 125), (30, 135),
+                                   (30, 189), (20, 195), (20, 251), (20, 393), (20, 514), (9, 1018), (9, 1029), (9, 2046),
+                                   (5, 2051), (5, 4093), (70000, 6), (20000, 131), (3000, 270), (4500, 1101), (600, 2101)], ids=str)
+def test_rows_of_odd_length(tpc, dtype, shape):
+    test_residual_norm(tpc, dtype, shape, 0.3)
