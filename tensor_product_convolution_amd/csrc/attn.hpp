@@ -235,15 +235,32 @@ __device__ __forceinline__ float bias_at(const tp_attn& d, int h, int b) {
   const size_t i = (size_t)h * d.n_buckets + b;
   return d.dtype == TP_F32 ? static_cast<const float*>(d.bias)[i] : (float)static_cast<const bf16_t*>(d.bias)[i];
 }
-template <int HG>
-__device__ __forceinline__ void fill_table(const tp_attn& d, float inv, int h0, float* tbl, int threads) {
-  const int ne = d.n_buckets > 0 ? d.n_buckets : 1;
-  for (int i = threadIdx.x; i < ne * HG * 8; i += threads) {
-    const int hh = (i >> 3) % HG, b = (i >> 3) / HG;
-    const float v = d.n_buckets > 0 ? bias_at(d, h0 + hh, b) * inv : 0.f;
-    reinterpret_cast<f4*>(tbl)[i] = f4{v, v, v, v};
+// THREADS / 64 threads share an entry's eight 16-byte chunks.  They load its value early, with
+// all else that the walk begins with, and later write its copies, starting at different
+// columns for different banks.
+template <int HG, int THREADS>
+struct TableFill {
+  static constexpr int kShare = THREADS / 64;
+  static_assert(THREADS % 64 == 0 && 8 % kShare == 0 && kMaxBuckets == 64);
+  float v[HG];
+  static __device__ __forceinline__ int entry(int u) { return (int)threadIdx.x / kShare + 64 * u; }
+  __device__ __forceinline__ void load(const tp_attn& d, int h0) {
+#pragma unroll
+    for (int u = 0; u < HG; ++u) v[u] = entry(u) < d.n_buckets * HG ? bias_at(d, h0 + entry(u) % HG, entry(u) / HG) : 0.f;
   }
-}
+  __device__ __forceinline__ void write(const tp_attn& d, float inv, float* tbl) const {
+    const int ne = d.n_buckets > 0 ? d.n_buckets : 1;
+#pragma unroll
+    for (int u = 0; u < HG; ++u) {
+      const int i = entry(u);
+      if (i >= ne * HG) break;
+      const float w = v[u] * inv;
+#pragma unroll
+      for (int j = threadIdx.x % kShare; j < 8; j += kShare)
+        reinterpret_cast<f4*>(tbl)[8 * i + ((i + j) & 7)] = f4{w, w, w, w};
+    }
+  }
+};
 
 typedef __attribute__((address_space(3))) float lds_f;
 __device__ __forceinline__ uint32_t lds_address(const float* p) { return (uint32_t)(uintptr_t)(lds_f*)p; }
@@ -361,6 +378,11 @@ struct Stager {
       const int64_t r = r0 + row_of(c) - lo;
       at[i] = (t & 1 ? safe1 + r * s1 : safe0 + r * s0) + head((t >> 1) % NS) * D + 8 * col_of(c);
     }
+  }
+  // back to the first of n tiles fetched since aim, `columns` to the right of it
+  __device__ __forceinline__ void again(int n, int columns) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) at[i] += columns - n * (array_of(chunk(i)) & 1 ? step1 : step0);
   }
   // loads the tile that aim (or the previous fetch) has come to, rows r0 ..
   __device__ __forceinline__ void fetch(int r0, int end, int D, const uint8_t* mask) {

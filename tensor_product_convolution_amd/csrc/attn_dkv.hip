@@ -125,11 +125,12 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
       sdel = q0 + tid < hi ? a.delta[at] : 0.f;
     }
   };
-  for (; h < h_hi; ++h) {
-    if (h > h_lo) __syncthreads();         // the previous head's table and columns have been read
-    st.aim(tid, a.q, a.qs, a.go, a.gos, lo, q_first, step, D, [&](int) { return h; });
-    prepare(0);
-    fill_table<1>(d, scale.inv, h, tbl, S::kThreads);
+  TableFill<1, S::kThreads> fill;
+  st.aim(tid, a.q, a.qs, a.go, a.gos, lo, q_first, step, D, [&](int) { return h; });
+  prepare(0);
+  fill.load(d, h);
+  while (true) {
+    fill.write(d, scale.inv, tbl);
     if (biased) {
       for (int i = lane; i < ne * 16; i += 64) reinterpret_cast<f4*>(my_cols)[i] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -200,6 +201,12 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
 #pragma unroll
       for (int i = 0; i < 16; i += 2) ColumnPair(due[i], due[i + 1]).add(ds[i], ds[i + 1]);
     }
+    const int done = h++;
+    if (h < h_hi) {                        // the next head's first tile, while this one's sums are taken
+      st.again(n, D);
+      prepare(0);
+      fill.load(d, h);
+    }
     if (a.gbias) {
       // an entry's 64 columns of every wave, 16 bytes at a time; lanes start at different
       // columns so that they read different banks
@@ -214,9 +221,11 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
             s += (v[0] + v[1]) + (v[2] + v[3]);
           }
         }
-        a.part[((size_t)h * gridDim.x + blockIdx.x) * nb + b] = s;
+        a.part[((size_t)done * gridDim.x + blockIdx.x) * nb + b] = s;
       }
     }
+    if (h == h_hi) break;
+    __syncthreads();                       // this head's table and columns have been read
   }
 
   float* join = reinterpret_cast<float*>(lds) + (size_t)kv * QS * S::kPart + lane;

@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
   prepare(0);
 
   const Scale scale(d.scale);
-  fill_table<HG>(d, scale.inv, h0, tbl, S::kThreads);
+  TableFill<HG, S::kThreads> fill;
+  fill.load(d, h0);
   const Buckets<HG> bk(d, tbl, lane);
 
   const int q = q0 + 32 * qw + (lane & 31), qc = q < hi ? q : hi - 1;
@@ -112,6 +113,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     st.stage(tiles_of(buf));
     rows.stage(tid, rows_of(buf));
   };
+  fill.write(d, scale.inv, tbl);
   __syncthreads();                         // the table
   uint32_t ent[16];
 #pragma unroll

@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   prepare(0);
 
   const Scale scale(d.scale);
-  fill_table<HG>(d, scale.inv, h0, tbl, S::kThreads);
+  TableFill<HG, S::kThreads> fill;
+  fill.load(d, h0);
   const Buckets<HG> bk(d, tbl, lane);
 
   // this lane's query
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
     st.stage(tiles_of(buf));
     rows.stage(tid, rows_of(buf));
   };
+  fill.write(d, scale.inv, tbl);
   __syncthreads();                         // the table
   uint32_t ent[16];
 #pragma unroll
