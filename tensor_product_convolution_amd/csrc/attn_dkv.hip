@@ -208,20 +208,27 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
       fill.load(d, h);
     }
     if (a.gbias) {
-      // an entry's 64 columns of every wave, 16 bytes at a time; lanes start at different
-      // columns so that they read different banks
-      __syncthreads();
-      for (int b = threadIdx.x; b < nb; b += S::kThreads) {
-        float s = 0.f;
-        for (int w = 0; w < NW; ++w) {
-          const f4* c4 = reinterpret_cast<const f4*>(cols + (size_t)(w * ne + b) * 64);
+      // each wave sums its own columns, a lane per entry, 16 bytes at a time; lanes start at
+      // different columns so that they read different banks
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      float s = 0.f;
+      if (lane < nb) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const f4 v = c4[(j + lane) & 15];
-            s += (v[0] + v[1]) + (v[2] + v[3]);
-          }
+        for (int j = 0; j < 16; ++j) {
+          const f4 v = reinterpret_cast<const f4*>(my_cols)[16 * lane + ((j + lane) & 15)];
+          s += (v[0] + v[1]) + (v[2] + v[3]);
         }
-        a.part[((size_t)done * gridDim.x + blockIdx.x) * nb + b] = s;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      my_cols[lane] = s;
+      __syncthreads();
+      if ((int)threadIdx.x < nb) {
+        s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += cols[(size_t)w * ne * 64 + lane];
+        a.part[((size_t)done * gridDim.x + blockIdx.x) * nb + lane] = s;
       }
     }
     if (h == h_hi) break;
