@@ -14,6 +14,12 @@
 // elements at a time, summed per workgroup and joined by a second kernel.  An LDS
 // float atomic takes 190 cycles a wave on gfx950; a read, an addition and a write of
 // a pair take 150 cycles of latency, which the distances of the next tile fill.
+//
+// About 420 vector instructions a tile of 32 x 32 pairs and head, and nearly as many LDS
+// cycles, bound it; the columns (256 bytes a bucket and wave) keep it at one to two waves a
+// SIMD.  1,536 atoms, 8 heads, 32 buckets: of 32, bfloat16 35 us, of 16, float32 49 us; 4,096
+// atoms, 4 query heads of 64 on one key head, 64 buckets, float32: 303 us (six products for
+// one: 113 TFLOP/s of float32 work).
 #include "attn.hpp"
 
 namespace tpc {
@@ -369,8 +375,8 @@ hipError_t launch(const AttnArgs& a) {
 
 // ---- which variant
 // As the query side, but the columns of the bias gradient bound the waves of a workgroup:
-// eight up to 32 buckets, four up to 64.  (us) 1,536 atoms, 8 heads of 32, bfloat16: 2x4 44,
-// 2x2 59, 4x1 100; 4,096 atoms: 4x2 145, 2x4 174; 512 molecules of 62 atoms: 2x1 130, 2x2 259.
+// eight up to 32 buckets, four up to 64.  (us) 1,536 atoms, 8 heads of 32, bfloat16: 2x4 40,
+// 2x2 58, 4x1 92; 4,096 atoms: 4x2 152, 2x4 169; 512 molecules of 62 atoms: 2x1 124, 2x2 215.
 template <typename T, int KS>
 hipError_t by_waves(const AttnArgs& a) {
   const Extent x(a.d, a.split ? a.d.n_heads : a.d.n_kv_heads);

@@ -11,6 +11,9 @@
 // r = sum_j ds_ij are kept too, and the key side, which forms ds again, takes
 // delta + r.  In bfloat16 grad_q of short rows notices as well (structures of 62 atoms:
 // 2.5e-3 off against 2.4e-3), so p k is summed beside ds k and r p k taken off at the end.
+//
+// Bound by the vector units as the forward is.  1,536 atoms, 8 heads: of 32, bfloat16 26 us, of
+// 16, float32 34 us; 4,096 atoms, 4 heads of 64, float32: 181 us.
 #include "attn.hpp"
 
 namespace tpc {
@@ -212,8 +215,10 @@ hipError_t launch(const AttnArgs& a) {
 // ---- which variant
 // The waves of a workgroup: with enough query tiles to fill the chip, eight tiles share the
 // staged keys; with few, two tiles share them and the other waves split the keys, four
-// ways where LDS holds the tiles; short structures get one wave per tile.  (us) 4,096
-// atoms, 8 heads of 32, bfloat16: 2x4 84, 8x1 178; 512 molecules of 62 atoms: 2x1 57, 1x1 67.
+// ways where LDS holds the tiles; of many structures under 1,024 atoms two tiles share
+// keys; structures of a tile get one wave.  (us) 4,096 atoms, 8 heads of 32, bfloat16:
+// 2x4 94, 8x1 261; 512 molecules of 62 atoms: 2x1 55, 1x1 60, 4x1 65; 120 structures of 300: 2x1
+// 108, 4x1 103.
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a, const Extent& x) {
   constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
@@ -226,8 +231,8 @@ hipError_t by_waves(const AttnArgs& a, const Extent& x) {
 }
 
 // Two heads to a wave share distances and buckets, where their operands fit the registers
-// and half the waves still fill the chip (4,096 atoms, 8 heads of 32: 84 against 106 us;
-// 1,536 atoms: 38 against 34 us).
+// and half the waves still fill the chip (4,096 atoms, 8 heads of 32: 94 against 120 us;
+// 1,536 atoms: 39 against 30 us).
 template <typename T, int KS>
 hipError_t by_heads(const AttnArgs& a) {
   const Extent x(a.d, a.d.n_heads);

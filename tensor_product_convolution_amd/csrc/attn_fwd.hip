@@ -4,6 +4,13 @@
 //
 // QW x KW waves: QW own 32 queries each and share staged keys, KW split the keys and
 // are joined through LDS at the end (for batches with few query tiles).
+//
+// The vector units bound it, not the matrix units: a pair costs about 11 instructions for
+// its distance and bucket, shared by HG heads, and 6 a head around the exponential,
+// against one 32-cycle product per 32 x 32 x 16.  16,384 atoms, 8 heads of 64, bfloat16: 973 us
+// (565 TFLOP/s, 46 % of a large library product's rate; vector units 65 % busy at two waves a
+// SIMD); 1,536 atoms, 8 heads: of 32, bfloat16 21 us, of 16, float32 30 us (48 workgroup
+// tiles x 8 heads, a quarter of the chip idle); 4,096 atoms, 4 heads of 64, float32 126 us.
 #include "attn.hpp"
 
 namespace tpc {
@@ -212,9 +219,11 @@ hipError_t launch(const AttnArgs& a) {
 // ---- which variant
 // The waves of a workgroup: with enough query tiles to fill the chip, eight tiles share the
 // staged keys; with few, two tiles share them and the other waves split the keys, four
-// ways where LDS holds the tiles; short structures get one wave per tile.  Measured
-// (us): 16,384 atoms, 8 heads of 64, bfloat16: 8x1 1,003, 2x4 1,380; 4,096 atoms, 8 heads of
-// 32: 2x4 78, 8x1 158; 512 molecules of 62 atoms, 8 heads of 32: 2x1 45, 1x1 58, 2x4 110.
+// ways where LDS holds the tiles; of many structures under 1,024 atoms four tiles share
+// keys; structures of a tile get one wave.  Measured (us): 16,384 atoms, 8 heads of 64,
+// bfloat16: 8x1 977, 2x4 1,674; 4,096 atoms, 8 heads of 32: 2x4 76, 8x1 215; 120 structures
+// of 300 atoms: 4x1 74, 2x1 86, 1x1 88, 2x4 144 (float32: 141, 2x1 179, 8x1 227); 512
+// molecules of 62 atoms, 64 buckets: 4x1 42, 2x1 44, 1x1 41, 2x4 110.
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a, const Extent& x) {
   constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
@@ -223,12 +232,12 @@ hipError_t by_waves(const AttnArgs& a, const Extent& x) {
   if (x.mean <= kTile) return launch<T, KS, HG, NKV, 1, 1>(a);
   if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, 8, 1>(a);
   if (x.mean >= 1024 || waves < 1024) return launch<T, KS, HG, NKV, 2, KX>(a);
-  return launch<T, KS, HG, NKV, 2, 1>(a);
+  return launch<T, KS, HG, NKV, 4, 1>(a);
 }
 
 // Two heads to a wave share distances and buckets, where their operands fit the registers
-// and half the waves still fill the chip (16,384 atoms: 1,003 against 1,104 us; 1,536
-// atoms: 32 against 24 us).
+// and half the waves still fill the chip (16,384 atoms: 977 against 1,414 us; 4,096: 76
+// against 104; 1,536: 32 against 24).
 template <typename T, int KS>
 hipError_t by_heads(const AttnArgs& a) {
   const Extent x(a.d, a.d.n_heads);
