@@ -547,6 +547,7 @@ __device__ __forceinline__ void clear(f16v acc[MT]) {
 }
 
 constexpr size_t kLdsMax = 160 * 1024;
+constexpr int kCUs = 256;
 
 // How many waves a call can use: 32-row tiles times heads, the mean length of a structure.
 struct Extent {

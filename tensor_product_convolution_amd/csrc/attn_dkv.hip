@@ -16,8 +16,8 @@
 // a pair take 150 cycles of latency, which the distances of the next tile fill.
 //
 // About 420 vector instructions a tile of 32 x 32 pairs and head, and nearly as many LDS
-// cycles, bound it; the columns (256 bytes a bucket and wave) keep it at one to two waves a
-// SIMD.  1,536 atoms, 8 heads, 32 buckets: of 32, bfloat16 35 us, of 16, float32 49 us; 4,096
+// cycles; the columns (256 bytes a bucket and wave) keep it at one to two waves a SIMD,
+// which do not cover each other's latency (vector units 34 % busy, LDS 26 %).  1,536 atoms, 8 heads, 32 buckets: of 32, bfloat16 35 us, of 16, float32 49 us; 4,096
 // atoms, 4 query heads of 64 on one key head, 64 buckets, float32: 303 us (six products for
 // one: 113 TFLOP/s of float32 work).
 #include "attn.hpp"
@@ -375,13 +375,18 @@ hipError_t launch(const AttnArgs& a) {
 
 // ---- which variant
 // As the query side, but the columns of the bias gradient bound the waves of a workgroup:
-// eight up to 32 buckets, four up to 64.  (us) 1,536 atoms, 8 heads of 32, bfloat16: 2x4 40,
+// eight up to 32 buckets, four up to 64.  (us) 1,536 atoms, 5 heads of 64 (245 tiles),
+// float32: 1x4 78, 2x2 110; 1,536 atoms, 8 heads of 32, bfloat16: 2x4 40,
 // 2x2 58, 4x1 92; 4,096 atoms: 4x2 152, 2x4 169; 512 molecules of 62 atoms: 2x1 124, 2x2 215.
 template <typename T, int KS>
 hipError_t by_waves(const AttnArgs& a) {
   const Extent x(a.d, a.split ? a.d.n_heads : a.d.n_kv_heads);
   const int nb = a.d.n_buckets;
   if (x.mean <= kTile) return launch<T, KS, 1, 1>(a);
+  if (x.units <= kCUs) {
+    if (DkvShape<T, KS, 1, 8>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 1, 8>(a);
+    if (DkvShape<T, KS, 1, 4>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 1, 4>(a);
+  }
   if (x.mean < 1024 && x.units >= 1024) return launch<T, KS, 2, 1>(a);
   if (x.units >= 1024 && DkvShape<T, KS, 4, 2>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 4, 2>(a);
   if (x.units < 1024 && DkvShape<T, KS, 2, 4>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 2, 4>(a);

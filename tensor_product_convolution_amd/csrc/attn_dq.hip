@@ -12,7 +12,7 @@
 // delta + r.  In bfloat16 grad_q of short rows notices as well (structures of 62 atoms:
 // 2.5e-3 off against 2.4e-3), so p k is summed beside ds k and r p k taken off at the end.
 //
-// Bound by the vector units as the forward is.  1,536 atoms, 8 heads: of 32, bfloat16 26 us, of
+// Bound as the forward is (vector units 40 % busy, latency of the rest).  1,536 atoms, 8 heads: of 32, bfloat16 26 us, of
 // 16, float32 34 us; 4,096 atoms, 4 heads of 64, float32: 181 us.
 #include "attn.hpp"
 
@@ -216,15 +216,21 @@ hipError_t launch(const AttnArgs& a) {
 // The waves of a workgroup: with enough query tiles to fill the chip, eight tiles share the
 // staged keys; with few, two tiles share them and the other waves split the keys, four
 // ways where LDS holds the tiles; of many structures under 1,024 atoms two tiles share
-// keys; structures of a tile get one wave.  (us) 4,096 atoms, 8 heads of 32, bfloat16:
+// keys; structures of a tile get one wave;
+// where a workgroup for each tile leaves CUs idle, its waves all split the keys.  (us) 4,096 atoms, 8 heads of 32, bfloat16:
 // 2x4 94, 8x1 261; 512 molecules of 62 atoms: 2x1 55, 1x1 60, 4x1 65; 120 structures of 300: 2x1
-// 108, 4x1 103.
+// 108, 4x1 103; 1,536 atoms, 5 heads of 64 (245 tiles): 1x8 26, 1x4 30, 2x4 34, with 8 heads
+// (392 tiles) 1x8 32, 2x4 28.
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a, const Extent& x) {
   constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
   constexpr int64_t fill = kPlanes<T> * KS <= 2 ? 4096 : 2048;       // waves a chip holds of this kernel
   const int64_t waves = x.units / HG;
   if (x.mean <= kTile) return launch<T, KS, HG, NKV, 1, 1>(a);
+  if constexpr (HG == 1 && KX == 4) {
+    constexpr int K1 = Tile<T, KS>::kElems * 4 * 8 <= 120 * 1024 ? 8 : 4;
+    if (x.units <= kCUs) return launch<T, KS, 1, 1, 1, K1>(a);
+  }
   if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, 8, 1>(a);
   if (x.mean >= 1024 || waves < 1024) return launch<T, KS, HG, NKV, 2, KX>(a);
   return launch<T, KS, HG, NKV, 2, 1>(a);

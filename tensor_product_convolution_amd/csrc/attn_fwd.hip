@@ -8,9 +8,10 @@
 // The vector units bound it, not the matrix units: a pair costs about 11 instructions for
 // its distance and bucket, shared by HG heads, and 6 a head around the exponential,
 // against one 32-cycle product per 32 x 32 x 16.  16,384 atoms, 8 heads of 64, bfloat16: 973 us
-// (565 TFLOP/s, 46 % of a large library product's rate; vector units 65 % busy at two waves a
-// SIMD); 1,536 atoms, 8 heads: of 32, bfloat16 21 us, of 16, float32 30 us (48 workgroup
-// tiles x 8 heads, a quarter of the chip idle); 4,096 atoms, 4 heads of 64, float32 126 us.
+// (565 TFLOP/s, 46 % of a large library product's rate; vector units 60 %, LDS 42 %, matrix
+// units 22 % busy at two waves a SIMD); 1,536 atoms, 8 heads: of 32, bfloat16 21 us, of 16,
+// float32 30 us (192 workgroups: a quarter of the chip is idle); 4,096 atoms, 4 heads of 64,
+// float32 127 us (matrix units 32 %: six products for one).
 #include "attn.hpp"
 
 namespace tpc {
@@ -220,16 +221,22 @@ hipError_t launch(const AttnArgs& a) {
 // The waves of a workgroup: with enough query tiles to fill the chip, eight tiles share the
 // staged keys; with few, two tiles share them and the other waves split the keys, four
 // ways where LDS holds the tiles; of many structures under 1,024 atoms four tiles share
-// keys; structures of a tile get one wave.  Measured (us): 16,384 atoms, 8 heads of 64,
+// keys; structures of a tile get one wave;
+// where a workgroup for each tile leaves CUs idle, its waves all split the keys.  Measured (us): 16,384 atoms, 8 heads of 64,
 // bfloat16: 8x1 977, 2x4 1,674; 4,096 atoms, 8 heads of 32: 2x4 76, 8x1 215; 120 structures
 // of 300 atoms: 4x1 74, 2x1 86, 1x1 88, 2x4 144 (float32: 141, 2x1 179, 8x1 227); 512
-// molecules of 62 atoms, 64 buckets: 4x1 42, 2x1 44, 1x1 41, 2x4 110.
+// molecules of 62 atoms, 64 buckets: 4x1 42, 2x1 44, 1x1 41, 2x4 110; 1,536 atoms, 5 heads of
+// 64 (245 tiles): 1x8 18, 1x4 23, 2x4 26, with 8 heads (392 tiles) 1x8 27, 2x4 23.
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a, const Extent& x) {
   constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
   constexpr int64_t fill = kPlanes<T> * KS <= 2 ? 4096 : 2048;       // waves a chip holds of this kernel
   const int64_t waves = x.units / HG;
   if (x.mean <= kTile) return launch<T, KS, HG, NKV, 1, 1>(a);
+  if constexpr (HG == 1 && KX == 4) {
+    constexpr int K1 = Tile<T, KS>::kElems * 4 * 8 <= 120 * 1024 ? 8 : 4;
+    if (x.units <= kCUs) return launch<T, KS, 1, 1, 1, K1>(a);
+  }
   if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, 8, 1>(a);
   if (x.mean >= 1024 || waves < 1024) return launch<T, KS, HG, NKV, 2, KX>(a);
   return launch<T, KS, HG, NKV, 4, 1>(a);

@@ -12,7 +12,7 @@
 // and no cancellation as in E[x^2] - E[x]^2).  Measured, of a copy's 5.07 TB/s: 100,000
 // float32 rows of 128 values at a stride of 1,152: forward 18.2 us (5.6 TB/s), backward 27.2
 // (5.6) and 3.9 for the weights' join; 32,768 bfloat16 rows of 1,024 with dropout and
-// residual: forward 54.8 (4.9), backward 67.0 (5.0) and 4.9.
+// residual: forward 54.8 (4.9), backward 67.0 (4.0) and 4.9.
 #include <algorithm>
 
 #include "internal.hpp"
