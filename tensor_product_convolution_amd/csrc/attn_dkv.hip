@@ -48,7 +48,7 @@ struct DkvShape {
   static constexpr int kPart = 2 * G::MT * 16 * 64;                  // floats of one wave to join
   static constexpr int kJoin = QS > 1 ? KV * QS * kPart * 4 : 0;
   static constexpr int kWork = kBuf * kBufs * QS;
-  static size_t lds_bytes(int nb) {
+  static constexpr size_t lds_bytes(int nb) {
     const size_t walk = kWork + (nb > 0 ? (size_t)nb * (128 + KV * QS * 256) : 128);
     return walk > kJoin ? walk : kJoin;    // the joined parts take the place of all else
   }
@@ -381,17 +381,27 @@ hipError_t launch(const AttnArgs& a) {
 template <typename T, int KS>
 hipError_t by_waves(const AttnArgs& a) {
   const Extent x(a.d, a.split ? a.d.n_heads : a.d.n_kv_heads);
-  const int nb = a.d.n_buckets;
+  hipError_t e = hipSuccess;
+  // launched where LDS holds its tiles and the columns; not built where it never does
+  const auto fits = [&](auto kv, auto qs) {
+    using S = DkvShape<T, KS, kv(), qs()>;
+    if constexpr (S::lds_bytes(1) <= kLdsMax) {
+      if (S::lds_bytes(a.d.n_buckets) <= kLdsMax) {
+        e = launch<T, KS, kv(), qs()>(a);
+        return true;
+      }
+    }
+    return false;
+  };
+  const std::integral_constant<int, 1> c1;
+  const std::integral_constant<int, 2> c2;
+  const std::integral_constant<int, 4> c4;
+  const std::integral_constant<int, 8> c8;
   if (x.mean <= kTile) return launch<T, KS, 1, 1>(a);
-  if (x.units <= kCUs) {
-    if (DkvShape<T, KS, 1, 8>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 1, 8>(a);
-    if (DkvShape<T, KS, 1, 4>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 1, 4>(a);
-  }
+  if (x.units <= kCUs && (fits(c1, c8) || fits(c1, c4))) return e;
   if (x.mean < 1024 && x.units >= 1024) return launch<T, KS, 2, 1>(a);
-  if (x.units >= 1024 && DkvShape<T, KS, 4, 2>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 4, 2>(a);
-  if (x.units < 1024 && DkvShape<T, KS, 2, 4>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 2, 4>(a);
-  if (DkvShape<T, KS, 2, 2>::lds_bytes(nb) <= kLdsMax) return launch<T, KS, 2, 2>(a);
-  return launch<T, KS, 2, 1>(a);
+  if (x.units >= 1024 ? fits(c4, c2) : fits(c2, c4)) return e;
+  return fits(c2, c2) ? e : launch<T, KS, 2, 1>(a);
 }
 
 template <typename T>
