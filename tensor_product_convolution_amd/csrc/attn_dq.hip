@@ -221,17 +221,22 @@ hipError_t launch(const AttnArgs& a) {
 // 2x4 94, 8x1 261; 512 molecules of 62 atoms: 2x1 55, 1x1 60, 4x1 65; 120 structures of 300: 2x1
 // 108, 4x1 103; 1,536 atoms, 5 heads of 64 (245 tiles): 1x8 26, 1x4 30, 2x4 34, with 8 heads
 // (392 tiles) 1x8 32, 2x4 28.
+// Eight waves leave a wave 256 registers; a kernel that needs more (wide heads) would spill
+// its operands and takes four: 8,000 atoms, 8 heads of 128, bfloat16: 4x1 1,220, 8x1 3,508; of
+// 96: 1,012, 1,174; 2,000 atoms: of 128 2x2 93, 2x4 244, of 96 79, 95.  (float32 heads of 64
+// spill little and keep 2x4: 211 against 270 at 4,096 atoms.)
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a, const Extent& x) {
-  constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 ? 4 : 2;
+  constexpr bool kWide = DqShape<T, KS, HG, NKV, 2, 4>::kRegs > 250;
+  constexpr int KX = Tile<T, KS>::kElems * 4 * NKV * 4 <= 120 * 1024 && !kWide ? 4 : 2, QX = kWide ? 4 : 8;
   constexpr int64_t fill = kPlanes<T> * KS <= 2 ? 4096 : 2048;       // waves a chip holds of this kernel
   const int64_t waves = x.units / HG;
   if (x.mean <= kTile) return launch<T, KS, HG, NKV, 1, 1>(a);
-  if constexpr (HG == 1 && KX == 4) {
-    constexpr int K1 = Tile<T, KS>::kElems * 4 * 8 <= 120 * 1024 ? 8 : 4;
+  if constexpr (HG == 1 && Tile<T, KS>::kElems * 4 * 4 <= 120 * 1024) {
+    constexpr int K1 = Tile<T, KS>::kElems * 4 * 8 <= 120 * 1024 && DqShape<T, KS, 1, 1, 1, 8>::kRegs <= 256 ? 8 : 4;
     if (x.units <= kCUs) return launch<T, KS, 1, 1, 1, K1>(a);
   }
-  if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, 8, 1>(a);
+  if (x.mean >= 1024 && waves >= fill) return launch<T, KS, HG, NKV, QX, 1>(a);
   if (x.mean >= 1024 || waves < 1024) return launch<T, KS, HG, NKV, 2, KX>(a);
   return launch<T, KS, HG, NKV, 2, 1>(a);
 }
