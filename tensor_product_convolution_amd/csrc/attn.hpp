@@ -279,7 +279,9 @@ struct Buckets {
     shift = 23 - lg;
     const int base = (int)(bits(d.r_min * d.r_min) >> shift), nb = d.n_buckets > 0 ? d.n_buckets : 1;
     lo = flt((uint32_t)base << shift);
-    hi = flt(((uint32_t)(base + nb) << shift) - 1);
+    // a range that passes the largest float ends at infinity: as a float beyond it is a NaN or
+    // negative, and would let distances below lo through
+    hi = flt(min(((uint32_t)(base + nb) << shift) - 1, 0x7f800000u));
     first = lds_address(tbl) + (lane & 31) * 4;
     add = first - base * kEntry;
   }
