@@ -81,10 +81,12 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   for (int hh = 0; hh < HG; ++hh) own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, scale.sign, Q[hh]);
 
   f16v O[HG][MT];
-  float m[HG], l[HG];
+  float m[HG], l[HG];                      // running maximum of S and sum
+  bool wide[HG];                           // a row of the wave is far from 0 (below)
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
-    m[hh] = kLowest;
+    m[hh] = kLowest * kLn2 * scale.inv;
+    wide[hh] = false;
     l[hh] = 0.f;
     clear<MT>(O[hh]);
   }
@@ -115,31 +117,50 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
 #pragma unroll
     for (int hh = 0; hh < HG; ++hh) {
       const uint16_t* vt = kt + (NKV == 1 ? 1 : hh * 2 + 1) * G::kElems;
-      float p[16], sum;
-      const auto exponentials = [&]() {
-        sum = 0.f;
+      // c S - (c m rounded) is one instruction, off by one factor of up to 2^(2^-24 |c m|) in all
+      // of a row.  From 10^9 on that overflows, or leaves the row's largest term 0: rows beyond
+      // |c m| = 2^12 take the difference first, in the branch below.
+      float p[16], sum = 0.f, cm = m[hh] * scale.c;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -m[hh]));
-          sum += p[i];
-        }
-      };
-      exponentials();
+      for (int i = 0; i < 16; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -cm));
+        sum += p[i];
+      }
       // The running maximum is raised when the tile's sum shows that it has been passed by
       // far: probabilities up to 2^9 lose nothing, most tiles need no maximum at all, and
       // the accumulators are rescaled in few.  NaN takes this way in every tile.
-      if (__any(!(sum <= 512.f))) {
+      if (wide[hh] || __any(!(sum <= 512.f))) {
+        const auto is_wide = [&]() { return fabsf(cm) > 4096.f && cm > 0.999999f * kLowest; };   // not before its first key
+        // what happens to a row does not depend on the others of the wave
+        const bool over = is_wide() || !(pair_sum(sum) <= 1024.f);
         float tm = fmaxf(sc[hh][0], sc[hh][1]);
 #pragma unroll
         for (int i = 2; i < 16; ++i) tm = fmaxf(tm, sc[hh][i]);
-        const float mn = fmaxf(m[hh], pair_max(tm) * scale.c), f = __builtin_amdgcn_exp2f(m[hh] - mn);
+        tm = pair_max(tm);
+        const float mn = over ? fmaxf(m[hh], tm) : m[hh], f = __builtin_amdgcn_exp2f((m[hh] - mn) * scale.c);
         m[hh] = mn;
         l[hh] *= f;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) O[hh][mt][i] *= f;
-        exponentials();
+        cm = mn * scale.c;
+        const bool w = is_wide();
+        wide[hh] = __any(w);
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          p[i] = __builtin_amdgcn_exp2f(fmaf(sc[hh][i], scale.c, -cm));
+          sum += p[i];
+        }
+        if (w) {
+          sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            p[i] = __builtin_amdgcn_exp2f((sc[hh][i] - mn) * scale.c);
+            sum += p[i];
+          }
+        }
       }
       l[hh] += sum;
 #pragma unroll
@@ -174,7 +195,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
       sum[hh] = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        factor[hh][w] = __builtin_amdgcn_exp2f(join[(w * HG + hh) * S::kPart] - m[hh]);
+        factor[hh][w] = __builtin_amdgcn_exp2f((join[(w * HG + hh) * S::kPart] - m[hh]) * scale.c);
         sum[hh] = fmaf(join[(w * HG + hh) * S::kPart + 64], factor[hh][w], sum[hh]);
       }
     } else {
@@ -184,13 +205,13 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   if (q >= hi) return;
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
-    const bool none = sum[hh] == 0.f;      // NaN is not none: it has to show
+    const bool empty = sum[hh] == 0.f;     // NaN is not empty: it has to show
     const float inv = 1.f / sum[hh];
     if (a.lse && half == 0 && kw == 0)
-      a.lse[(size_t)(h0 + hh) * d.n_nodes + q] = none ? -INFINITY : (m[hh] + __builtin_amdgcn_logf(sum[hh])) * kLn2;
+      a.lse[(size_t)(h0 + hh) * d.n_nodes + q] = empty ? -INFINITY : (m[hh] * scale.c + __builtin_amdgcn_logf(sum[hh])) * kLn2;
     const auto store = [&](int gi, float v[4]) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = none ? 0.f : v[j] * inv;
+      for (int j = 0; j < 4; ++j) v[j] = empty ? 0.f : v[j] * inv;
       store4<T>(a.out, a.os, q, h0 + hh, D, half, gi / 4, gi % 4, v);
     };
     if (KW > 1) {

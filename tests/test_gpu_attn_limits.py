@@ -1,12 +1,14 @@
 """Attention at the ends of what its entry points accept: bucket ranges that pass the
-largest float.
+largest float, huge scores.
 
 Tolerances are those derived in test_gpu_attn.py, whose cases these are.
 """
 import numpy as np
 import pytest
 
-from .test_gpu_attn import Case, tpc  # noqa: F401  (tpc is the module's fixture)
+from oracle import layers as ol
+
+from .test_gpu_attn import Case, U, W, tpc  # noqa: F401  (tpc is the module's fixture)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -23,3 +25,40 @@ def test_bucket_ranges_that_pass_the_largest_float(tpc, dtype, r_min, steps, nb)
     far = 10.0 ** r.uniform(0, 20, size=(115, 1)) * r.normal(size=(115, 3))
     c.kw["pos"] = torch.tensor(far.astype(np.float32), device="cuda")
     c.check(tpc)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [-5e29, -1e12, -1e9, 1e9, 1e12])
+@pytest.mark.parametrize("n", [70, 300])
+def test_huge_scores_of_one_size(tpc, dtype, size, n):
+    """Every score is one huge bias: out is the mean of v."""
+    c = Case(dtype, [n], 2, 2, 16, nb=4, packed=False)
+    c.kw["bias"][:] = size
+    c.q[:] = 0
+    out, lse = tpc.attn_forward(c.q, c.k, c.v, c.segt, **c.kw)
+    v, bias = c.v.double(), float(c.kw["bias"][0, 0])
+    # n equal probabilities: sums of n terms in float32, one division, the type's rounding
+    tol = ((n + 4) * U + (W if dtype == "bf16" else 2 * U)) * v.abs().mean(0)
+    assert ((out.double() - v.mean(0)).abs() <= tol).all()
+    assert ((lse.double() - bias - np.log(n)).abs() <= 8 * U * abs(bias)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_huge_scores_of_some_rows_and_tiles(tpc, dtype):
+    """Biases of very different sizes in one row: the largest bucket of a row takes it all, wherever
+    its tile comes, and rows beside it are not disturbed."""
+    c = Case(dtype, [300], 2, 2, 16, nb=4, steps=1, packed=False)
+    c.q[:] = 0
+    c.kw["bias"][:] = torch.tensor([-1e12, -1e9, 3.0, -np.inf], device="cuda").to(c.kw["bias"].dtype)
+    # buckets: r_min = 0.5, one step an octave of d2: 0 below 0.71, 1 to 1, 2 to 1.41, 3 beyond
+    pos = torch.zeros(300, 3, device="cuda")
+    pos[:, 0] = 10 * (torch.arange(300, device="cuda") % 60)                  # rows p, p + 60 .. share a place
+    pos[60:120, 1], pos[180:240, 1] = 0.8, 1.2                                # 1, 2 from the first
+    c.kw["pos"] = pos
+    out, lse = tpc.attn_forward(c.q, c.k, c.v, c.segt, **c.kw)
+    h, kw, _ = c.host()
+    ref, rlse = ol.attn_forward(**h, **kw)
+    size = np.abs(h["v"]).max()
+    tol = 16 * U * size + (W if dtype == "bf16" else 0) * np.abs(ref)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - rlse) <= 8 * U * np.abs(rlse)).all()
