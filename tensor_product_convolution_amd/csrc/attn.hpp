@@ -228,6 +228,15 @@ struct Scale {
   }
 };
 
+// A row's lse in base-2 units, for p = exp2(c S - lse); a row without keys gets p = 0.
+// lse and this product are off by up to 4 2^-24 of their size.  From 2^22 on, where a score's own
+// rounding is half a unit, that may make p huge or, from 10^9 on, infinite (and 0 times it
+// NaN): there lse is raised by 8 2^-24 of its size, which keeps p below 1.
+__device__ __forceinline__ float row_lse(float e) {
+  const float x = e * kLog2e, size = fabsf(x);
+  return e == -INFINITY ? INFINITY : size > 4194304.f ? fmaf(size, 0x1p-21f, x) : x;
+}
+
 // LDS bias table of HG heads, [entry][HG][32], in units of S; 32 copies of every value,
 // so that the lanes of a half wave, each with a bucket of its own, read 32 different
 // banks.

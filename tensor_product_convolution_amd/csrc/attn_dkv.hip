@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
 
   typename S::Stage st;
   RowStager rows;
-  float slse = INFINITY, sdel = 0.f;
+  float slse = 0.f, sdel = 0.f;            // of the rows that were fetched last
   const int tid = kv * 64 + lane;          // among the threads that share a tile
   char* mine = lds + qs * S::kBufs * S::kBuf;
   const auto tiles_of = [&](int buf) { return reinterpret_cast<uint16_t*>(mine + buf * S::kBuf); };
@@ -125,10 +125,8 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
     rows.fetch(tid, d, biased, q0, hi, nullptr);
     if (tid < kTile) {
       const size_t at = (size_t)h * d.n_nodes + min(q0 + tid, hi - 1);
-      const float e = a.lse_in[at];
-      // rows past the end or without keys: p = exp2(s - inf) = 0
-      slse = q0 + tid < hi && e != -INFINITY ? e * kLog2e : INFINITY;
-      sdel = q0 + tid < hi ? a.delta[at] : 0.f;
+      slse = a.lse_in[at];
+      sdel = a.delta[at];
     }
   };
   TableFill<1, S::kThreads> fill;
@@ -149,8 +147,8 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
       st.stage(tiles_of(buf));
       rows.stage(tid, rows_of(buf));
       if (tid < kTile) {
-        stat_of(buf)[tid] = slse;
-        stat_of(buf)[kTile + tid] = sdel;
+        stat_of(buf)[tid] = rows.live ? row_lse(slse) : INFINITY;   // past the end: p = 0
+        stat_of(buf)[kTile + tid] = rows.live ? sdel : 0.f;
       }
     };
     __syncthreads();                       // the table

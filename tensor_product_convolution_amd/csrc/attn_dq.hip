@@ -97,9 +97,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (DqShape<T, KS, HG, NKV, QW, KW>
     }
     delta[hh] = pair_sum(s);
     const size_t at = (size_t)(h0 + hh) * d.n_nodes + qc;
-    const float e = a.lse_in[at];
-    // a row without keys has lse = -inf: p = exp2(s - inf) = 0
-    lse[hh] = q < hi && e != -INFINITY ? e * kLog2e : INFINITY;
+    lse[hh] = q < hi ? row_lse(a.lse_in[at]) : INFINITY;
   }
 
   constexpr bool kCorrect = P == 1;

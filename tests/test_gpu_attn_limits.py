@@ -62,3 +62,47 @@ def test_huge_scores_of_some_rows_and_tiles(tpc, dtype):
     tol = 16 * U * size + (W if dtype == "bf16" else 0) * np.abs(ref)
     assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
     assert (np.abs(lse.double().cpu().numpy() - rlse) <= 8 * U * np.abs(rlse)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-1e9, -3e9, -7e11, -5e29])
+@pytest.mark.parametrize("n", [40, 300])
+def test_rows_of_huge_negative_scores_leave_finite_gradients(tpc, dtype, low, n):
+    """A masked atom far from all others, where a finite large negative bias masks far pairs:
+    its row holds such scores only.  It has no upstream gradient, so nothing but its own out
+    and lse may differ from a bias of -inf, bit for bit."""
+    c = Case(dtype, [n, 33], 4, 2, 32, nb=16, steps=1, box=3.0)
+    c.kw["pos"][7] += 1e4
+    c.kw["key_mask"] = torch.ones(n + 33, dtype=torch.uint8, device="cuda")
+    c.kw["key_mask"][7] = 0
+    c.go[7] = 0
+    c.kw["bias"][:, 15] = -np.inf
+    c.run(tpc)
+    want = [c.out.clone(), c.lse.clone(), *(g.clone() for g in c.grads)]
+    assert torch.all(c.lse[:, 7] == -np.inf)
+    c.kw["bias"][:, 15] = low
+    c.run(tpc)
+    got = [c.out, c.lse, *c.grads]
+    assert torch.isfinite(c.out).all() and torch.isfinite(c.lse).all()
+    want[0][7], want[1][:, 7] = c.out[7], c.lse[:, 7]
+    for name, g, w in zip(("out", "lse", "grad_q", "grad_k", "grad_v", "grad_bias"), got, want):
+        assert torch.equal(g, w), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [-5e29, -1e12, -1e9, 1e9, 1e12])
+def test_probabilities_of_huge_scores_stay_below_one(tpc, dtype, size):
+    """Every score is one huge bias: 32 bits cannot hold the backward's probabilities there, but
+    they stay between 0 and 1."""
+    n, d = 70, 16
+    c = Case(dtype, [n], 2, 2, d, nb=4, packed=False)
+    c.kw["bias"][:] = size
+    c.q[:] = 0
+    c.run(tpc)
+    v, go = c.v.double(), c.go.double()
+    over = 1 + 2 ** -7
+    assert (c.grads[2].double().abs() <= over * go.abs().sum(0)).all()
+    # |ds| <= |dp| + |delta| for p <= 1
+    ds = (go.abs()[:, None] * (v.abs()[None] + v.abs().mean(0))).sum(-1)
+    assert (c.grads[0].double().abs() <= over * d ** -0.5 * torch.einsum("ijh,jhd->ihd", ds, c.k.double().abs())).all()
+    assert not c.grads[1].any() and torch.isfinite(c.grads[3]).all()
