@@ -33,7 +33,8 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4 lds_s4;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -1e30f;         // scores at or below count as masked
+// scores at or below -1e30 count as masked; a little above it, so that rounding lets none through
+constexpr float kLowest = -0.9999e30f;
 constexpr int kTile = 32;
 constexpr int kMaxBuckets = 64;
 

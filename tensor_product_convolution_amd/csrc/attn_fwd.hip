@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   bool wide[HG];                           // a row of the wave is far from 0 (below)
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
-    m[hh] = kLowest * kLn2 * scale.inv;
+    m[hh] = kLowest * scale.inv;
     wide[hh] = false;
     l[hh] = 0.f;
     clear<MT>(O[hh]);
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
       // far: probabilities up to 2^9 lose nothing, most tiles need no maximum at all, and
       // the accumulators are rescaled in few.  NaN takes this way in every tile.
       if (wide[hh] || __any(!(sum <= 512.f))) {
-        const auto is_wide = [&]() { return fabsf(cm) > 4096.f && cm > 0.999999f * kLowest; };   // not before its first key
+        const auto is_wide = [&]() { return fabsf(cm) > 4096.f && cm > 0.999999f * kLog2e * kLowest; };   // not before its first key
         // what happens to a row does not depend on the others of the wave
         const bool over = is_wide() || !(pair_sum(sum) <= 1024.f);
         float tm = fmaxf(sc[hh][0], sc[hh][1]);

@@ -1,5 +1,5 @@
 """Attention at the ends of what its entry points accept: bucket ranges that pass the
-largest float, huge scores.
+largest float, huge scores, where masked scores begin.
 
 Tolerances are those derived in test_gpu_attn.py, whose cases these are.
 """
@@ -106,3 +106,18 @@ def test_probabilities_of_huge_scores_stay_below_one(tpc, dtype, size):
     ds = (go.abs()[:, None] * (v.abs()[None] + v.abs().mean(0))).sum(-1)
     assert (c.grads[0].double().abs() <= over * d ** -0.5 * torch.einsum("ijh,jhd->ihd", ds, c.k.double().abs())).all()
     assert not c.grads[1].any() and torch.isfinite(c.grads[3]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_where_masked_scores_begin(tpc, dtype):
+    """Scores at or below -1e30 count as masked, those above do not."""
+    c = Case(dtype, [50], 2, 2, 16, nb=4, packed=False)
+    for size in (-1.01e30, -1e30):
+        c.kw["bias"][:] = size
+        c.run(tpc)
+        assert not c.out.any() and torch.all(c.lse == -np.inf) and not any(g.any() for g in c.grads)
+    c.kw["bias"][:] = -9.9e29
+    c.run(tpc)
+    mean = c.v.double().mean(0)
+    tol = (54 * U + (W if dtype == "bf16" else 2 * U)) * c.v.double().abs().mean(0)
+    assert ((c.out.double() - mean).abs() <= tol).all() and torch.isfinite(c.lse).all()
