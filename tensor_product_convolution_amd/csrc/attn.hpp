@@ -464,11 +464,19 @@ struct RowStager {
   }
 };
 
+// Between a wave's own LDS accesses where lanes read what other lanes wrote, or write again
+// what they read: the hardware executes a wave's LDS accesses in order, the fence keeps the
+// compiler to it (a wave barrier alone restrains scheduling only).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Walks the tiles of one group of waves: prepare(i) starts tile i's loads into registers,
 // stage(i, buffer) puts them into LDS, work(i, buffer) uses them.  A tile that several
 // waves share is staged one tile ahead into the other of two buffers, with one barrier
 // a tile, or, where LDS holds one buffer only, between two barriers.  A wave on its own
-// needs no barrier and one buffer (its LDS accesses are executed in order).  All groups
+// needs no barrier and one buffer.  All groups
 // of the workgroup take the same n.  The caller has done prepare(0), as early as it can.
 template <bool SHARED, int BUFS, typename Prepare, typename Stage, typename Work>
 __device__ __forceinline__ void walk(int n, Prepare&& prepare, Stage&& stage, Work&& work) {
@@ -485,10 +493,10 @@ __device__ __forceinline__ void walk(int n, Prepare&& prepare, Stage&& stage, Wo
   } else {
     for (int i = 0; i < n; ++i) {
       if (SHARED) __syncthreads();
-      else __builtin_amdgcn_wave_barrier();
+      else wave_sync();
       stage(0);
       if (SHARED) __syncthreads();
-      else __builtin_amdgcn_wave_barrier();
+      else wave_sync();
       if (i + 1 < n) prepare(i + 1);
       work(0);
     }

@@ -214,8 +214,7 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
     if (a.gbias) {
       // each wave sums its own columns, a lane per entry, 16 bytes at a time; lanes start at
       // different columns so that they read different banks
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       float s = 0.f;
       if (lane < nb) {
 #pragma unroll
@@ -224,8 +223,7 @@ __global__ void __launch_bounds__(64 * KV * QS, (DkvShape<T, KS, KV, QS>::kRegs 
           s += (v[0] + v[1]) + (v[2] + v[3]);
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      wave_sync();
       my_cols[lane] = s;
       __syncthreads();
       if ((int)threadIdx.x < nb) {
