@@ -88,15 +88,23 @@ __device__ __forceinline__ void to_frag(const float* x, Frag<1>& f) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f.p[0][j] = (__bf16)x[j];
 }
+// FAR: an infinity is split into (largest bfloat16, the same, infinity), not into infinity and NaN,
+// so that its products are infinite whatever the other operand's pieces are.
+template <bool FAR = false>
 __device__ __forceinline__ void to_frag(const float* x, Frag<3>& f) {
+  const auto upper = [](float v) {
+    return bits(FAR ? __builtin_amdgcn_fmed3f(v, -0x1.fep+127f, 0x1.fep+127f) : v) & 0xffff0000u;
+  };
   u4 h, m, l;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float a = x[2 * j], b = x[2 * j + 1];
-    const float ra = a - flt(bits(a) & 0xffff0000u), rb = b - flt(bits(b) & 0xffff0000u);
-    const float sa = ra - flt(bits(ra) & 0xffff0000u), sb = rb - flt(bits(rb) & 0xffff0000u);
-    h[j] = high_halves(bits(a), bits(b));
-    m[j] = high_halves(bits(ra), bits(rb));
+    const uint32_t ha = upper(a), hb = upper(b);
+    const float ra = a - flt(ha), rb = b - flt(hb);
+    const uint32_t ma = upper(ra), mb = upper(rb);
+    const float sa = ra - flt(ma), sb = rb - flt(mb);
+    h[j] = FAR ? high_halves(ha, hb) : high_halves(bits(a), bits(b));
+    m[j] = FAR ? high_halves(ma, mb) : high_halves(bits(ra), bits(rb));
     l[j] = high_halves(bits(sa), bits(sb));          // at most 8 bits left: exact
   }
   f.p[0] = __builtin_bit_cast(b8, h);
@@ -113,6 +121,7 @@ struct Raw<bf16_t> {
   __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const u4*>(p); }
   __device__ __forceinline__ void keep(bool k) { v = k ? v : u4{0, 0, 0, 0}; }
   __device__ __forceinline__ void negate() { v ^= 0x80008000u; }
+  template <bool FAR>
   __device__ __forceinline__ void frag(Frag<1>& f) const { f.p[0] = __builtin_bit_cast(b8, v); }
   __device__ __forceinline__ float at(int j) const { return (float)__builtin_bit_cast(b8, v)[j]; }
 };
@@ -131,9 +140,10 @@ struct Raw<float> {
     a = -a;
     b = -b;
   }
+  template <bool FAR>
   __device__ __forceinline__ void frag(Frag<3>& f) const {
     const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    to_frag(x, f);
+    to_frag<FAR>(x, f);
   }
   __device__ __forceinline__ float at(int j) const { return j < 4 ? a[j] : b[j - 4]; }
 };
@@ -167,10 +177,10 @@ __device__ __forceinline__ Frag<G::P> col_frag(const uint16_t* tile, int mt, int
 }
 
 // store eight consecutive values into a staged tile
-template <typename G, typename T>
+template <typename G, bool FAR, typename T>
 __device__ __forceinline__ void put(uint16_t* tile, int row, int col8, const Raw<T>& r) {
   Frag<G::P> f;
-  r.frag(f);
+  r.template frag<FAR>(f);
 #pragma unroll
   for (int p = 0; p < G::P; ++p)
     *reinterpret_cast<b8*>(tile + p * G::kPlane + row * G::kRow + 8 * col8) = f.p[p];
@@ -418,15 +428,20 @@ struct Stager {
       at[i] += array_of(chunk(i)) & 1 ? step1 : step0;
     }
   }
-  __device__ __forceinline__ void stage(uint16_t* tiles) {
+  __device__ __forceinline__ void stage(uint16_t* tiles, bool far = false) {
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) raw[i].keep(live[i] && byte[i] != 0);
     }
+    if (far) put_all<true>(tiles);
+    else put_all<false>(tiles);
+  }
+  template <bool FAR>
+  __device__ __forceinline__ void put_all(uint16_t* tiles) {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int c = chunk(i);
-      if (array_of(c) < kArrays) put<G>(tiles + array_of(c) * G::kElems, row_of(c), col_of(c), raw[i]);
+      if (array_of(c) < kArrays) put<G, FAR>(tiles + array_of(c) * G::kElems, row_of(c), col_of(c), raw[i]);
     }
   }
 };
@@ -510,7 +525,7 @@ constexpr int buffers(int bytes, int share, int groups) { return share > 1 && 2 
 // contraction elements 16 kk + 8 half ..
 template <typename T, int KS>
 __device__ __forceinline__ void own_rows(const void* p, int64_t stride, int r, int head, int D, int half, bool keep,
-                                         float sign, Frag<kPlanes<T>> f[KS]) {
+                                         float sign, Frag<kPlanes<T>> f[KS], bool far = false) {
 #pragma unroll
   for (int kk = 0; kk < KS; ++kk) {
     const int c = 16 * kk + 8 * half;
@@ -518,7 +533,8 @@ __device__ __forceinline__ void own_rows(const void* p, int64_t stride, int r, i
     w.load(static_cast<const T*>(p) + (size_t)r * stride + (size_t)head * D + (c < D ? c : 0));
     w.keep(keep && c < D && sign != 0.f);
     if (sign < 0.f) w.negate();
-    w.frag(f[kk]);
+    if (far) w.template frag<true>(f[kk]);
+    else w.template frag<false>(f[kk]);
   }
 }
 

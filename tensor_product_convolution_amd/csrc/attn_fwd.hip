@@ -34,17 +34,17 @@ struct FwdShape {
   static constexpr int kRegs = HG * (KS * G::P * 4 + G::MT * 16 + 16) + 60 + Stage::kChunks * (G::P == 1 ? 6 : 10);
 };
 
-template <typename T, int KS, int HG, int NKV, int QW, int KW>
-__global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW>::kRegs > 210 ? 1 : 2))
-    k_attn_fwd(AttnArgs a) {
+// One workgroup's queries.  Float32 operands are split with FAR or without; true: without, and
+// a sum came out that is not finite.
+template <bool FAR, typename T, int KS, int HG, int NKV, int QW, int KW>
+__device__ __forceinline__ bool attn_fwd(const AttnArgs& a, char* lds) {
   using S = FwdShape<T, KS, HG, NKV, QW, KW>;
   using G = Tile<T, KS>;
   constexpr int P = G::P, MT = G::MT;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   float* tbl = reinterpret_cast<float*>(lds + S::kWork);
   const tp_attn& d = a.d;
   int lo, hi, q0;
-  if (!find_tile(d, kTile * QW, blockIdx.x, lo, hi, q0)) return;
+  if (!find_tile(d, kTile * QW, blockIdx.x, lo, hi, q0)) return false;
   const int lane = threadIdx.x & 63, half = lane >> 5, wv = threadIdx.x >> 6;
   const int kw = wv % KW, qw = wv / KW;
   const int h0 = blockIdx.y * HG, rep = d.n_heads / d.n_kv_heads, D = d.head_dim;
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   }
   Frag<P> Q[HG][KS];
 #pragma unroll
-  for (int hh = 0; hh < HG; ++hh) own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, scale.sign, Q[hh]);
+  for (int hh = 0; hh < HG; ++hh) own_rows<T, KS>(a.q, a.qs, qc, h0 + hh, D, half, true, scale.sign, Q[hh], FAR);
 
   f16v O[HG][MT];
   float m[HG], l[HG];                      // running maximum of S and sum
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
   }
 
   const auto stage = [&](int buf) {
-    st.stage(tiles_of(buf));
+    st.stage(tiles_of(buf), FAR);
     rows.stage(tid, rows_of(buf));
   };
   fill.write(d, scale.inv, tbl);
@@ -173,6 +173,27 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
     }
   });
 
+  bool again = false;
+  if (P > 1 && !FAR) {
+    float t = 0.f;
+#pragma unroll
+    for (int hh = 0; hh < HG; ++hh)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (32 * mt + 8 * (i / 4) < 16 * KS) t = fmaf(O[hh][mt][i], 0.f, t);   // columns that are staged
+    again = __any(t != t);
+    if (QW * KW > 1) {
+      uint32_t* found = reinterpret_cast<uint32_t*>(lds);
+      __syncthreads();                     // the tiles have been read
+      if (lane == 0) found[wv] = again;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < QW * KW; ++w) again |= __builtin_amdgcn_readfirstlane(found[w]) != 0;
+    }
+  }
+
   // statistics of the row over all waves that share it
   float factor[HG][KW], sum[HG];
   float* join = reinterpret_cast<float*>(lds) + (size_t)qw * KW * HG * S::kPart + lane;
@@ -202,7 +223,7 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
       sum[hh] = pair_sum(l[hh]);
     }
   }
-  if (q >= hi) return;
+  if (q >= hi) return again;
 #pragma unroll
   for (int hh = 0; hh < HG; ++hh) {
     const bool empty = sum[hh] == 0.f;     // NaN is not empty: it has to show
@@ -228,6 +249,20 @@ __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW
         store(gi, v);
       }
     }
+  }
+  return again;
+}
+
+// The split of float32 operands turns infinities into NaN.  A workgroup that finds values which are
+// not finite walks again with the longer split that keeps them (in every walk it costs 3 %).
+template <typename T, int KS, int HG, int NKV, int QW, int KW>
+__global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW>::kRegs > 210 ? 1 : 2))
+    k_attn_fwd(AttnArgs a) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const bool again = attn_fwd<false, T, KS, HG, NKV, QW, KW>(a, lds);
+  if (kPlanes<T> > 1 && __any(again)) {
+    __syncthreads();
+    (void)attn_fwd<true, T, KS, HG, NKV, QW, KW>(a, lds);
   }
 }
 

@@ -1,5 +1,5 @@
 """Attention at the ends of what its entry points accept: bucket ranges that pass the
-largest float, huge scores, where masked scores begin.
+largest float, huge scores, where masked scores begin, infinite operands.
 
 Tolerances are those derived in test_gpu_attn.py, whose cases these are.
 """
@@ -121,3 +121,53 @@ def test_where_masked_scores_begin(tpc, dtype):
     mean = c.v.double().mean(0)
     tol = (54 * U + (W if dtype == "bf16" else 2 * U)) * c.v.double().abs().mean(0)
     assert ((c.out.double() - mean).abs() <= tol).all() and torch.isfinite(c.lse).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 40, 300])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf])
+def test_infinite_values_reach_out_as_infinities(tpc, dtype, n, bad):
+    """One infinite element of v: the outputs that it enters are infinite, all else, grad_v with
+    it, is bit for bit as before."""
+    c = Case(dtype, [n, 20], 2, 2, 40, nb=8, packed=False).run(tpc)
+    want, lse, gv = c.out.clone(), c.lse.clone(), c.grads[2].clone()
+    c.v[n // 2, 1, 11] = bad
+    c.run(tpc)
+    want[:n, 1, 11] = bad
+    assert torch.equal(c.out, want) and torch.equal(c.lse, lse) and torch.equal(c.grads[2], gv)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [40, 300])
+def test_infinite_keys_that_give_scores_of_minus_infinity(tpc, dtype, n):
+    """Such a key has no weight in any row: out and lse are those of a masked key.  An infinite
+    query on the other side of the sign leaves its own row empty."""
+    c = Case(dtype, [n, 20], 2, 2, 24, nb=8, packed=False)
+    c.q[:, :, 3] = c.q[:, :, 3].abs() + 0.25
+    c.kw["key_mask"] = torch.ones(n + 20, dtype=torch.uint8, device="cuda")
+    c.kw["key_mask"][n // 2] = 0
+    c.run(tpc)
+    want = [c.out.clone(), c.lse.clone()]
+    c.kw["key_mask"][n // 2] = 1
+    c.k[n // 2, :, 3] = -np.inf
+    got = tpc.attn_forward(c.q, c.k, c.v, c.segt, **c.kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    c.k[:, :, 3] = c.k[:, :, 3].abs() + 0.25
+    c.k[n // 2, :, 3] = 1
+    c.q[5, :, 3] = -np.inf
+    out, lse = tpc.attn_forward(c.q, c.k, c.v, c.segt, **c.kw)
+    assert not out[5].any() and torch.all(lse[:, 5] == -np.inf)
+    keep = torch.arange(n + 20, device="cuda") != 5
+    assert torch.isfinite(out[keep]).all() and torch.isfinite(lse[:, keep]).all()
+
+
+def test_largest_floats(tpc):
+    """Values beyond the largest bfloat16, which rounding to bfloat16 would make infinite, are
+    exact: a single key's value comes back bit for bit."""
+    c = Case("f32", [1] * 40, 2, 2, 16, packed=False)
+    c.q[:] = 0
+    c.v[:, 0, :] = torch.finfo(torch.float32).max
+    c.v[:, 1, :8] = -3.3961e38
+    c.v[:, 1, 8:] = 3.39e38
+    c.run(tpc)
+    assert torch.equal(c.out, c.v)
