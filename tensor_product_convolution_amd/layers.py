@@ -90,6 +90,15 @@ def _rows(t, name, dtype, shape, dev):
     return t.data_ptr(), strides[0] if shape[0] > 1 else want
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+# ctypes cuts an integer to the lower bits of a narrower argument without a word
+def _too_large(**sizes):
+    name, n = max(sizes.items(), key=lambda kv: kv[1])
+    raise ValueError(f"{name}: {n} is more than 32 bits hold")
+
+
 def _call(dev, f, *args):
     """The C entry point on the current stream of device ``dev``."""
     if torch._C._cuda_getDevice() == dev:
@@ -136,6 +145,8 @@ def _norm_forward(x, residual, gamma, beta, drop, eps):
         raise ValueError("x must be [rows, columns]")
     dtype, shape = x.dtype, x.shape
     n, c = shape
+    if c > _INT32_MAX:
+        _too_large(columns=c)
     px, xs = _rows(x, "x", dtype, shape, dev)
     pg = _need(gamma, "gamma", torch.float32, (c,), dev)
     pb = _need(beta, "beta", torch.float32, (c,), dev)
@@ -170,6 +181,8 @@ def _norm_backward(grad_y, h, gamma, mean, rstd, grad_res, drop, want_x, want_we
         raise ValueError("h must be [rows, columns]")
     dtype, shape = h.dtype, h.shape
     n, c = shape
+    if c > _INT32_MAX:
+        _too_large(columns=c)
     ph, hs = _rows(h, "h", dtype, shape, dev)
     py, ys = _rows(grad_y, "grad_y", dtype, shape, dev)
     pg = _need(gamma, "gamma", torch.float32, (c,), dev)
@@ -241,6 +254,8 @@ def _describe(q, k, v, seg_ptr, pos, bias, r_min, steps, key_mask, scale):
         pk = _need(key_mask, "key_mask", torch.uint8, (n,), dev)
     if scale is None:
         scale = d ** -0.5 if d else 1.0
+    if max(n, m - 1, hq, hk, d, nb, abs(steps)) > _INT32_MAX:
+        _too_large(nodes=n, structures=m - 1, heads=hq, key_heads=hk, head_dim=d, buckets=nb, steps=abs(steps))
     return _Attn(code, n, m - 1, hq, hk, d, pseg, pk, pp, pb, nb, steps, r_min, scale), dev, rows
 
 
