@@ -596,14 +596,16 @@ struct Extent {
 };
 
 // a launch with `bytes` of LDS, which above 64 KiB have to be asked for
-template <typename K, typename... A>
-hipError_t launch_lds(K kernel, dim3 grid, int threads, size_t bytes, hipStream_t st, A... args) {
+template <typename K>
+hipError_t launch_lds(K kernel, dim3 grid, int threads, size_t bytes, const AttnArgs& args) {
+  if ((uint64_t)grid.x * threads > UINT32_MAX) return hipErrorInvalidConfiguration;
+  if (args.dry) return hipSuccess;
   if (bytes > 64 * 1024) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)kLdsMax);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, grid, dim3(threads), bytes, st, args...);
+  hipLaunchKernelGGL(kernel, grid, dim3(threads), bytes, args.stream, args);
   return hipGetLastError();
 }
 

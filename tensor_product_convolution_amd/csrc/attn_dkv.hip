@@ -359,8 +359,8 @@ hipError_t launch(const AttnArgs& a) {
   using S = DkvShape<T, KS, KV, QS>;
   const int tiles = a.d.n_nodes / (kTile * KV) + a.d.n_segments;
   hipError_t e = launch_lds(k_attn_dkv<T, KS, KV, QS>, dim3(tiles, a.split ? a.d.n_heads : a.d.n_kv_heads), S::kThreads,
-                            S::lds_bytes(a.d.n_buckets), a.stream, a);
-  if (e != hipSuccess) return e;
+                            S::lds_bytes(a.d.n_buckets), a);
+  if (e != hipSuccess || a.dry) return e;
   if (a.split) {
     const int64_t n = (int64_t)a.d.n_nodes * a.d.n_kv_heads * 2 * (a.d.head_dim / 4);
     hipLaunchKernelGGL(k_attn_join_kv<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, a.stream, a);
@@ -417,9 +417,14 @@ hipError_t attn_backward(const AttnArgs& args) {
   AttnArgs a = args;
   a.split = split_heads(a.d);
   if (a.d.n_nodes == 0) return a.d.dtype == TP_F32 ? join_bias<float>(a, 0) : join_bias<bf16_t>(a, 0);
-  hipError_t e = attn_backward_q(a);       // also leaves delta for the key side
-  if (e != hipSuccess) return e;
-  return a.d.dtype == TP_F32 ? by_width<float>(a) : by_width<bf16_t>(a);
+  // both grids are checked before the first launch; the query side leaves delta for the key side
+  hipError_t e = hipSuccess;
+  for (const bool dry : {true, false}) {
+    a.dry = dry;
+    if ((e = attn_backward_q(a)) != hipSuccess) return e;
+    if ((e = a.d.dtype == TP_F32 ? by_width<float>(a) : by_width<bf16_t>(a)) != hipSuccess) return e;
+  }
+  return e;
 }
 
 AttnWorkspace attn_workspace(const tp_attn& d) {

@@ -207,7 +207,7 @@ template <typename T, int KS, int HG, int NKV, int QW, int KW>
 hipError_t launch(const AttnArgs& a) {
   using S = DqShape<T, KS, HG, NKV, QW, KW>;
   const dim3 grid((unsigned)(a.d.n_nodes / (kTile * QW) + a.d.n_segments), (unsigned)(a.d.n_heads / HG));
-  return launch_lds(k_attn_dq<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a.stream, a);
+  return launch_lds(k_attn_dq<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a);
 }
 
 // ---- which variant

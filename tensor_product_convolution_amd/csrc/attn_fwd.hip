@@ -270,7 +270,7 @@ template <typename T, int KS, int HG, int NKV, int QW, int KW>
 hipError_t launch(const AttnArgs& a) {
   using S = FwdShape<T, KS, HG, NKV, QW, KW>;
   const dim3 grid((unsigned)(a.d.n_nodes / (kTile * QW) + a.d.n_segments), (unsigned)(a.d.n_heads / HG));
-  return launch_lds(k_attn_fwd<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a.stream, a);
+  return launch_lds(k_attn_fwd<T, KS, HG, NKV, QW, KW>, grid, S::kThreads, S::lds_bytes(a.d.n_buckets), a);
 }
 
 // ---- which variant

@@ -60,8 +60,8 @@ tp_status check_attn(const char* where, const tp_attn* a) {
   if (!known(a->dtype)) return fail(where, "unknown element type");
   if (a->n_nodes < 0 || a->n_segments < 0) return fail(where, "negative size");
   if (a->n_nodes > 0 && a->n_segments == 0) return fail(where, "nodes without a structure");
-  // row numbers run up to eight tiles past the end, the grid has a tile for every 32 nodes
-  // and one for every structure
+  // row numbers run up to eight tiles past the end, tile numbers to one for every 32 nodes and
+  // one for every structure
   if (a->n_nodes > std::numeric_limits<int32_t>::max() - 4096 ||
       (int64_t)a->n_nodes / 32 + a->n_segments > std::numeric_limits<int32_t>::max())
     return fail(where, "too many nodes or structures for one launch", TP_ERR_OVERFLOW);
@@ -87,6 +87,13 @@ tp_status check_attn_pointers(const char* where, const tp_attn* a) {
   if (!aligned(a->seg_ptr, 4) || !aligned(a->pos, 4) || !aligned(a->bias, size_of(a->dtype)))
     return fail(where, "misaligned pointer");
   return TP_OK;
+}
+
+// the status of an attention launch
+tp_status launched(const char* where, hipError_t e) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(where, "too many nodes or structures for one launch", TP_ERR_OVERFLOW);
+  return e == hipSuccess ? TP_OK : tpc::hip_error(e, (std::string(where) + " launch").c_str());
 }
 
 struct Rows {
@@ -252,8 +259,7 @@ tp_status tp_attn_forward(const tp_attn* a, const void* q, int64_t q_stride, con
     args.os = out_stride;
     args.lse = lse;
     args.stream = stream;
-    hipError_t e = tpc::attn_forward(args);
-    return e == hipSuccess ? TP_OK : tpc::hip_error(e, "tp_attn_forward launch");
+    return launched(me, tpc::attn_forward(args));
   });
 }
 
@@ -316,8 +322,7 @@ tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, co
     args.part = args.delta + w.part;
     args.kv_part = args.delta + w.kv_part;
     args.stream = stream;
-    hipError_t e = tpc::attn_backward(args);
-    return e == hipSuccess ? TP_OK : tpc::hip_error(e, "tp_attn_backward launch");
+    return launched(me, tpc::attn_backward(args));
   });
 }
 

@@ -219,6 +219,8 @@ hipError_t norm_backward(const NormBwdArgs& a);
 hipError_t dropout_apply(int dtype, int64_t n, const void* x, const void* r, const DropArgs& d, void* out,
                          hipStream_t st);
 
+// The passes return hipErrorInvalidConfiguration, with nothing launched, where a grid would have
+// more threads in a dimension than 32 bits count.
 struct AttnArgs {
   tp_attn d;
   const void *q = nullptr, *k = nullptr, *v = nullptr, *out_in = nullptr, *go = nullptr;
@@ -228,6 +230,7 @@ struct AttnArgs {
   const float* lse_in = nullptr;
   float *delta = nullptr, *part = nullptr, *kv_part = nullptr;   // workspace of the backward
   bool split = false;                             // query heads that share a key head apart
+  bool dry = false;                               // the grid is checked, nothing launched
   hipStream_t stream = nullptr;
 };
 hipError_t attn_forward(const AttnArgs& a);
