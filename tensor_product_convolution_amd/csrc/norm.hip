@@ -365,7 +365,7 @@ template <typename T, bool RES>
 __global__ void __launch_bounds__(kThreads)
     k_dropout(int64_t n, const T* x, const T* r, DropArgs d, T* out) {
   constexpr int N = Chunk<T>::kN;
-  const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * N;
+  const int64_t e = (((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x) * N;
   if (e >= n) return;
   const int left = n - e < N ? (int)(n - e) : N;
   float v[N], q[N];
@@ -457,7 +457,9 @@ hipError_t norm_bwd(const NormBwdArgs& a) {
 template <typename T>
 hipError_t dropout(int64_t n, const void* x, const void* r, const DropArgs& d, void* out, hipStream_t st) {
   const int64_t per = (int64_t)kThreads * Chunk<T>::kN;
-  const dim3 grid((unsigned)((n + per - 1) / per));
+  // rows of 2^22 workgroups: a grid's dimension holds fewer than 2^32 threads
+  const int64_t blocks = (n + per - 1) / per, row = std::min<int64_t>(blocks, 1 << 22);
+  const dim3 grid((unsigned)row, (unsigned)((blocks + row - 1) / row));
   if (r)
     hipLaunchKernelGGL((k_dropout<T, true>), grid, dim3(kThreads), 0, st, n, (const T*)x, (const T*)r, d, (T*)out);
   else
