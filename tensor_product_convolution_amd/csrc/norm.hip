@@ -22,6 +22,7 @@ namespace tpc {
 namespace {
 
 constexpr int kThreads = 256;
+static_assert(kNormMaxCols <= 256 * 8 * Chunk<float>::kN && kNormMaxCols <= 256 * 4 * Chunk<bf16_t>::kN);
 
 // Sum of a (and b) over the TPR threads of a row, in a fixed order.
 template <int TPR>
@@ -409,8 +410,9 @@ hipError_t pick_shape(int n_cols, F&& f) {
   if (n <= 128) return pick_layout<64, 2>(whole, f);
   if (n <= 256) return pick_layout<kSmall ? 64 : 256, kSmall ? 4 : 1>(whole, f);
   if (n <= 512) return pick_layout<256, 2>(whole, f);
-  if (n <= 1024) return pick_layout<256, 4>(whole, f);
-  return pick_layout<256, 8>(whole, f);
+  if constexpr (kSmall)
+    if (n > 1024) return pick_layout<256, 8>(whole, f);
+  return pick_layout<256, 4>(whole, f);    // kNormMaxCols bfloat16 values are 1,024 chunks
 }
 
 // workgroups that walk the rows: enough waves to cover the latency, few enough that weights
