@@ -687,7 +687,8 @@ tp_status tp_layer_norm_backward(int32_t dtype, int64_t n_rows, int32_t n_cols, 
  * every operation rounded once, and bits() the float's representation,
  *   bucket = clamp((bits(d2) >> s) - (bits(r_min r_min) >> s), 0, n_buckets - 1),
  * s = 23 - log2(steps): `steps` linear steps in each octave of d2, all below r_min in
- * bucket 0, all beyond the range in the last.  pos NULL: no bias (bias NULL,
+ * bucket 0, all beyond the range in the last; a distance that is NaN (of a NaN
+ * position, or two infinite ones) counts as bucket 0.  pos NULL: no bias (bias NULL,
  * n_buckets 0).  The bias has no gradient with respect to the positions (it is
  * piecewise constant). */
 typedef struct {

@@ -11,7 +11,8 @@ LOWEST = -1e30          # scores at or below count as masked
 
 
 def buckets(pos, r_min, steps, n_buckets):
-    """[n, n] bucket of every pair of rows of pos (float32 [n, 3])."""
+    """[n, n] bucket of every pair of rows of pos (float32 [n, 3]); a distance that is not a
+    number has no bits to go by and counts as bucket 0."""
     p = np.asarray(pos, dtype=np.float32)
     shift = 23 - int(np.log2(steps))
     with np.errstate(invalid="ignore", over="ignore"):
@@ -20,7 +21,7 @@ def buckets(pos, r_min, steps, n_buckets):
         d2 = (sq[..., 0] + sq[..., 1]) + sq[..., 2]
     r = np.float32(r_min)
     base = int((r * r).view(np.int32)) >> shift
-    return np.clip((d2.view(np.int32).astype(np.int64) >> shift) - base, 0, n_buckets - 1)
+    return np.where(np.isnan(d2), 0, np.clip((d2.view(np.int32).astype(np.int64) >> shift) - base, 0, n_buckets - 1))
 
 
 def _probs(q, k, b, live, scale):

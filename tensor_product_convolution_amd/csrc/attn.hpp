@@ -309,7 +309,8 @@ struct Buckets {
     add = first - base * kEntry;
   }
   // the squared distance, every operation rounded once (no fused multiply-add).  It is
-  // clamped as a float: positive floats are ordered as their representations.
+  // clamped as a float: positive floats are ordered as their representations, and the median of NaN
+  // is the lower bound (bucket 0).
   __device__ __forceinline__ uint32_t address(float ax, float ay, float az, float bx, float by, float bz) const {
 #pragma clang fp contract(off)
     const float dx = ax - bx, dy = ay - by, dz = az - bz;

@@ -1,5 +1,6 @@
 """Attention at the ends of what its entry points accept: bucket ranges that pass the
-largest float, huge scores, where masked scores begin, infinite operands.
+largest float, huge scores, where masked scores begin, infinite operands,
+positions that are no numbers.
 
 Tolerances are those derived in test_gpu_attn.py, whose cases these are.
 """
@@ -171,3 +172,13 @@ def test_largest_floats(tpc):
     c.v[:, 1, 8:] = 3.39e38
     c.run(tpc)
     assert torch.equal(c.out, c.v)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_positions_that_are_not_numbers_count_as_the_first_bucket(tpc, dtype):
+    """NaN positions, and infinite ones on both sides of a pair."""
+    c = Case(dtype, [45, 70], 2, 2, 16, nb=8, box=4.0)
+    c.kw["pos"][4] = np.nan
+    c.kw["pos"][50, 1] = -np.nan
+    c.kw["pos"][60], c.kw["pos"][61] = np.inf, np.inf
+    c.check(tpc)
