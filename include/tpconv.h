@@ -610,8 +610,9 @@ tp_status tp_conv_sph_harm_backward(int32_t lmax, const float* r, int32_t n_edge
  *
  * Element types: TP_F32 or TP_BF16 for the arrays marked T below.  Sums, row
  * statistics and softmax statistics are held in 32 bits; each T output is
- * rounded once.  Arrays marked T need the alignment of their element only,
- * except where a comment asks for 16 bytes.  Deterministic: no atomics, fixed
+ * rounded once (what attention rounds before its products is said there).
+ * Arrays marked T need the alignment of their element only, except where a
+ * comment asks for 16 bytes.  Deterministic: no atomics, fixed
  * summation order. */
 #define TP_F32 0
 #define TP_BF16 1
@@ -682,6 +683,15 @@ tp_status tp_layer_norm_backward(int32_t dtype, int64_t n_rows, int32_t n_cols, 
  * below -1e30 count as masked (a bias of -inf or of the type's lowest value
  * masks its bucket).  Masked keys' rows of k and v are never multiplied: what
  * they hold, NaN included, reaches no output.
+ * Precision: in bfloat16 probabilities and score gradients are rounded to the type
+ * before they are multiplied with rows of v, k, q and grad_out (outputs are 1.4
+ * times as far off as by their own rounding alone).  In float32 a product leaves
+ * out up to 2^-21 of itself, towards zero.  The forward takes scores of any
+ * size; infinities in rows that count give what the formulas give.  The
+ * backward's probabilities, exp(s - lse), are off by up to 2.4e-7 |s| from lse's
+ * rounding alone; beyond |s| = 2.9e6, where a score itself is rounded by a quarter,
+ * they lie between 0 and 1 and mean no more.  In float32 its gradients are NaN where
+ * an infinite q, k, v or grad_out enters a product.
  * The bucket is a geometric step of the distance (positions as given, no
  * periodic images): with float32 dx = x_i - x_j, ..., d2 = (dx dx + dy dy) + dz dz,
  * every operation rounded once, and bits() the float's representation,
@@ -702,7 +712,7 @@ typedef struct {
   const void* bias;         /* T [n_heads][n_buckets] */
   int32_t n_buckets;        /* 1..64 */
   int32_t steps;            /* 1, 2, 4 or 8 */
-  float r_min;              /* > 0 */
+  float r_min;              /* 1e-15 to 1e15 */
   float scale;              /* 0, or 1e-8 to 1e8 in size */
 } tp_attn;
 
@@ -722,9 +732,13 @@ tp_status tp_attn_backward_workspace(const tp_attn* a, size_t* bytes);
  *   dp_ij = grad_out_i . v_j,  ds_ij = p_ij (dp_ij - grad_out_i . out_i)
  *   grad_q_i = scale sum_j ds_ij k_j;  grad_k_j, grad_v_j summed over the query
  *   heads that share the key head;  grad_bias[h][c] = sum of ds over bucket c.
- * out and lse are tp_attn_forward's.  grad_out, grad_q [n_nodes][n_heads][head_dim]
+ * out and lse are tp_attn_forward's, over all keys: every row of ds then sums to
+ * zero, and so do a head's buckets.  What rounding leaves of both sums is taken off
+ * (grad_bias as a whole, row sums in the key side's ds), so out and lse joined
+ * from softmaxes over parts of the keys give wrong gradients here.  grad_out, grad_q [n_nodes][n_heads][head_dim]
  * and grad_k, grad_v [n_nodes][n_kv_heads][head_dim] with their strides (16-byte
- * multiples as above), grad_bias T [n_heads][n_buckets] (NULL: skipped). */
+ * multiples as above), grad_bias T [n_heads][n_buckets] (NULL: skipped).  ws:
+ * tp_attn_backward_workspace bytes, 16-byte aligned. */
 tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, const void* k,
                            int64_t k_stride, const void* v, int64_t v_stride, const void* out,
                            int64_t out_stride, const float* lse, const void* grad_out,

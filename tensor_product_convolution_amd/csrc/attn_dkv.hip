@@ -9,6 +9,9 @@
 // shared and there are too few key tiles to fill the chip, every query head gets
 // workgroups of its own, whose float32 parts a second kernel adds up.
 //
+// bfloat16 rounds p and ds to the type for their products, as the forward does; the bias
+// gradient sums the unrounded ds.
+//
 // The bias gradient goes into LDS columns private to the lane (no two lanes add to
 // one word, so plain reads and writes do and the order of the sums is fixed), two
 // elements at a time, summed per workgroup and joined by a second kernel.  An LDS

@@ -2,6 +2,10 @@
 // One pass over the keys with a running maximum and sum per query (see attn.hpp
 // for the tile layout); HG heads share the tile's distances and buckets.
 //
+// bfloat16 probabilities are rounded to the type for p v, a choice: in two pieces (float32's
+// would be three) that product would be twice as long, and out, which is rounded to the type
+// itself, is 2.4e-3 off with and 1.7e-3 without.  The sum that divides it is of the unrounded ones.
+//
 // QW x KW waves: QW own 32 queries each and share staged keys, KW split the keys and
 // are joined through LDS at the end (for batches with few query tiles).
 //
