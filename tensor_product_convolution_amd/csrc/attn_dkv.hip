@@ -377,14 +377,22 @@ hipError_t launch(const AttnArgs& a) {
 // eight up to 32 buckets, four up to 64.  (us) 1,536 atoms, 5 heads of 64 (245 tiles),
 // float32: 1x4 78, 2x2 110; 1,536 atoms, 8 heads of 32, bfloat16: 2x4 40,
 // 2x2 58, 4x1 92; 4,096 atoms: 4x2 152, 2x4 169; 512 molecules of 62 atoms: 2x1 124, 2x2 215.
+// Eight waves leave a wave 256 registers, and wide heads spill.  Where waves split the queries
+// four or eight ways four waves then do better, whole backward, 8 to 20 buckets: 1,536 atoms,
+// 8 heads, float32, of 64: 2x4 207, 2x2 184, of 40: 178, 169 (of 32: 102, 122; bfloat16 of 64: 79,
+// 94); 1,100 atoms, 4 heads of 64, bfloat16: 1x8 51, 1x4 49 (of 48: 45, 47; float32 of 32: 57,
+// 60).  4x2 stays ahead with 125 registers spilled: 4,096 atoms, 8 heads of 64, float32: 818,
+// 2x2 881, 4x1 802; bfloat16: 291, 424, 401.
 template <typename T, int KS>
 hipError_t by_waves(const AttnArgs& a) {
   const Extent x(a.d, a.split ? a.d.n_heads : a.d.n_kv_heads);
   hipError_t e = hipSuccess;
-  // launched where LDS holds its tiles and the columns; not built where it never does
+  // launched where LDS holds its tiles and the columns; not built where it never does, nor
+  // where a split over eight waves spills
   const auto fits = [&](auto kv, auto qs) {
     using S = DkvShape<T, KS, kv(), qs()>;
-    if constexpr (S::lds_bytes(1) <= kLdsMax) {
+    constexpr bool kSpills = kv() * qs() == 8 && qs() > 2 && S::kRegs > 250;
+    if constexpr (S::lds_bytes(1) <= kLdsMax && !kSpills) {
       if (S::lds_bytes(a.d.n_buckets) <= kLdsMax) {
         e = launch<T, KS, kv(), qs()>(a);
         return true;

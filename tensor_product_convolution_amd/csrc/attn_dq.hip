@@ -225,7 +225,8 @@ hipError_t launch(const AttnArgs& a) {
 // Eight waves leave a wave 256 registers; a kernel that needs more (wide heads) would spill
 // its operands and takes four: 8,000 atoms, 8 heads of 128, bfloat16: 4x1 1,220, 8x1 3,508; of
 // 96: 1,012, 1,174; 2,000 atoms: of 128 2x2 93, 2x4 244, of 96 79, 95.  (float32 heads of 64
-// spill little and keep 2x4: 211 against 270 at 4,096 atoms.)
+// spill 51 registers at 2x4, 17 MiB of writes at 4,096 atoms, and keep it all the same: 211
+// against 270.)
 template <typename T, int KS, int HG, int NKV>
 hipError_t by_waves(const AttnArgs& a, const Extent& x) {
   constexpr bool kWide = DqShape<T, KS, HG, NKV, 2, 4>::kRegs > 250;
