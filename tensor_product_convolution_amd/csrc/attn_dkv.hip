@@ -20,9 +20,9 @@
 //
 // About 420 vector instructions a tile of 32 x 32 pairs and head, and nearly as many LDS
 // cycles; the columns (256 bytes a bucket and wave) keep it at one to two waves a SIMD,
-// which do not cover each other's latency (vector units 34 % busy, LDS 26 %).  1,536 atoms, 8 heads, 32 buckets: of 32, bfloat16 35 us, of 16, float32 49 us; 4,096
-// atoms, 4 query heads of 64 on one key head, 64 buckets, float32: 303 us (six products for
-// one: 113 TFLOP/s of float32 work).
+// which do not cover each other's latency (vector units 35 % busy, LDS 27 %).  1,536 atoms, 8 heads, 32 buckets: of 32, bfloat16 34 us, of
+// 16, float32 48 us; 4,096 atoms, 4 query heads of 64 on one key head, 64 buckets, float32: 300 us
+// (six products for one: 114 TFLOP/s of float32 work).
 #include "attn.hpp"
 
 namespace tpc {

@@ -11,11 +11,11 @@
 //
 // The vector units bound it, not the matrix units: a pair costs about 11 instructions for
 // its distance and bucket, shared by HG heads, and 6 a head around the exponential,
-// against one 32-cycle product per 32 x 32 x 16.  16,384 atoms, 8 heads of 64, bfloat16: 973 us
-// (565 TFLOP/s, 46 % of a large library product's rate; vector units 60 %, LDS 42 %, matrix
-// units 22 % busy at two waves a SIMD); 1,536 atoms, 8 heads: of 32, bfloat16 21 us, of 16,
+// against one 32-cycle product per 32 x 32 x 16.  16,384 atoms, 8 heads of 64, bfloat16: 986 us
+// (557 TFLOP/s, 45 % of a large library product's rate; vector units 59 %, LDS 41 %, matrix
+// units 22 % busy at two waves a SIMD); 1,536 atoms, 8 heads: of 32, bfloat16 22 us, of 16,
 // float32 30 us (192 workgroups: a quarter of the chip is idle); 4,096 atoms, 4 heads of 64,
-// float32 127 us (matrix units 32 %: six products for one).
+// float32 133 us (matrix units 31 %: six products for one).
 #include "attn.hpp"
 
 namespace tpc {
@@ -258,7 +258,8 @@ __device__ __forceinline__ bool attn_fwd(const AttnArgs& a, char* lds) {
 }
 
 // The split of float32 operands turns infinities into NaN.  A workgroup that finds values which are
-// not finite walks again with the longer split that keeps them (in every walk it costs 3 %).
+// not finite walks again with the longer split that keeps them.  The check takes 1 % of 4,096 atoms,
+// 4 heads of 64 (123 against 121 us), 3 % of 1,536, 8 heads of 16; the longer split in every walk 3 %.
 template <typename T, int KS, int HG, int NKV, int QW, int KW>
 __global__ void __launch_bounds__(64 * QW * KW, (FwdShape<T, KS, HG, NKV, QW, KW>::kRegs > 210 ? 1 : 2))
     k_attn_fwd(AttnArgs a) {
