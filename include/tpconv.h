@@ -719,7 +719,8 @@ typedef struct {
 /* Forward.  q, out [n_nodes] rows of n_heads x head_dim, k, v of n_kv_heads x
  * head_dim, T, each with its row stride in elements (views of one projected row
  * are fine); base pointers and strides in bytes must be multiples of 16 (TP_ERR_ARG).
- * lse float32 [n_heads][n_nodes]. */
+ * lse float32 [n_heads][n_nodes] (NULL: skipped).  Outputs, here and in the backward, must not
+ * overlap inputs. */
 tp_status tp_attn_forward(const tp_attn* a, const void* q, int64_t q_stride, const void* k,
                           int64_t k_stride, const void* v, int64_t v_stride, void* out,
                           int64_t out_stride, float* lse, hipStream_t stream);
