@@ -686,9 +686,9 @@ tp_status tp_layer_norm_backward(int32_t dtype, int64_t n_rows, int32_t n_cols, 
  * Precision: in bfloat16 probabilities and score gradients are rounded to the type
  * before they are multiplied with rows of v, k, q and grad_out (outputs are 1.4
  * times as far off as by their own rounding alone).  In float32 a product leaves
- * out up to 2^-21 of itself, towards zero.  The forward takes scores of any
- * size; infinities in rows that count give what the formulas give.  The
- * backward's probabilities, exp(s - lse), are off by up to 2.4e-7 |s| from lse's
+ * out up to 2^-21 of itself, towards zero.  The forward takes scores of any size
+ * (s / |scale| has to be a float32); infinities in rows that count give what the
+ * formulas give.  The backward's probabilities, exp(s - lse), are off by up to 2.4e-7 |s| from lse's
  * rounding alone; beyond |s| = 2.9e6, where a score itself is rounded by a quarter,
  * they lie between 0 and 1 and mean no more.  In float32 its gradients are NaN where
  * an infinite q, k, v or grad_out enters a product.
