@@ -423,7 +423,8 @@ def run(s):
     if op == "experts":
         weight, index = tpc.route_forward(s["logits"], case["k"])
         groups = tpc.group_rows(index, case["experts"])
-        h, z = tpc.grouped_linear_forward(s["x"], s["w1"], groups, bias=s["b1"], act="silu", y_rows="grouped", want_pre=case["step"])
+        h = tpc.grouped_linear_forward(s["x"], s["w1"], groups, bias=s["b1"], act="silu", y_rows="grouped", want_pre=case["step"])
+        h, z = h if case["step"] else (h, None)
         y = tpc.grouped_linear_forward(h, s["w2"], groups, x_rows="grouped")
         out = [weight, index, tpc.combine_forward(y, weight)]
         if case["step"]:
