@@ -747,6 +747,192 @@ tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, co
                            int64_t gk_stride, void* grad_v, int64_t gv_stride, void* grad_bias,
                            void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- norm and rotation of queries and keys ------------------------------------
+ * In front of tp_attn: each head of q and k is normed over its head_dim values and the pairs
+ * of its first 2 n_pairs values are turned by angles that depend on the row's position, in
+ * one pass:
+ *   r = 1 / sqrt(mean(x^2) + eps),  y = x r gamma         (gamma_q, gamma_k; both NULL: y = x)
+ *   t_i = sum_a pos[a] freq[i][a]                         (axes 1 to 3; freq in radians)
+ *   (y_a, y_b) -> (y_a cos t_i - y_b sin t_i, y_a sin t_i + y_b cos t_i)
+ * for pair i = (i, n_pairs + i), or (2 i, 2 i + 1) where interleaved; values from 2 n_pairs on are
+ * only normed, n_pairs 0 turns nothing.  A product of two such rows depends on the difference of
+ * their positions alone: with wave vectors as freq and atoms' coordinates, scores do not change as the
+ * structure moves, nor from one periodic image to the next where the wave vectors are
+ * reciprocal lattice vectors; with one axis and falling frequencies it is the rotation by place in a
+ * chain.  Positions are float32 or int32 (TP_POS_*).  Angles are formed in 64 bits (a place of
+ * 2^28 keeps its angle to 1e-7), everything else in 32, outputs are rounded once. */
+#define TP_POS_F32 0
+#define TP_POS_I32 1
+typedef struct {
+  int32_t dtype;                        /* of q, k, their outputs and gradients */
+  int32_t n_heads, n_kv_heads, head_dim; /* heads 1..1024 each, head_dim 1..256 */
+  int64_t n_rows;
+  const float *gamma_q, *gamma_k;       /* [head_dim], both or none */
+  float eps;                            /* finite, >= 0 */
+  int32_t pos_type, axes;               /* axes 1..3 */
+  const void* pos;                      /* [n_rows][axes]; NULL where n_pairs is 0 */
+  const double* freq;                   /* [n_pairs][axes] */
+  int32_t n_pairs;                      /* 0..head_dim / 2 */
+  int32_t interleaved;                  /* 0 or 1 */
+} tp_heads;
+
+/* q, q_out [n_rows] rows of n_heads x head_dim, k, k_out of n_kv_heads x head_dim, T, each with
+ * its row stride in elements (views of one projected row are fine).  q_out may be q
+ * and k_out k (with the same stride); otherwise outputs must not overlap inputs. */
+tp_status tp_head_norm_rotate_forward(const tp_heads* h, const void* q, int64_t q_stride, const void* k,
+                                      int64_t k_stride, void* q_out, int64_t qo_stride, void* k_out,
+                                      int64_t ko_stride, hipStream_t stream);
+
+/* Workspace bytes of tp_head_norm_rotate_backward (partial sums of the weight gradients; pointers
+ * unused). */
+tp_status tp_head_norm_rotate_workspace(const tp_heads* h, size_t* bytes);
+
+/* Backward of the above from grad_qo, grad_ko, the gradients of q_out and k_out: grad_q, grad_k
+ * (T, with strides; may take the place of grad_qo, grad_ko), grad_gamma_q, grad_gamma_k
+ * (float32 [head_dim], both or none NULL, summed over rows and heads) and grad_pos (float32
+ * [n_rows][axes], NULL: skipped; float32 positions only).  q and k are read again, no statistics are
+ * kept. */
+tp_status tp_head_norm_rotate_backward(const tp_heads* h, const void* grad_qo, int64_t gqo_stride,
+                                       const void* grad_ko, int64_t gko_stride, const void* q,
+                                       int64_t q_stride, const void* k, int64_t k_stride, void* grad_q,
+                                       int64_t gq_stride, void* grad_k, int64_t gk_stride,
+                                       float* grad_gamma_q, float* grad_gamma_k, float* grad_pos,
+                                       void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- products grouped by element or expert ---------------------------------------
+ * Linear layers whose weights depend on the row: on the chemical element of the atom, or on the
+ * experts that a router chooses for it.  An entry of `index` is a slot: slot s chooses a group for
+ * source row s / fan (fan 1: one group for each row, as for elements).
+ *
+ * The k groups of largest logit of each row (1 <= k <= 16, k <= n_groups <= 1024), the
+ * lowest group first among equals, in falling order, with
+ *   weight = softmax of the logits over the chosen   (over_all 0)
+ *          = softmax over all groups, at the chosen  (over_all 1)
+ * logits T [n_rows] with a row stride; weight float32, index int32, [n_rows][k].  Logits of -inf or NaN
+ * are never chosen: choices that are left over get index -1 and weight 0. */
+tp_status tp_route_forward(int32_t dtype, int64_t n_rows, int32_t n_groups, int32_t k, int32_t over_all,
+                           const void* logits, int64_t logits_stride, float* weight, int32_t* index,
+                           hipStream_t stream);
+
+/* grad_logits T [n_rows][n_groups] (contiguous, all written) from grad_weight float32 [n_rows][k]:
+ * grad l_j = w_j sum_i w_i (gw_j - gw_i), over all groups with gw = 0 for those not chosen.
+ * weight and index are the forward's, logits its input (read where over_all; may be NULL
+ * otherwise). */
+tp_status tp_route_backward(int32_t dtype, int64_t n_rows, int32_t n_groups, int32_t k, int32_t over_all,
+                            const void* logits, int64_t logits_stride, const float* weight,
+                            const int32_t* index, const float* grad_weight, void* grad_logits,
+                            hipStream_t stream);
+
+/* The slots in group order: rows [n] int32 holds the slots of group 0, then those of group 1, ...,
+ * each in ascending order, behind them those whose index is no group (negative or >= n_groups);
+ * ptr [n_groups + 1] int32 the groups' offsets.  n < 2^31, n_groups 1..1024.  ws:
+ * tp_group_workspace bytes (0 for few slots). */
+tp_status tp_group_workspace(int64_t n, int32_t n_groups, size_t* bytes);
+tp_status tp_group_rows(const int32_t* index, int64_t n, int32_t n_groups, int32_t* ptr, int32_t* rows,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* A product by group.  Rows of x: source rows (TP_ROWS_SOURCE: slot s reads row s / fan), or one row
+ * for each slot, in group order (TP_ROWS_GROUPED).  Rows of y: by slot (TP_ROWS_SOURCE), or in group
+ * order.  Slots without a group read nothing and get rows of zeros.  ptr and rows are
+ * tp_group_rows'; entries out of range are clamped, so wrong arrays give meaningless results but no
+ * access out of bounds.
+ * Precision: sums in 32 bits; bfloat16 operands are multiplied exactly; of a float32 product up
+ * to 2^-21 of itself is left out, towards zero (0.7 2^-24 on average). */
+#define TP_ROWS_SOURCE 0
+#define TP_ROWS_GROUPED 1
+#define TP_ACT_NONE 0
+#define TP_ACT_SILU 1
+typedef struct {
+  int32_t dtype;             /* of x, y, w, bias and their gradients */
+  int32_t n_groups, n_in, n_out;
+  int64_t n_slots;           /* < 2^31, a multiple of fan */
+  int32_t fan;               /* slots of a source row */
+  int32_t x_rows, y_rows;    /* TP_ROWS_* */
+  const int32_t* ptr;        /* [n_groups + 1] */
+  const int32_t* rows;       /* [n_slots] */
+  const void* w;             /* T [n_groups][n_in][n_out] */
+} tp_grouped;
+
+/* z_s = x_row(s) w[e(s)] + bias[e(s)] (bias T [n_groups][n_out] or NULL), y = act(z).  With
+ * TP_ACT_SILU, y = z / (1 + exp(-z)) of z rounded to T, and z is written to pre (NULL: not; y's rows and
+ * stride).  Outputs must not overlap inputs. */
+tp_status tp_grouped_linear_forward(const tp_grouped* g, const void* x, int64_t x_stride, const void* bias,
+                                    int32_t act, void* y, int64_t y_stride, void* pre, hipStream_t stream);
+
+/* Workspace bytes of tp_grouped_linear_backward with these outputs (pointers unused). */
+tp_status tp_grouped_linear_workspace(const tp_grouped* g, int32_t want_x, int32_t want_w, size_t* bytes);
+
+/* Backward from grad_z, the gradient of z (y's rows; of y itself without an activation):
+ *   grad_x = grad_z w^T, summed over the slots of a source row (each slot's part rounded to T first);
+ *            times silu'(pre) where pre is given: x = silu(pre), pre with x's rows (fan 1 or grouped
+ *            rows), so that grad_x is the grad_z of the product in front
+ *   grad_w[e] = sum over the group's slots of x^T grad_z,  grad_bias[e] = sum of grad_z
+ * grad_x (gx_stride n_in where source rows have several slots), grad_w, grad_bias: NULL: skipped;
+ * grad_bias goes with grad_w.  Groups without slots get zeros.  ws: 16-byte aligned. */
+tp_status tp_grouped_linear_backward(const tp_grouped* g, const void* grad_z, int64_t gz_stride,
+                                     const void* x, int64_t x_stride, const void* pre, int64_t pre_stride,
+                                     void* grad_x, int64_t gx_stride, void* grad_w, void* grad_bias,
+                                     void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* out[n] = sum_j weight[n][j] y[n k + j] (weight NULL: 1), k >= 1; y T [n_rows k][n_cols], out T
+ * [n_rows][n_cols], contiguous. */
+tp_status tp_combine_forward(int32_t dtype, int64_t n_rows, int32_t k, int32_t n_cols, const void* y,
+                             const float* weight, void* out, hipStream_t stream);
+/* grad_y[n k + j] = weight[n][j] grad_out[n],  grad_weight[n][j] = grad_out[n] . y[n k + j] */
+tp_status tp_combine_backward(int32_t dtype, int64_t n_rows, int32_t k, int32_t n_cols, const void* grad_out,
+                              const void* y, const float* weight, void* grad_y, float* grad_weight,
+                              hipStream_t stream);
+
+/* ---- the AdamW step ---------------------------------------------------------------
+ * One step over many tensors:
+ *   t = t + 1;  G = g min(1, max_norm / |g|), |g| the 2-norm over all gradients (max_norm 0: G = g)
+ *   m = beta1 m + (1 - beta1) G,  v = beta2 v + (1 - beta2) G^2
+ *   p = p (1 - lr decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * Where max_norm is given (+inf: only the norm is taken) and the norm is not finite, the step changes
+ * nothing but *norm.  Without it a gradient that is not finite reaches its parameter and state.
+ *
+ * States lie in arrays over all tensors, each tensor from a multiple of 256 values on, in order; what
+ * lies between holds zeros.  bits 32: float32.  bits 8: one byte a value, and a float32 unit for
+ * each 256: value = unit x code's value, unit = max / 1.875 (rounded to float32); code c of a second
+ * moment (0..255): c 2^-33 below 8, else 2^(c / 8 - 31) (1 + c % 8 / 8); of a first moment
+ * bit 7 is the sign and c = code & 127: c 2^-17 below 8, else 2^(c / 8 - 15) (1 + c % 8 / 8).  A
+ * value between two codes takes the upper one where its share of the way plus u / 65536 reaches
+ * 1; u: the lower (first moment) or upper (second) 16 bits of word i % 4 of block i / 4 of the
+ * generator of tp_dropout with key seed and offset t, i the value's place in the state array.
+ * A second moment above zero has code 1 at least.  The parameter's step uses the moments before they
+ * are rounded.
+ *
+ * Helper: bytes of the table, values of a state array, bytes of the workspace, for tensors of these
+ * sizes (host array). */
+tp_status tp_adamw_sizes(int32_t n_tensors, const int64_t* sizes, size_t* table_bytes,
+                         int64_t* state_values, size_t* ws_bytes);
+/* Fills a host buffer of table_bytes, which the caller copies to the device: params float32, copies
+ * (bfloat16 of each parameter, written by the step; the array or entries may be NULL), decay (NULL: 0).
+ * Tensors must not overlap. */
+tp_status tp_adamw_table(int32_t n_tensors, const int64_t* sizes, void* const* params, void* const* copies,
+                         const float* decay, void* host_table);
+
+typedef struct {
+  int32_t bits, grad_dtype, n_tensors;
+  const int64_t* sizes;      /* host, as given to tp_adamw_table */
+  const void* table;         /* device */
+  void *m, *v;               /* device: float32, or uint8 where bits is 8 */
+  float *m_unit, *v_unit;    /* device, bits 8: [state_values / 256] */
+  double beta1, beta2;       /* [0, 1) */
+  double eps, lr, max_norm;  /* eps, max_norm >= 0 */
+  const float* lr_at;        /* device: the rate is read there; NULL: lr */
+  uint64_t seed;
+  void* scalars;             /* device, 64 bytes, zeros before the first step; the first 8 are t */
+} tp_adamw;
+
+/* grads: host array of n_tensors device pointers (of grad_dtype).  norm: device float32, NULL: not
+ * wanted; written where max_norm > 0.  m, v, table, scalars and ws 16-byte aligned. */
+tp_status tp_adamw_step(const tp_adamw* a, const void* const* grads, float* norm, void* ws, size_t ws_bytes,
+                        hipStream_t stream);
+/* The values of n (a multiple of 256) 8-bit states, second != 0: of second moments. */
+tp_status tp_adamw_values(int32_t second, int64_t n, const uint8_t* codes, const float* units, float* out,
+                          hipStream_t stream);
+
 /* Thread-local description of the last failure on this thread (helper for
  * error reporting; valid until the next failing call on the thread). */
 const char* tp_conv_last_error(void);

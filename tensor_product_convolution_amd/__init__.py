@@ -40,6 +40,10 @@ EXPORTS = (
     "tp_conv_gaunt_double_workspace", "tp_conv_double_backward_gaunt",
     "tp_dropout_apply", "tp_layer_norm_forward", "tp_layer_norm_workspace", "tp_layer_norm_backward",
     "tp_attn_forward", "tp_attn_backward_workspace", "tp_attn_backward",
+    "tp_head_norm_rotate_forward", "tp_head_norm_rotate_workspace", "tp_head_norm_rotate_backward",
+    "tp_route_forward", "tp_route_backward", "tp_group_workspace", "tp_group_rows", "tp_grouped_linear_forward",
+    "tp_grouped_linear_workspace", "tp_grouped_linear_backward", "tp_combine_forward", "tp_combine_backward",
+    "tp_adamw_sizes", "tp_adamw_table", "tp_adamw_step", "tp_adamw_values",
     "tp_conv_last_error",
 )
 
@@ -138,6 +142,22 @@ def lib():
         "tp_attn_forward": (I32, [VP] + [VP, I64] * 4 + [VP, VP]),
         "tp_attn_backward_workspace": (I32, [VP, ctypes.POINTER(SZ)]),
         "tp_attn_backward": (I32, [VP] + [VP, I64] * 4 + [VP] + [VP, I64] * 4 + [VP, VP, SZ, VP]),
+        "tp_head_norm_rotate_forward": (I32, [VP] + [VP, I64] * 4 + [VP]),
+        "tp_head_norm_rotate_workspace": (I32, [VP, ctypes.POINTER(SZ)]),
+        "tp_head_norm_rotate_backward": (I32, [VP] + [VP, I64] * 6 + [VP, VP, VP, VP, SZ, VP]),
+        "tp_route_forward": (I32, [I32, I64, I32, I32, I32, VP, I64, VP, VP, VP]),
+        "tp_route_backward": (I32, [I32, I64, I32, I32, I32, VP, I64, VP, VP, VP, VP, VP]),
+        "tp_group_workspace": (I32, [I64, I32, ctypes.POINTER(SZ)]),
+        "tp_group_rows": (I32, [VP, I64, I32, VP, VP, VP, SZ, VP]),
+        "tp_grouped_linear_forward": (I32, [VP, VP, I64, VP, I32, VP, I64, VP, VP]),
+        "tp_grouped_linear_workspace": (I32, [VP, I32, I32, ctypes.POINTER(SZ)]),
+        "tp_grouped_linear_backward": (I32, [VP] + [VP, I64] * 4 + [VP, VP, VP, SZ, VP]),
+        "tp_combine_forward": (I32, [I32, I64, I32, I32, VP, VP, VP, VP]),
+        "tp_combine_backward": (I32, [I32, I64, I32, I32, VP, VP, VP, VP, VP, VP]),
+        "tp_adamw_sizes": (I32, [I32, VP, ctypes.POINTER(SZ), ctypes.POINTER(I64), ctypes.POINTER(SZ)]),
+        "tp_adamw_table": (I32, [I32, VP, VP, VP, VP, VP]),
+        "tp_adamw_step": (I32, [VP, VP, VP, VP, SZ, VP]),
+        "tp_adamw_values": (I32, [I32, I64, VP, VP, VP, VP]),
         "tp_conv_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -952,10 +972,13 @@ def radial_workspace(plan, n_nodes, with_mix):
     return b.value
 
 
-# Attention, layer norm and dropout (layers.py), loaded on first use: plans and CG tables
-# need no torch.
+# Attention, layer norm and dropout (layers.py) and what stands around them (blocks.py), loaded on
+# first use: plans and CG tables need no torch.
 _LAYERS = ("Dropout", "attn_forward", "attn_backward", "layer_norm_forward", "layer_norm_backward",
            "layer_norm_residual_forward", "layer_norm_residual_backward", "dropout_forward", "dropout_backward")
+_BLOCKS = ("rotary_frequencies", "head_norm_rotate_forward", "head_norm_rotate_backward", "Groups", "route_forward",
+           "route_backward", "group_rows", "grouped_linear_forward", "grouped_linear_backward", "combine_forward",
+           "combine_backward", "AdamW")
 
 
 def __getattr__(name):
@@ -963,8 +986,12 @@ def __getattr__(name):
         from . import layers
         globals().update({n: getattr(layers, n) for n in _LAYERS})
         return globals()[name]
+    if name in _BLOCKS:
+        from . import blocks
+        globals().update({n: getattr(blocks, n) for n in _BLOCKS})
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_LAYERS})
+    return sorted({*globals(), *_LAYERS, *_BLOCKS})

@@ -3,35 +3,16 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <exception>
-#include <limits>
-#include <string>
 
-#include "internal.hpp"
+#include "capi_checks.hpp"
 
-using tpc::set_error;
+using namespace tpc;
 
 namespace {
 
-tp_status fail(const char* where, const char* what, tp_status code = TP_ERR_ARG) {
-  return set_error(code, std::string(where) + ": " + what);
-}
+constexpr const char* kTooMany = "too many nodes or structures for one launch";
 
-// No exception leaves a C entry point.
-template <typename F>
-tp_status guarded(F&& f) noexcept {
-  try {
-    return f();
-  } catch (...) {
-    return TP_ERR_HIP;
-  }
-}
-
-bool known(int32_t dtype) { return dtype == TP_F32 || dtype == TP_BF16; }
-int64_t size_of(int32_t dtype) { return dtype == TP_F32 ? 4 : 2; }
-bool aligned(const void* p, int64_t to) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(to - 1)) == 0; }
-
-tp_status check_drop(const char* where, const tp_dropout* d, tpc::DropArgs* out) {
+tp_status check_drop(const char* where, const tp_dropout* d, DropArgs* out) {
   if (!(d->p >= 0.0 && d->p < 1.0)) return fail(where, "dropout probability must be in [0, 1)");
   out->k0 = (uint32_t)d->seed;
   out->k1 = (uint32_t)(d->seed >> 32);
@@ -45,13 +26,9 @@ tp_status check_drop(const char* where, const tp_dropout* d, tpc::DropArgs* out)
 tp_status check_rows(const char* where, int32_t dtype, int64_t n_rows, int32_t n_cols) {
   if (!known(dtype)) return fail(where, "unknown element type");
   if (n_rows < 0 || n_cols < 0) return fail(where, "negative size");
-  if (n_cols < 1 || n_cols > tpc::kNormMaxCols) return fail(where, "rows of 1 to 8192 values only", TP_ERR_UNSUPPORTED);
+  if (n_cols < 1 || n_cols > kNormMaxCols) return fail(where, "rows of 1 to 8192 values only", TP_ERR_UNSUPPORTED);
   if (n_rows > std::numeric_limits<int64_t>::max() / 64 / n_cols) return fail(where, "too many rows", TP_ERR_OVERFLOW);
   return TP_OK;
-}
-
-bool bad_stride(int64_t stride, int64_t cols, int64_t rows) {
-  return stride < cols || (rows > 0 && stride > std::numeric_limits<int64_t>::max() / 8 / rows);
 }
 
 // sizes and options of an attention description (no pointers)
@@ -89,13 +66,6 @@ tp_status check_attn_pointers(const char* where, const tp_attn* a) {
   return TP_OK;
 }
 
-// the status of an attention launch
-tp_status launched(const char* where, hipError_t e) {
-  if (e == hipErrorInvalidConfiguration)
-    return fail(where, "too many nodes or structures for one launch", TP_ERR_OVERFLOW);
-  return e == hipSuccess ? TP_OK : tpc::hip_error(e, (std::string(where) + " launch").c_str());
-}
-
 struct Rows {
   const void* p;
   int64_t stride;
@@ -127,11 +97,11 @@ tp_status tp_dropout_apply(int32_t dtype, int64_t n, const void* x, const void* 
     if (n >= (int64_t)1 << 40) return fail(me, "too many elements for one launch", TP_ERR_OVERFLOW);
     const int64_t es = size_of(dtype);
     if (!aligned(x, es) || !aligned(residual, es) || !aligned(out, es)) return fail(me, "misaligned pointer");
-    tpc::DropArgs d;
+    DropArgs d;
     tp_status s = check_drop(me, drop, &d);
     if (s != TP_OK || n == 0) return s;
-    hipError_t e = tpc::dropout_apply(dtype, n, x, residual, d, out, stream);
-    return e == hipSuccess ? TP_OK : tpc::hip_error(e, "tp_dropout_apply launch");
+    hipError_t e = dropout_apply(dtype, n, x, residual, d, out, stream);
+    return e == hipSuccess ? TP_OK : hip_error(e, "tp_dropout_apply launch");
   });
 }
 
@@ -152,7 +122,7 @@ tp_status tp_layer_norm_forward(int32_t dtype, int64_t n_rows, int32_t n_cols, c
     if (!aligned(x, es) || !aligned(residual, es) || !aligned(y, es) || !aligned(h, es) || !aligned(gamma, 4) ||
         !aligned(beta, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
       return fail(me, "misaligned pointer");
-    tpc::NormArgs a;
+    NormArgs a;
     if (drop && (s = check_drop(me, drop, &a.drop)) != TP_OK) return s;
     if (n_rows == 0) return TP_OK;
     a.dtype = dtype;
@@ -171,8 +141,8 @@ tp_status tp_layer_norm_forward(int32_t dtype, int64_t n_rows, int32_t n_cols, c
     a.mean = mean;
     a.rstd = rstd;
     a.stream = stream;
-    hipError_t e = tpc::norm_forward(a);
-    return e == hipSuccess ? TP_OK : tpc::hip_error(e, "tp_layer_norm_forward launch");
+    hipError_t e = norm_forward(a);
+    return e == hipSuccess ? TP_OK : hip_error(e, "tp_layer_norm_forward launch");
   });
 }
 
@@ -180,7 +150,7 @@ tp_status tp_layer_norm_workspace(int32_t dtype, int64_t n_rows, int32_t n_cols,
   return guarded([&]() -> tp_status {
     if (!bytes) return fail("tp_layer_norm_workspace", "bytes is NULL");
     tp_status s = check_rows("tp_layer_norm_workspace", dtype, n_rows, n_cols);
-    if (s == TP_OK) *bytes = tpc::norm_workspace_bytes(dtype, n_rows, n_cols);
+    if (s == TP_OK) *bytes = norm_workspace_bytes(dtype, n_rows, n_cols);
     return s;
   });
 }
@@ -205,10 +175,10 @@ tp_status tp_layer_norm_backward(int32_t dtype, int64_t n_rows, int32_t n_cols, 
         !aligned(grad_gamma, 4) || !aligned(grad_beta, 4) || !aligned(ws, 4))
       return fail(me, "misaligned pointer");
     if (grad_gamma) {
-      const size_t need = tpc::norm_workspace_bytes(dtype, n_rows, n_cols);
+      const size_t need = norm_workspace_bytes(dtype, n_rows, n_cols);
       if (need && (!ws || ws_bytes < need)) return fail(me, "workspace missing or too small", TP_ERR_WORKSPACE);
     }
-    tpc::NormBwdArgs a;
+    NormBwdArgs a;
     if (drop && (s = check_drop(me, drop, &a.drop)) != TP_OK) return s;
     if (n_rows == 0 && !grad_gamma) return TP_OK;
     a.dtype = dtype;
@@ -228,8 +198,8 @@ tp_status tp_layer_norm_backward(int32_t dtype, int64_t n_rows, int32_t n_cols, 
     a.grad_beta = grad_beta;
     a.part = static_cast<float*>(ws);
     a.stream = stream;
-    hipError_t e = tpc::norm_backward(a);
-    return e == hipSuccess ? TP_OK : tpc::hip_error(e, "tp_layer_norm_backward launch");
+    hipError_t e = norm_backward(a);
+    return e == hipSuccess ? TP_OK : hip_error(e, "tp_layer_norm_backward launch");
   });
 }
 
@@ -247,7 +217,7 @@ tp_status tp_attn_forward(const tp_attn* a, const void* q, int64_t q_stride, con
     if (a->n_nodes == 0) return TP_OK;
     if (!aligned(lse, 4)) return fail(me, "misaligned pointer");
     if ((s = check_attn_pointers(me, a)) != TP_OK) return s;
-    tpc::AttnArgs args;
+    AttnArgs args;
     args.d = *a;
     args.q = q;
     args.k = k;
@@ -259,7 +229,7 @@ tp_status tp_attn_forward(const tp_attn* a, const void* q, int64_t q_stride, con
     args.os = out_stride;
     args.lse = lse;
     args.stream = stream;
-    return launched(me, tpc::attn_forward(args));
+    return launched(me, attn_forward(args), kTooMany);
   });
 }
 
@@ -267,7 +237,7 @@ tp_status tp_attn_backward_workspace(const tp_attn* a, size_t* bytes) {
   return guarded([&]() -> tp_status {
     if (!bytes) return fail("tp_attn_backward_workspace", "bytes is NULL");
     tp_status s = check_attn("tp_attn_backward_workspace", a);
-    if (s == TP_OK) *bytes = tpc::attn_workspace(*a).floats * sizeof(float);
+    if (s == TP_OK) *bytes = attn_workspace(*a).floats * sizeof(float);
     return s;
   });
 }
@@ -294,11 +264,11 @@ tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, co
       if (!lse) return fail(me, "lse is NULL");
       if ((s = check_attn_pointers(me, a)) != TP_OK) return s;
     }
-    const tpc::AttnWorkspace w = tpc::attn_workspace(*a);
+    const AttnWorkspace w = attn_workspace(*a);
     if (w.floats > 0 && (!ws || ws_bytes < w.floats * sizeof(float)))
       return fail(me, "workspace missing or too small", TP_ERR_WORKSPACE);
     if (a->n_nodes == 0 && !grad_bias) return TP_OK;
-    tpc::AttnArgs args;
+    AttnArgs args;
     args.d = *a;
     args.q = q;
     args.k = k;
@@ -322,7 +292,7 @@ tp_status tp_attn_backward(const tp_attn* a, const void* q, int64_t q_stride, co
     args.part = args.delta + w.part;
     args.kv_part = args.delta + w.kv_part;
     args.stream = stream;
-    return launched(me, tpc::attn_backward(args));
+    return launched(me, attn_backward(args), kTooMany);
   });
 }
 

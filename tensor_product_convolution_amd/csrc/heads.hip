@@ -1,0 +1,402 @@
+// Norm of queries and keys over each head, with the rotation by position, in one pass.
+//
+//   r = 1 / sqrt(mean(x^2) + eps);  y = x r gamma
+//   t = sum_a pos_a freq_ia;  (a, b) -> (a cos t - b sin t, a sin t + b cos t)  for pair i of y
+// and backward, with h the upstream gradient rotated back:
+//   grad_gamma = sum_rows h x r;  s = h gamma;  grad_x = r (s - x r mean(s x r))
+//   grad t_i = sum_heads (h_b a - h_a b);  grad_pos_a = sum_i grad t_i freq_ia
+//
+// Bound by HBM: q and k are read once and written once.  A few threads hold a head, each
+// the two values of up to 4 (float32) or 8 (bfloat16) pairs, so that pairs need no exchange in
+// either layout.  The angles of a block of rows are taken once, into LDS, and
+// serve all heads: turns in 64 bits, so that far positions keep their angle, and only the
+// fraction of a turn goes on in 32.
+#include <algorithm>
+
+#include "internal.hpp"
+#include "rows.hpp"
+
+namespace tpc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTrig = 2048;                // angles that a workgroup holds
+constexpr int kMaxAxes = 3;
+
+// The pairs of a thread.  A head is cut into chunks of kN pairs: first those of the rotated
+// part, then those of the rest, whose pairs turn by nothing.  A chunk is two runs of up to kN
+// values: its pairs' first and second values (half layout), or adjacent pairs one after the
+// other (interleaved; the rest always).
+template <typename T, bool INTER>
+struct Chunks {
+  static constexpr int N = Chunk<T>::kN;
+  int at[2], left[2];                      // first element and length of the runs (may be <= 0)
+  int pair;                                // first pair, -1 in the rest
+  int pairs;                               // rotated pairs of the chunk
+  __device__ __forceinline__ Chunks(int c, int d, int n_pairs) {
+    const int turned = (n_pairs + N - 1) / N;
+    pair = c < turned ? c * N : -1;
+    pairs = c < turned ? min(N, n_pairs - c * N) : 0;
+    if (c < turned && !INTER) {
+      at[0] = c * N;
+      at[1] = n_pairs + c * N;
+      left[0] = left[1] = pairs;
+    } else {
+      const int first = c < turned ? 2 * c * N : 2 * n_pairs + 2 * (c - turned) * N;
+      const int n = c < turned ? 2 * pairs : max(0, min(2 * N, d - first));
+      at[0] = first;
+      at[1] = first + N;
+      left[0] = min(N, n);
+      left[1] = n - N;
+    }
+  }
+  // value j of run i, i N + j in all, is first (0) or second (1) value of a pair
+  static constexpr __device__ __forceinline__ int first(int j) { return INTER ? 2 * j : j; }
+  static constexpr __device__ __forceinline__ int second(int j) { return INTER ? 2 * j + 1 : N + j; }
+};
+
+template <typename T, bool INTER>
+struct RawPairs {
+  RawChunk<T> run[2];
+  __device__ __forceinline__ void load(const T* head, const Chunks<T, INTER>& c) {
+    run[0].load(head + c.at[0], c.left[0]);
+    run[1].load(head + c.at[1], c.left[1]);
+  }
+  __device__ __forceinline__ float at(int j) const { return run[j / Chunk<T>::kN].at(j % Chunk<T>::kN); }
+};
+
+template <typename T, bool INTER>
+__device__ __forceinline__ void store_pairs(T* head, const Chunks<T, INTER>& c, const float* v) {
+  store_chunk(head + c.at[0], c.left[0], v);
+  store_chunk(head + c.at[1], c.left[1], v + Chunk<T>::kN);
+}
+
+// float32 values laid out like a head
+template <typename T, bool INTER>
+__device__ __forceinline__ void load_like(const float* w, const Chunks<T, INTER>& c, float* v) {
+  constexpr int N = Chunk<T>::kN;
+#pragma unroll
+  for (int i = 0; i < 2 * N; i += 4) load_chunk(w + c.at[i / N] + i % N, c.left[i / N] - i % N, v + i);
+}
+
+// cos and sin of a row's angle i.  Whole turns are taken off in 64 bits.
+__device__ __forceinline__ float2 turn_of(const HeadArgs& a, int64_t row, int i) {
+  double t = 0.0;
+  for (int x = 0; x < a.axes; ++x) {
+    const int64_t at = row * a.axes + x;
+    const double p = a.pos_int ? (double)static_cast<const int32_t*>(a.pos)[at] : (double)static_cast<const float*>(a.pos)[at];
+    t = fma(p, a.freq[(int64_t)i * a.axes + x], t);
+  }
+  t *= 0.15915494309189533577;             // 1 / (2 pi)
+  float s, c;
+  sincospif(2.f * (float)(t - rint(t)), &s, &c);
+  return make_float2(c, s);
+}
+
+__device__ __forceinline__ void fill_angles(const HeadArgs& a, int64_t row0, int rows, float2* cs) {
+  if (a.pairs == 0) return;
+  for (int i = threadIdx.x; i < rows * a.pairs; i += kThreads) cs[i] = turn_of(a, row0 + i / a.pairs, i % a.pairs);
+}
+
+template <typename T, bool INTER>
+__device__ __forceinline__ void cos_sin(const float2* cs, const Chunks<T, INTER>& c, float2* o) {
+#pragma unroll
+  for (int j = 0; j < Chunk<T>::kN; ++j) o[j] = j < c.pairs ? cs[c.pair + j] : make_float2(1.f, 0.f);
+}
+
+// sum over the 2^lg neighbouring threads of a head, in a fixed order
+__device__ __forceinline__ float head_sum(float v, int lg) {
+  for (int m = 1 << lg >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+// Which head of which row a thread has in turn `it` of a block of rows
+struct Item {
+  int row, head;
+  __device__ __forceinline__ Item(const HeadArgs& a, int it) {
+    const int i = (it * kThreads + (int)threadIdx.x) >> a.lg;
+    row = i / (a.hq + a.hk);
+    head = i - row * (a.hq + a.hk);
+  }
+};
+
+template <typename T, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads)
+    k_heads_fwd(HeadArgs a) {
+  constexpr int V = 2 * Chunk<T>::kN;
+  __shared__ float2 cs[kTrig];
+  const Chunks<T, INTER> c((int)threadIdx.x & ((1 << a.lg) - 1), a.d, a.pairs);
+  float g[2][V];
+  if (NORM) {
+    load_like<T, INTER>(a.gamma_q, c, g[0]);
+    load_like<T, INTER>(a.gamma_k, c, g[1]);
+  }
+  const int64_t row0 = (int64_t)blockIdx.x * a.rows;
+  const int rows = (int)min((int64_t)a.rows, a.n_rows - row0), heads = a.hq + a.hk;
+  const int turns = (rows * heads * (1 << a.lg) + kThreads - 1) / kThreads;
+  const auto source = [&](const Item& it) {
+    return it.head < a.hq ? (const T*)a.q + (row0 + it.row) * a.q_stride + it.head * a.d
+                          : (const T*)a.k + (row0 + it.row) * a.k_stride + (it.head - a.hq) * a.d;
+  };
+  RawPairs<T, INTER> x;
+  {                                        // in flight while the angles are taken
+    const Item it(a, 0);
+    if (it.row < rows) x.load(source(it), c);
+  }
+  fill_angles(a, row0, rows, cs);
+  __syncthreads();
+  for (int n = 0; n < turns; ++n) {
+    const Item it(a, n), next(a, n + 1);
+    const bool has = it.row < rows;        // the same for all threads of a head
+    float v[V];
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] = has ? x.at(j) : 0.f;
+      s += v[j] * v[j];
+    }
+    if (next.row < rows) x.load(source(next), c);
+    if (NORM) {
+      const float r = 1.f / sqrtf(head_sum(s, a.lg) / (float)a.d + a.eps);
+      const bool key = it.head >= a.hq;
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = v[j] * r * (key ? g[1][j] : g[0][j]);
+    }
+    if (!has) continue;
+    float2 t[V / 2];
+    cos_sin(cs + it.row * a.pairs, c, t);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      const float p = v[c.first(j)], q = v[c.second(j)];
+      v[c.first(j)] = p * t[j].x - q * t[j].y;
+      v[c.second(j)] = p * t[j].y + q * t[j].x;
+    }
+    store_pairs(it.head < a.hq ? (T*)a.q_out + (row0 + it.row) * a.qo_stride + it.head * a.d
+                               : (T*)a.k_out + (row0 + it.row) * a.ko_stride + (it.head - a.hq) * a.d,
+                c, v);
+  }
+}
+
+// One pass over blocks of rows; a workgroup's part of the weight gradients stays in registers
+// until its last block.  part [gridDim.x][2][d]; a single workgroup writes the gradients itself.
+template <typename T, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads)
+    k_heads_bwd(HeadBwdArgs b) {
+  const HeadArgs& a = b.f;
+  constexpr int V = 2 * Chunk<T>::kN;
+  __shared__ float2 cs[kTrig];
+  extern __shared__ float sums[];          // [kMaxAxes][rows x heads], then [2^lg chunks of V]
+  const int lane_c = (int)threadIdx.x & ((1 << a.lg) - 1);
+  const Chunks<T, INTER> c(lane_c, a.d, a.pairs);
+  const int heads = a.hq + a.hk, per_axis = a.rows * heads;
+  float g[2][V], gg[2][V], f[kMaxAxes][V / 2];
+#pragma unroll
+  for (int j = 0; j < V; ++j) gg[0][j] = gg[1][j] = 0.f;
+  if (NORM) {
+    load_like<T, INTER>(a.gamma_q, c, g[0]);
+    load_like<T, INTER>(a.gamma_k, c, g[1]);
+  }
+  if (b.grad_pos) {
+#pragma unroll
+    for (int x = 0; x < kMaxAxes; ++x)
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) f[x][j] = x < a.axes && j < c.pairs ? (float)a.freq[(c.pair + j) * a.axes + x] : 0.f;
+  }
+  for (int64_t row0 = (int64_t)blockIdx.x * a.rows; row0 < a.n_rows; row0 += (int64_t)gridDim.x * a.rows) {
+    const int rows = (int)min((int64_t)a.rows, a.n_rows - row0);
+    const int turns = (rows * heads * (1 << a.lg) + kThreads - 1) / kThreads;
+    RawPairs<T, INTER> x, u;
+    const auto fetch = [&](const Item& it) {
+      if (it.row >= rows) return;
+      const int64_t row = row0 + it.row;
+      if (it.head < a.hq) {
+        x.load((const T*)a.q + row * a.q_stride + it.head * a.d, c);
+        u.load((const T*)b.gq_up + row * b.gq_up_stride + it.head * a.d, c);
+      } else {
+        x.load((const T*)a.k + row * a.k_stride + (it.head - a.hq) * a.d, c);
+        u.load((const T*)b.gk_up + row * b.gk_up_stride + (it.head - a.hq) * a.d, c);
+      }
+    };
+    fetch(Item(a, 0));
+    fill_angles(a, row0, rows, cs);
+    __syncthreads();
+    for (int n = 0; n < turns; ++n) {
+      const Item it(a, n);
+      const bool has = it.row < rows, key = it.head >= a.hq;
+      float v[V], h[V];
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        v[j] = has ? x.at(j) : 0.f;
+        h[j] = has ? u.at(j) : 0.f;
+      }
+      fetch(Item(a, n + 1));
+      float2 t[V / 2];
+      cos_sin(cs + (has ? it.row : 0) * a.pairs, c, t);
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float p = h[c.first(j)], q = h[c.second(j)];
+        h[c.first(j)] = p * t[j].x + q * t[j].y;
+        h[c.second(j)] = q * t[j].x - p * t[j].y;
+      }
+      float r = 1.f, m = 0.f;
+      if (NORM) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          s1 += v[j] * v[j];
+          s2 += h[j] * (key ? g[1][j] : g[0][j]) * v[j];
+        }
+        r = 1.f / sqrtf(head_sum(s1, a.lg) / (float)a.d + a.eps);
+        m = head_sum(s2, a.lg) * r / (float)a.d;
+      }
+      float w[kMaxAxes] = {0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const int p = c.first(j), q = c.second(j);
+        if (b.grad_pos) {                  // of the angle, from the pair before it is turned
+          const float yp = NORM ? v[p] * r * (key ? g[1][p] : g[0][p]) : v[p];
+          const float yq = NORM ? v[q] * r * (key ? g[1][q] : g[0][q]) : v[q];
+          const float gt = h[q] * yp - h[p] * yq;
+#pragma unroll
+          for (int k = 0; k < kMaxAxes; ++k) w[k] += gt * f[k][j];
+        }
+      }
+      if (NORM) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float z = v[j] * r;
+          const float e = has ? h[j] * z : 0.f;
+          gg[0][j] += key ? 0.f : e;
+          gg[1][j] += key ? e : 0.f;
+          h[j] = r * (h[j] * (key ? g[1][j] : g[0][j]) - z * m);
+        }
+      }
+      if (b.grad_pos) {
+#pragma unroll
+        for (int k = 0; k < kMaxAxes; ++k) {
+          if (k >= a.axes) break;
+          const float s = head_sum(w[k], a.lg);
+          if (has && lane_c == 0) sums[k * per_axis + it.row * heads + it.head] = s;
+        }
+      }
+      if (!has) continue;
+      const int64_t row = row0 + it.row;
+      store_pairs(key ? (T*)b.gk + row * b.gk_stride + (it.head - a.hq) * a.d : (T*)b.gq + row * b.gq_stride + it.head * a.d,
+                  c, h);
+    }
+    __syncthreads();
+    if (b.grad_pos) {
+      for (int i = threadIdx.x; i < rows * a.axes; i += kThreads) {
+        const int row = i / a.axes, k = i - row * a.axes;
+        float s = 0.f;
+        for (int h = 0; h < heads; ++h) s += sums[k * per_axis + row * heads + h];
+        b.grad_pos[(row0 + row) * a.axes + k] = s;
+      }
+      __syncthreads();
+    }
+  }
+  if (!NORM || !b.grad_gamma_q) return;
+  // over the threads that hold the same chunk: lanes of a wave, then the waves one after the other
+  const int lane = threadIdx.x & 63, n_chunks = 1 << a.lg;
+  for (int wave = 0; wave < kThreads / 64; ++wave) {
+    if ((int)threadIdx.x >> 6 == wave) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          float s = gg[i][j];
+          for (int m = n_chunks; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
+          float* to = sums + (i * n_chunks + lane_c) * V + j;
+          if (lane < n_chunks) *to = (wave ? *to : 0.f) + s;
+        }
+    }
+    __syncthreads();
+  }
+  float* out[2] = {b.grad_gamma_q, b.grad_gamma_k};
+  if (gridDim.x > 1) {
+    out[0] = b.part + (size_t)blockIdx.x * 2 * a.d;
+    out[1] = out[0] + a.d;
+  }
+  if ((int)threadIdx.x < n_chunks) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      store_chunk(out[i] + c.at[0], min(4, c.left[0]), sums + (i * n_chunks + lane_c) * V);
+      if (V > 8) store_chunk(out[i] + c.at[0] + 4, min(4, c.left[0] - 4), sums + (i * n_chunks + lane_c) * V + 4);
+      store_chunk(out[i] + c.at[1], min(4, c.left[1]), sums + (i * n_chunks + lane_c) * V + V / 2);
+      if (V > 8) store_chunk(out[i] + c.at[1] + 4, min(4, c.left[1] - 4), sums + (i * n_chunks + lane_c) * V + V / 2 + 4);
+    }
+  }
+}
+
+// Weight gradients from the workgroups' parts [n][2][d], a wave per value, in a fixed order.
+__global__ void __launch_bounds__(kThreads)
+    k_heads_join(const float* __restrict__ part, int n, int d, float* __restrict__ gq, float* __restrict__ gk) {
+  const int col = (blockIdx.x * kThreads + threadIdx.x) >> 6, lane = threadIdx.x & 63;
+  if (col >= 2 * d) return;
+  float s = 0.f;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 64) s += part[(size_t)i * 2 * d + col];
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m, 64);
+  if (lane == 0) (col < d ? gq[col] : gk[col - d]) = s;
+}
+
+constexpr int kBwdBlocks = 1024;           // workgroups that walk the rows of the backward
+
+// Threads per head (their binary logarithm) and rows per workgroup: enough items for a few
+// turns of the workgroup, fewer where the rows would not fill the chip.
+void shape_of(int dtype, HeadArgs& a) {
+  const int n = dtype == TP_F32 ? Chunk<float>::kN : Chunk<bf16_t>::kN;
+  const int chunks = (a.pairs + n - 1) / n + (a.d - 2 * a.pairs + 2 * n - 1) / (2 * n);
+  a.lg = 0;
+  while ((1 << a.lg) < chunks) ++a.lg;
+  const int64_t most = std::max(1, std::min(kTrig / std::max(1, a.pairs), (4 * kThreads) / ((a.hq + a.hk) << a.lg)));
+  a.rows = (int)std::max<int64_t>(1, std::min<int64_t>({most, 64, (a.n_rows + 1023) / 1024}));
+}
+
+int64_t bwd_blocks(const HeadArgs& a) {
+  return std::max<int64_t>(1, std::min<int64_t>(kBwdBlocks, (a.n_rows + a.rows - 1) / a.rows));
+}
+
+template <typename F>
+hipError_t pick(int dtype, bool interleaved, bool norm, F&& f) {
+  const auto two = [&](auto t, auto inter) { return norm ? f(t, inter, std::true_type()) : f(t, inter, std::false_type()); };
+  const auto one = [&](auto t) { return interleaved ? two(t, std::true_type()) : two(t, std::false_type()); };
+  return dtype == TP_F32 ? one(float()) : one(bf16_t());
+}
+
+}  // namespace
+
+size_t heads_workspace_bytes(int dtype, HeadArgs a) {
+  shape_of(dtype, a);
+  const int64_t n = bwd_blocks(a);
+  return n == 1 ? 0 : (size_t)n * 2 * a.d * sizeof(float);
+}
+
+hipError_t heads_forward(int dtype, HeadArgs a) {
+  shape_of(dtype, a);
+  const int64_t blocks = (a.n_rows + a.rows - 1) / a.rows;
+  if (blocks > 0xffffffffLL / kThreads) return hipErrorInvalidConfiguration;
+  return pick(dtype, a.interleaved, a.gamma_q != nullptr, [&](auto t, auto inter, auto norm) {
+    hipLaunchKernelGGL((k_heads_fwd<decltype(t), inter(), norm()>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t heads_backward(int dtype, HeadBwdArgs b) {
+  HeadArgs& a = b.f;
+  shape_of(dtype, a);
+  const int n = (int)bwd_blocks(a);
+  hipError_t e = pick(dtype, a.interleaved, a.gamma_q != nullptr, [&](auto t, auto inter, auto norm) {
+    constexpr int V = 2 * Chunk<decltype(t)>::kN;
+    const size_t floats = std::max(kMaxAxes * a.rows * (a.hq + a.hk), 2 * (V << a.lg));
+    hipLaunchKernelGGL((k_heads_bwd<decltype(t), inter(), norm()>), dim3(n), dim3(kThreads), floats * sizeof(float), a.stream, b);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || n == 1 || !b.grad_gamma_q) return e;
+  hipLaunchKernelGGL(k_heads_join, dim3((2 * a.d + 3) / 4), dim3(kThreads), 0, a.stream, b.part, n, a.d, b.grad_gamma_q,
+                     b.grad_gamma_k);
+  return hipGetLastError();
+}
+
+}  // namespace tpc

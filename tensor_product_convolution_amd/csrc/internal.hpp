@@ -243,4 +243,119 @@ struct AttnWorkspace {
 };
 AttnWorkspace attn_workspace(const tp_attn& d);
 
+// ---- norm and rotation of queries and keys (heads.hip) --------------------------
+// hipErrorInvalidConfiguration, with nothing launched, where a grid would be too large
+struct HeadArgs {
+  int64_t n_rows = 0, q_stride = 0, k_stride = 0, qo_stride = 0, ko_stride = 0;
+  int hq = 0, hk = 0, d = 0, pairs = 0, axes = 0;
+  bool pos_int = false, interleaved = false;
+  const void *q = nullptr, *k = nullptr, *pos = nullptr;
+  const double* freq = nullptr;
+  const float *gamma_q = nullptr, *gamma_k = nullptr;   // null: no norm
+  float eps = 0.f;
+  void *q_out = nullptr, *k_out = nullptr;
+  int lg = 0, rows = 0;                           // set by the launch
+  hipStream_t stream = nullptr;
+};
+struct HeadBwdArgs {
+  HeadArgs f;
+  int64_t gq_up_stride = 0, gk_up_stride = 0, gq_stride = 0, gk_stride = 0;
+  const void *gq_up = nullptr, *gk_up = nullptr;
+  void *gq = nullptr, *gk = nullptr;
+  float *grad_gamma_q = nullptr, *grad_gamma_k = nullptr, *grad_pos = nullptr, *part = nullptr;
+};
+constexpr int kHeadsMaxDim = 256;
+size_t heads_workspace_bytes(int dtype, HeadArgs a);
+hipError_t heads_forward(int dtype, HeadArgs a);
+hipError_t heads_backward(int dtype, HeadBwdArgs b);
+
+// ---- routing and products by group (route.hip, grouped*.hip) ---------------------
+constexpr int kMaxGroups = 1024, kMaxChoices = 16;
+struct RouteArgs {
+  int dtype = TP_F32;
+  int64_t n_rows = 0, stride = 0;
+  int n_groups = 0, k = 0;
+  bool over_all = false;                          // weights are the softmax over all groups, not over the chosen
+  const void* logits = nullptr;
+  float* weight = nullptr;
+  int32_t* index = nullptr;
+  // backward
+  const float *weight_in = nullptr, *grad_weight = nullptr;
+  const int32_t* index_in = nullptr;
+  void* grad_logits = nullptr;
+  hipStream_t stream = nullptr;
+};
+hipError_t route_forward(const RouteArgs& a);
+hipError_t route_backward(const RouteArgs& a);
+size_t group_workspace_bytes(int64_t n, int n_groups);
+hipError_t group_rows(const int32_t* index, int64_t n, int n_groups, int32_t* ptr, int32_t* rows, void* ws, hipStream_t st);
+struct CombineArgs {
+  int dtype = TP_F32;
+  int64_t n_rows = 0;
+  int k = 0, n_cols = 0;
+  const void *y = nullptr, *go = nullptr;
+  const float* weight = nullptr;                  // null: 1
+  void *out = nullptr, *gy = nullptr;
+  float* grad_weight = nullptr;
+  hipStream_t stream = nullptr;
+};
+// c[row] = a[row] w_e (+ bias) and what follows, for the rows of each group; slots from
+// ptr[n_groups] on belong to no group and get zeros.  Rows of a and c: those of the slots in
+// group order (div 0), or rows[slot] / div.
+struct GroupedArgs {
+  int dtype = TP_F32, n_groups = 0, act = 0;
+  int64_t n = 0;                                  // slots, fewer than 2^31
+  const int32_t *ptr = nullptr, *rows = nullptr;
+  const void *a = nullptr, *w = nullptr, *bias = nullptr;
+  int64_t lda = 0, ldc = 0;
+  int a_div = 0, c_div = 0;
+  int k = 0, cols = 0;                            // contraction, columns of c
+  bool transposed = false;                        // w is [n_groups][cols][k], not [k][cols]
+  void *c = nullptr, *pre_out = nullptr;          // pre_out: before the activation, rows of c
+  const void* pre = nullptr;                      // c is multiplied by the activation's slope here; rows of c
+  int64_t ldpre = 0;
+  hipStream_t stream = nullptr;
+};
+hipError_t grouped_product(const GroupedArgs& a);
+// grad_w[e] = sum over the rows of group e of x^T gy, grad_bias[e] = sum of gy
+struct GroupedWeightArgs {
+  int dtype = TP_F32, n_groups = 0;
+  int64_t n = 0, ldx = 0, ldg = 0;
+  const int32_t *ptr = nullptr, *rows = nullptr;
+  const void *x = nullptr, *gy = nullptr;
+  int x_div = 0, g_div = 0, k = 0, cols = 0;
+  void *grad_w = nullptr, *grad_bias = nullptr;
+  float* part = nullptr;
+  hipStream_t stream = nullptr;
+};
+size_t grouped_weight_workspace(int dtype, int64_t n, int n_groups, int k, int cols);
+hipError_t grouped_weight_grad(const GroupedWeightArgs& a);
+hipError_t combine_forward(const CombineArgs& a);
+hipError_t combine_backward(const CombineArgs& a);
+
+// ---- the AdamW step (adamw.hip) -----------------------------------------------------
+constexpr int kAdamBlock = 256;                   // state values that share a unit
+struct AdamArgs {
+  int bits = 32, grad_dtype = TP_F32, n_tensors = 0;
+  const int64_t* sizes = nullptr;                 // host
+  const void* table = nullptr;
+  void *m = nullptr, *v = nullptr;
+  float *m_unit = nullptr, *v_unit = nullptr;
+  double beta1 = 0, beta2 = 0, eps = 0, lr = 0, max_norm = 0;
+  const float* lr_at = nullptr;                   // device, null: lr
+  uint64_t seed = 0;
+  void *scalars = nullptr, *ws = nullptr;
+  float* norm = nullptr;
+  const void* const* grads = nullptr;             // host
+  hipStream_t stream = nullptr;
+};
+// bytes of the table, elements of the state arrays, bytes of the workspace; -1: too many
+int64_t adamw_table_bytes(int n_tensors, const int64_t* sizes);
+int64_t adamw_state_size(int n_tensors, const int64_t* sizes);
+size_t adamw_workspace_bytes(int n_tensors, const int64_t* sizes);
+void adamw_table_fill(int n_tensors, const int64_t* sizes, void* const* params, void* const* copies, const float* decay,
+                      void* table);
+hipError_t adamw_step(const AdamArgs& a);
+hipError_t adamw_values(int second, int64_t n, const uint8_t* codes, const float* units, float* out, hipStream_t st);
+
 }  // namespace tpc

@@ -83,7 +83,7 @@ def _rows(t, name, dtype, shape, dev):
     strides = t.stride()
     want = 1
     for i in range(len(shape) - 1, 0, -1):
-        if strides[i] != want and shape[i] != 1:
+        if strides[i] != want and shape[i] != 1 and shape[0]:      # no rows: nothing to be contiguous
             raise ValueError(f"{name}: rows must be contiguous")
         want *= shape[i]
     # the stride of a single row says nothing
