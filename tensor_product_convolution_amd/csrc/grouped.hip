@@ -11,8 +11,9 @@
 namespace tpc {
 namespace {
 
-// BM x BN tile of four waves, WM x WN each, S contraction values a step.  ALONG: w rows run along the contraction
-// (transposed).  EVEN: contraction and columns are multiples of 8.
+// Rows of any length and alignment: staged through registers.  BM x BN tile of four waves, WM x WN
+// each, S contraction values a step.  ALONG: w rows run along the contraction (transposed).  EVEN:
+// contraction and columns are multiples of 8.
 template <typename T, int BM, int BN, int WM, int WN, int S, bool ALONG, bool EVEN>
 __global__ void __launch_bounds__(kGemmThreads)
     k_grouped(GroupedArgs a, int n_rows, int n_cols) {
@@ -138,24 +139,158 @@ __global__ void __launch_bounds__(kGemmThreads)
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S>
-hipError_t launch(const GroupedArgs& a) {
-  const int64_t rows = a.n / BM + a.n_groups + 1, cols = (a.cols + BN - 1) / BN;
-  if (rows * cols > 0xffffffffLL / kGemmThreads) return hipErrorInvalidConfiguration;
-  const bool even = a.k % 8 == 0 && a.cols % 8 == 0;
-  const auto go = [&](auto along, auto whole) {
-    hipLaunchKernelGGL((k_grouped<T, BM, BN, WM, WN, S, along(), whole()>), dim3((unsigned)(rows * cols)), dim3(kGemmThreads), 0,
-                       a.stream, a, (int)rows, (int)cols);
-    return hipGetLastError();
-  };
-  const auto first = [&](auto along) { return even ? go(along, std::true_type()) : go(along, std::false_type()); };
-  return a.transposed ? first(std::true_type()) : first(std::false_type());
+// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32.
+template <typename T, int WM, int WN, int MB, int NB, bool ALONG>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+    k_grouped_fast(GroupedArgs a, int n_rows, int n_cols) {
+  constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
+  typedef AlongLds<T, BM, W> TA;
+  typedef typename std::conditional<ALONG, AlongLds<T, BN, W>, AcrossLds<T, BN, W>>::type TB;
+  __shared__ __attribute__((aligned(16))) uint8_t a0[TA::kBytes], b0[TB::kBytes], a1[TA::kBytes], b1[TB::kBytes];
+  __shared__ int arow[BM], crow[BM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int rt, ct;
+  place_tile(blockIdx.x, n_rows, n_cols, rt, ct);
+  Part part;
+  const int n = (int)a.n;
+  if (!find_part(a.ptr, a.n_groups + 1, n, BM, rt, part) || part.first >= part.hi) return;
+  const int rows = min(BM, part.hi - part.first), col0 = ct * BN;
+  for (int i = tid; i < BM; i += 64 * W) {
+    // rows past the part's end repeat its last one; nothing of them is stored
+    const int place = part.first + min(i, rows - 1), slot = a.a_div || a.c_div ? slot_at(a.rows, place, n) : 0;
+    arow[i] = a.a_div ? slot / a.a_div : place;
+    crow[i] = i < rows ? (a.c_div ? slot : place) : -1;
+  }
+  const bool none = part.group == a.n_groups;        // slots without a group
+  const int wm = wave % WM, wn = wave / WM;
+  Sums<T, MB, NB> sums;
+  sums.clear();
+  if (!none) {
+    const T *pa[TA::Q], *pb[TB::Q];
+    const T* w = (const T*)a.w + (int64_t)part.group * a.k * a.cols;
+    if constexpr (ALONG) {
+#pragma unroll
+      for (int q = 0; q < TB::Q; ++q)
+        pb[q] = w + (int64_t)min(col0 + TB::row(q, wave, lane), a.cols - 1) * a.k + TB::first(lane);
+    } else {
+#pragma unroll
+      for (int q = 0; q < TB::Q; ++q) {
+        const int row = TB::row(q, wave, lane);
+        pb[q] = w + (int64_t)row * a.cols + min(col0 + TB::first(row, lane), a.cols - TB::kPer);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < TA::Q; ++q) pa[q] = (const T*)a.a + arow[TA::row(q, wave, lane)] * a.lda + TA::first(lane);
+    const int steps = (a.k + S - 1) / S;
+    const T* zeros = reinterpret_cast<const T*>(kZeros);
+    const auto load = [&](int t, int buffer) {
+      const int k0 = t * S, mine = k0 + TA::first(lane);
+      if (k0 + S <= a.k) {
+#pragma unroll
+        for (int q = 0; q < TA::Q; ++q) fetch16(pa[q] + k0, TA::place(buffer ? a1 : a0, q, wave));
+#pragma unroll
+        for (int q = 0; q < TB::Q; ++q)
+          fetch16(pb[q] + (ALONG ? k0 : (int64_t)k0 * a.cols), TB::place(buffer ? b1 : b0, q, wave));
+      } else {
+#pragma unroll
+        for (int q = 0; q < TA::Q; ++q) fetch16(mine < a.k ? pa[q] + k0 : zeros, TA::place(buffer ? a1 : a0, q, wave));
+#pragma unroll
+        for (int q = 0; q < TB::Q; ++q)
+          fetch16((ALONG ? mine : k0 + TB::row(q, wave, lane)) < a.k ? pb[q] + (ALONG ? k0 : (int64_t)k0 * a.cols) : zeros,
+                  TB::place(buffer ? b1 : b0, q, wave));
+      }
+    };
+    const auto all = [&](auto far) {
+      walk(steps, load, [&](int buffer, int t) {
+        multiply<T, TA, TB, MB, NB, far()>(buffer ? a1 : a0, buffer ? b1 : b0, wm, wn, lane, sums);
+        if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) sums.gather();
+      });
+      sums.gather();
+    };
+    all(std::false_type());
+    // an infinite operand has pieces that are not numbers: such a tile is formed again, with pieces
+    // that keep infinities
+    if constexpr (sizeof(T) == 4) {
+      if (__syncthreads_or(!sums.finite())) {
+        sums.clear();
+        all(std::true_type());
+      }
+    }
+  }
+  __syncthreads();
+  // the waves' own parts of the buffers
+  constexpr int kOwn = 32 * 32 * NB * sizeof(float), kA = TA::kBytes / kOwn, kB = TB::kBytes / kOwn;
+  static_assert(2 * kA + 2 * kB >= W);
+  uint8_t* own = wave < kA ? a0 + wave * kOwn
+                 : wave < kA + kB ? b0 + (wave - kA) * kOwn
+                 : wave < 2 * kA + kB ? a1 + (wave - kA - kB) * kOwn : b1 + (wave - 2 * kA - kB) * kOwn;
+  const int col = col0 + 32 * NB * wn + lane % (4 * NB) * 8, left = a.cols - col;
+  float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (a.bias && !none && left > 0) load8((const T*)a.bias + (int64_t)part.group * a.cols + col, left, bias);
+  hand_out<T, MB, NB>(sums, reinterpret_cast<float*>(own), lane, [&](int r, int, float* v) {
+    const int row = crow[32 * MB * wm + r];
+    if (row < 0 || left <= 0) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += bias[j];
+    if (a.pre) {
+      float z[8];
+      load8((const T*)a.pre + row * a.ldpre + col, left, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = none ? 0.f : v[j] * silu_slope(z[j]);
+    }
+    if (a.act) {                           // the activation is that of the stored value
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (float)(T)v[j];
+      if (a.pre_out) store8((T*)a.pre_out + row * a.ldc + col, left, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
+    }
+    store8((T*)a.c + row * a.ldc + col, left, v);
+  });
+}
+
+template <typename F>
+hipError_t tiles(const GroupedArgs& a, int bm, int bn, F&& f) {
+  const int64_t rows = a.n / bm + a.n_groups + 1, cols = (a.cols + bn - 1) / bn;
+  if (rows * cols > 0xffffffffLL / 512) return hipErrorInvalidConfiguration;
+  f(dim3((unsigned)(rows * cols)), (int)rows, (int)cols);
+  return hipGetLastError();
+}
+
+template <typename T, int WM, int WN, int MB, int NB>
+hipError_t fast(const GroupedArgs& a) {
+  return tiles(a, 32 * WM * MB, 32 * WN * NB, [&](dim3 grid, int rows, int cols) {
+    if (a.transposed)
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, true>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
+    else
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, false>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
+  });
+}
+
+template <typename T>
+hipError_t any(const GroupedArgs& a) {
+  constexpr int S = sizeof(T) == 4 ? 32 : 64;
+  return tiles(a, 64, 64, [&](dim3 grid, int rows, int cols) {
+    if (a.transposed)
+      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, true, false>), grid, dim3(kGemmThreads), 0, a.stream, a, rows, cols);
+    else
+      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, false, false>), grid, dim3(kGemmThreads), 0, a.stream, a, rows, cols);
+  });
 }
 
 template <typename T>
 hipError_t product(const GroupedArgs& a) {
-  if (a.n <= 32 * (int64_t)a.n_groups) return launch<T, 32, 128, 32, 32, 64>(a);
-  return launch<T, 128, 128, 64, 64, kPlanes<T> == 3 ? 32 : 64>(a);
+  constexpr int N = 16 / sizeof(T);
+  const auto whole = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  if (a.k % N || a.cols % N || a.lda % N || !whole(a.a) || !whole(a.w)) return any<T>(a);
+  const int64_t even = a.n / a.n_groups;
+  if (even <= 32) return fast<T, 1, 4, 1, 1>(a);
+  const auto count = [&](int bm, int bn) { return (a.n / bm + a.n_groups / 2) * ((a.cols + bn - 1) / bn); };
+  if constexpr (sizeof(T) == 2)
+    if (even >= 192 && count(256, 256) >= 256) return fast<T, 2, 4, 4, 2>(a);
+  if (count(128, 128) >= 256) return fast<T, 2, 2, 2, 2>(a);
+  return fast<T, 2, 2, 1, 1>(a);
 }
 
 }  // namespace

@@ -116,8 +116,8 @@ struct AcrossTile {
 
 // Part t of the groups cut into parts of `size` slots: group e's parts start at number
 // ptr[e] / size + e, which never overlap and leave at most one unused number per group, so
-// n / size + groups numbers cover any groups without the host knowing them.  Looked up 64
-// groups at a time.  `groups` counts the one behind the last pointer (slots without a group),
+// n / size + groups numbers cover any groups without the host knowing them.  Numbers grow
+// with the group, so the part's group is the count of those that start by then.  `groups` counts the one behind the last pointer (slots without a group),
 // which ends at n.  False: an unused number, but for the first of an empty group.
 struct Part {
   int group, lo, hi, first;                // slots of the group, first slot of the part
@@ -125,16 +125,14 @@ struct Part {
 __device__ __forceinline__ bool find_part(const int32_t* ptr, int groups, int n, int size, int t, Part& p) {
   const int lane = threadIdx.x & 63;
   const auto start = [&](int e) { return min(max(ptr[e], 0), n); };
-  int b = 0, left = groups;
-  while (left > 1) {
-    const int step = (left + 63) >> 6, at = b + lane * step;
-    const bool le = lane * step < left && start(at) / size + at <= t;
-    const int cnt = __popcll(__ballot(le));
-    if (cnt == 0) return false;            // not a valid ptr
-    b += (cnt - 1) * step;
-    left = min(step, left - (cnt - 1) * step);
+  int count = 0;                           // groups that start at or before part t
+#pragma unroll 4
+  for (int e = 0; e < groups; e += 64) {
+    const bool le = e + lane < groups && start(e + lane) / size + e + lane <= t;
+    count += __popcll(__ballot(le));
   }
-  p.group = __builtin_amdgcn_readfirstlane(b);
+  if (count == 0) return false;            // not a valid ptr
+  p.group = __builtin_amdgcn_readfirstlane(count - 1);
   p.lo = start(p.group);
   p.hi = p.group + 1 < groups ? start(p.group + 1) : n;
   const int64_t first = (int64_t)p.lo + (int64_t)(t - (p.lo / size + p.group)) * size;
@@ -142,6 +140,10 @@ __device__ __forceinline__ bool find_part(const int32_t* ptr, int groups, int n,
   return first == p.lo || (first > p.lo && first < p.hi);
 }
 
+// a slot by its place in group order; what is out of range is clamped
+__device__ __forceinline__ int slot_at(const int32_t* rows, int place, int n) {
+  return (int)min((uint32_t)rows[place], (uint32_t)(n - 1));
+}
 // the row of a slot: itself, or rows[slot] / div
 __device__ __forceinline__ int row_of(const int32_t* rows, int slot, int div, int n) {
   if (div == 0) return slot;
@@ -161,10 +163,261 @@ __device__ __forceinline__ void place_tile(int id, int rows, int cols, int& r, i
   c = in / high;
 }
 
-__device__ __forceinline__ float silu(float z) { return z / (1.f + expf(-z)); }
+// exp and reciprocal to a unit in the last place each: 4 u of a value, where the product in front is
+// off by more; at z = -88 and below the sigmoid is 0
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+}
+__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 __device__ __forceinline__ float silu_slope(float z) {
-  const float s = 1.f / (1.f + expf(-z));
+  const float s = sigmoid(z);
   return s * (1.f + z * (1.f - s));
+}
+
+// ---- the fast path: operands straight to LDS --------------------------------------------
+// Tiles of 16-byte chunks go from memory to LDS without passing registers (one instruction
+// moves 64 chunks to consecutive places), in the operands' type; the permutation of a row's chunks is
+// made by what each lane fetches.  Two buffers, so that a step's loads have the step
+// before to arrive in.  float32 is split into its three pieces as the fragments are read: pieces
+// in LDS would take half as many bytes again and would be formed once for every tile that
+// shares an operand anyway.  Needs rows of whole, aligned chunks; the rest of a step past the
+// contraction's end is fetched from a chunk of zeros.
+typedef __attribute__((address_space(1))) const void global_bytes;
+typedef __attribute__((address_space(3))) void lds_bytes;
+__device__ __forceinline__ void fetch16(const void* from, void* to) {
+  __builtin_amdgcn_global_load_lds((global_bytes*)from, (lds_bytes*)to, 16, 0, 0);
+}
+static __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+// contraction values of a step: 128 bytes
+template <typename T>
+constexpr int kDeep = 128 / sizeof(T);
+
+// R rows with the contraction along them.  A wave's instruction q takes rows 8 q .. 8 q + 7.
+template <typename T, int R, int WAVES>
+struct AlongLds {
+  static constexpr int kBytes = R * 128, Q = R / 8 / WAVES, kPer = 16 / sizeof(T);
+  static_assert(R % (8 * WAVES) == 0);
+  static __device__ __forceinline__ int row(int q, int wave, int lane) { return 8 * (q * WAVES + wave) + (lane >> 3); }
+  static __device__ __forceinline__ int first(int lane) { return ((lane & 7) ^ (lane >> 3)) * kPer; }   // value of the row
+  static __device__ __forceinline__ uint8_t* place(uint8_t* t, int q, int wave) { return t + 1024 * (q * WAVES + wave); }
+  static __device__ __forceinline__ const uint8_t* chunk(const uint8_t* t, int row, int c) {
+    return t + row * 128 + (c ^ (row & 7)) * 16;
+  }
+  // rows 32 block + l % 32, contraction 16 kk + 8 (l / 32) + 0..7
+  static __device__ __forceinline__ void read(const uint8_t* t, int block, int kk, int lane, Octet<T>& o) {
+    const int r = 32 * block + (lane & 31);
+    if constexpr (sizeof(T) == 2) {
+      o.v.v = __builtin_bit_cast(Chunk<bf16_t>::vec, *reinterpret_cast<const b8*>(chunk(t, r, 2 * kk + (lane >> 5))));
+    } else {
+      o.a.v = __builtin_bit_cast(Chunk<float>::vec, *reinterpret_cast<const f4*>(chunk(t, r, 4 * kk + 2 * (lane >> 5))));
+      o.b.v = __builtin_bit_cast(Chunk<float>::vec, *reinterpret_cast<const f4*>(chunk(t, r, 4 * kk + 2 * (lane >> 5) + 1)));
+    }
+  }
+};
+
+// Rows of the contraction, R values of the operand's index each.
+template <typename T, int R, int WAVES>
+struct AcrossLds {
+  static constexpr int kRow = R * sizeof(T), kLanes = kRow / 16, kRows = 64 / kLanes;       // rows of an instruction
+  static constexpr int kBytes = kDeep<T> * kRow, Q = kBytes / 1024 / WAVES, kPer = 16 / sizeof(T);
+  static_assert(kLanes <= 64 && kBytes % (1024 * WAVES) == 0);
+  static __device__ __forceinline__ int row(int q, int wave, int lane) { return kRows * (q * WAVES + wave) + lane / kLanes; }
+  // pairs of chunks stay together for the transpose loads of 4 rows of 32 bytes; the two halves of a
+  // wave read float32 rows 8 apart from different banks
+  static __device__ __forceinline__ int turn(int row) {
+    return sizeof(T) == 4 ? (row >> 3 & 1) * 8 : kRow >= 256 ? 2 * (row & 7) : 2 * (row >> 1 & 3);
+  }
+  static __device__ __forceinline__ int first(int row, int lane) { return ((lane % kLanes) ^ turn(row)) * kPer; }
+  static __device__ __forceinline__ uint8_t* place(uint8_t* t, int q, int wave) { return t + 1024 * (q * WAVES + wave); }
+  static __device__ __forceinline__ const uint8_t* at(const uint8_t* t, int row, int col) {
+    return t + row * kRow + ((col / kPer) ^ turn(row)) * 16 + col % kPer * sizeof(T);
+  }
+  static __device__ __forceinline__ void read(const uint8_t* t, int block, int kk, int lane, Octet<T>& o) {
+    if constexpr (sizeof(T) == 2) {
+      const int r = 16 * kk + 8 * (lane >> 5) + ((lane & 15) >> 2), c = 32 * block + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+      const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at(t, r, c));
+      const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at(t, r + 4, c));
+      o.v.v = __builtin_bit_cast(Chunk<bf16_t>::vec, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const int r = 16 * kk + 8 * (lane >> 5), c = 32 * block + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o.a.v[j] = *reinterpret_cast<const float*>(at(t, r + j, c));
+        o.b.v[j] = *reinterpret_cast<const float*>(at(t, r + 4 + j, c));
+      }
+    }
+  }
+};
+
+// An octet as an operand.  FAR: an infinity stays one (split.hpp).
+template <bool FAR>
+__device__ __forceinline__ Frag<1> operand(const Octet<bf16_t>& o) {
+  Frag<1> f;
+  f.p[0] = __builtin_bit_cast(b8, o.v.v);
+  return f;
+}
+template <bool FAR>
+__device__ __forceinline__ Frag<3> operand(const Octet<float>& o) {
+  Frag<3> f;
+  const float x[8] = {o.at(0), o.at(1), o.at(2), o.at(3), o.at(4), o.at(5), o.at(6), o.at(7)};
+  to_frag<FAR>(x, f);
+  return f;
+}
+
+// The accumulators of a wave: MB x NB blocks of 32 x 32, C transposed (lane l holds row l % 32 of
+// a block and columns 8 (i / 4) + 4 (l / 32) + i % 4).  In float32 a sum of thousands of products, six
+// pieces each, would round more than their products do: what has come together in `part` goes to `all`
+// every kTurn contraction values.
+template <typename T, int MB, int NB>
+struct Sums {
+  static constexpr bool kTwo = sizeof(T) == 4;
+  static constexpr int kTurn = 256;
+  f16v part[MB][NB], all[kTwo ? MB : 1][kTwo ? NB : 1];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          part[i][j][r] = 0.f;
+          if constexpr (kTwo) all[i][j][r] = 0.f;
+        }
+  }
+  __device__ __forceinline__ void gather() {
+    if constexpr (kTwo) {
+#pragma unroll
+      for (int i = 0; i < MB; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            all[i][j][r] += part[i][j][r];
+            part[i][j][r] = 0.f;
+          }
+    }
+  }
+  __device__ __forceinline__ const f16v& total(int i, int j) const {
+    if constexpr (kTwo)
+      return all[i][j];
+    else
+      return part[i][j];
+  }
+  __device__ __forceinline__ bool finite() const {
+    bool ok = true;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) ok &= fabsf(total(i, j)[r]) < INFINITY;
+    return ok;
+  }
+};
+
+// One staged step's products.  bias: colsum[j] takes the sum of the wave's B operand.
+template <typename T, typename TA, typename TB, int MB, int NB, bool FAR, bool BIAS = false>
+__device__ __forceinline__ void multiply(const uint8_t* ta, const uint8_t* tb, int wm, int wn, int lane, Sums<T, MB, NB>& s,
+                                         float* colsum = nullptr, bool bias = false) {
+#pragma unroll
+  for (int kk = 0; kk < kDeep<T> / 16; ++kk) {
+    Frag<kPlanes<T>> fb[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      Octet<T> o;
+      TB::read(tb, wn * NB + j, kk, lane, o);
+      if (BIAS && bias) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) colsum[j] += o.at(e);
+      }
+      fb[j] = operand<FAR>(o);
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      Octet<T> o;
+      TA::read(ta, wm * MB + i, kk, lane, o);
+      const Frag<kPlanes<T>> fa = operand<FAR>(o);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) s.part[i][j] = mma(fb[j], fa, s.part[i][j]);
+    }
+  }
+}
+
+// The loop over the steps: load(step, buffer) fetches, product(buffer, step) multiplies.  The buffers are
+// separate arrays and take turns by name, so that the compiler sees that what is fetched is not what
+// is read, and waits for nothing in between.
+// All waves meet: what this one fetched is in LDS, what it read has been read.  The fences are the
+// wave's, for the compiler alone.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_s_waitcnt(0x0070);              // vmcnt 0, lgkmcnt 0
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+template <typename Load, typename Product>
+__device__ __forceinline__ void walk(int steps, Load&& load, Product&& product) {
+  if (steps <= 0) return;
+  load(0, 0);
+  meet();
+  int t = 0;
+  for (; t + 2 <= steps; t += 2) {
+    load(t + 1, 1);
+    product(0, t);
+    meet();
+    if (t + 2 < steps) load(t + 2, 0);
+    product(1, t + 1);
+    meet();
+  }
+  if (t < steps) product(0, t);
+}
+
+// eight values, loaded and stored by the type's chunks; left: values there are
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, float* v) {
+  constexpr int N = Chunk<T>::kN;
+#pragma unroll
+  for (int c = 0; c < 8; c += N) load_chunk(p + c, left - c, v + c);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int left, const float* v) {
+  constexpr int N = Chunk<T>::kN;
+#pragma unroll
+  for (int c = 0; c < 8; c += N) store_chunk(p + c, left - c, v + c);
+}
+
+__device__ __forceinline__ void wave_in_order() {  // LDS accesses of a wave on its own stay in order
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Hands a wave's sums out as rows: out(row of the wave's blocks, first column of eight, values), by
+// way of 32 x 32 NB float32 of LDS that are the wave's own, whose 16-byte chunks are permuted by the row.
+template <typename T, int MB, int NB, typename Out>
+__device__ __forceinline__ void hand_out(const Sums<T, MB, NB>& s, float* lds, int lane, Out&& out) {
+  constexpr int C = 8 * NB, L = 4 * NB, R = 64 / L;           // chunks of a row, lanes of a row, rows at a time
+#pragma unroll
+  for (int i = 0; i < MB; ++i) {
+    wave_in_order();
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f16v& v = s.total(i, j);
+        const int row = lane & 31, c = 8 * j + 2 * q + (lane >> 5);
+        reinterpret_cast<f4*>(lds)[row * C + (c ^ (row & (C - 1)))] = f4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+      }
+    wave_in_order();
+#pragma unroll
+    for (int p = 0; p < 32 / R; ++p) {
+      const int row = p * R + lane / L, c = lane % L * 2;
+      const f4 a = reinterpret_cast<const f4*>(lds)[row * C + (c ^ (row & (C - 1)))];
+      const f4 b = reinterpret_cast<const f4*>(lds)[row * C + ((c + 1) ^ (row & (C - 1)))];
+      float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      out(32 * i + row, 4 * c, v);
+    }
+  }
 }
 
 }  // namespace tpc

@@ -17,6 +17,7 @@ __device__ __forceinline__ int64_t part_slot(const Part& p, int size) {
   return 2 * (int64_t)(p.first / size) + (p.first == p.lo);
 }
 
+// Rows of any length and alignment: staged through registers.
 template <typename T, int B, int W, bool EVEN>
 __global__ void __launch_bounds__(kGemmThreads)
     k_grouped_weight(GroupedWeightArgs a, int size, int n_rows, int n_cols) {
@@ -143,21 +144,134 @@ __global__ void __launch_bounds__(kGemmThreads)
   }
 }
 
-// groups of several parts: their sum, in the parts' order
+// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32.  The rows' numbers are
+// loaded a step ahead of the rows, a lane each.
+template <typename T, int WM, int WN, int MB, int NB>
+__global__ void __launch_bounds__(64 * WM * WN, 2)
+    k_grouped_weight_fast(GroupedWeightArgs a, int size, int n_rows, int n_cols) {
+  constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
+  typedef AcrossLds<T, BM, W> TA;
+  typedef AcrossLds<T, BN, W> TB;
+  __shared__ __attribute__((aligned(16))) uint8_t a0[TA::kBytes], b0[TB::kBytes], a1[TA::kBytes], b1[TB::kBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = n_rows * n_cols, tile = blockIdx.x % tiles;
+  Part part;
+  const int n = (int)a.n;
+  if (!find_part(a.ptr, a.n_groups + 1, n, size, blockIdx.x / tiles, part) || part.group == a.n_groups) return;
+  const int k0 = tile / n_cols * BM, c0 = tile % n_cols * BN, end = min(part.hi, part.first + size);
+  const int wm = wave % WM, wn = wave / WM;
+  const bool bias = a.grad_bias && k0 == 0 && wm == 0;
+  const T* zeros = reinterpret_cast<const T*>(kZeros);
+  int next = 0;                            // the slot that this lane knows of the next step
+  const auto numbers = [&](int t) {
+    const int place = part.first + t * S + (lane & (S - 1));
+    next = a.x_div || a.g_div ? slot_at(a.rows, min(place, end - 1), n) : 0;
+  };
+  const auto load = [&](int t, int buffer) {
+    const int s0 = part.first + t * S;
+#pragma unroll
+    for (int q = 0; q < TA::Q; ++q) {
+      const int r = TA::row(q, wave, lane), slot = __shfl(next, r, 64), row = a.x_div ? slot / a.x_div : s0 + r;
+      const T* from = (const T*)a.x + row * a.ldx + min(k0 + TA::first(r, lane), a.k - TA::kPer);
+      fetch16(s0 + r < end ? from : zeros, TA::place(buffer ? a1 : a0, q, wave));
+    }
+#pragma unroll
+    for (int q = 0; q < TB::Q; ++q) {
+      const int r = TB::row(q, wave, lane), slot = __shfl(next, r, 64), row = a.g_div ? slot : s0 + r;
+      const T* from = (const T*)a.gy + row * a.ldg + min(c0 + TB::first(r, lane), a.cols - TB::kPer);
+      fetch16(s0 + r < end ? from : zeros, TB::place(buffer ? b1 : b0, q, wave));
+    }
+    numbers(t + 1);
+  };
+  const int steps = part.first < end ? (end - part.first + S - 1) / S : 0;
+  Sums<T, MB, NB> sums;
+  float colsum[NB];
+  const auto all = [&](auto far) {
+    sums.clear();
+#pragma unroll
+    for (int j = 0; j < NB; ++j) colsum[j] = 0.f;
+    numbers(0);
+    walk(steps, load, [&](int buffer, int t) {
+      multiply<T, TA, TB, MB, NB, far(), true>(buffer ? a1 : a0, buffer ? b1 : b0, wm, wn, lane, sums, colsum, bias);
+      if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) sums.gather();
+    });
+    sums.gather();
+  };
+  all(std::false_type());
+  if constexpr (sizeof(T) == 4) {          // infinities: again, with pieces that keep them
+    if (__syncthreads_or(!sums.finite())) all(std::true_type());
+  }
+  __syncthreads();
+  constexpr int kOwn = 32 * 32 * NB * sizeof(float), kA = TA::kBytes / kOwn, kB = TB::kBytes / kOwn;
+  static_assert(2 * kA + 2 * kB >= W);
+  uint8_t* own = wave < kA ? a0 + wave * kOwn
+                 : wave < kA + kB ? b0 + (wave - kA) * kOwn
+                 : wave < 2 * kA + kB ? a1 + (wave - kA - kB) * kOwn : b1 + (wave - 2 * kA - kB) * kOwn;
+  const bool whole = part.hi - part.lo <= size;
+  const int64_t mat = (int64_t)a.k * a.cols;
+  float* to = whole ? nullptr : a.part + part_slot(part, size) * (mat + a.cols);
+  const int col = c0 + 32 * NB * wn + lane % (4 * NB) * 8, left = a.cols - col;
+  hand_out<T, MB, NB>(sums, reinterpret_cast<float*>(own), lane, [&](int r, int, float* v) {
+    const int row = k0 + 32 * MB * wm + r;
+    if (row >= a.k || left <= 0) return;
+    const int64_t at = (int64_t)row * a.cols + col;
+    if (whole)
+      store8((T*)a.grad_w + part.group * mat + at, left, v);
+    else
+      store8(to + at, left, v);
+  });
+  if (!bias) return;
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const float s = colsum[j] + __shfl_xor(colsum[j], 32, 64);
+    const int c = c0 + 32 * NB * wn + 32 * j + lane;
+    if (lane >= 32 || c >= a.cols) continue;
+    if (whole)
+      ((T*)a.grad_bias)[(int64_t)part.group * a.cols + c] = (T)s;
+    else
+      to[mat + c] = s;
+  }
+}
+
+// Groups of several parts: their sum.  `lanes` threads take every lanes-th part of four values each
+// and are joined in LDS, in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(kGemmThreads)
-    k_grouped_join(GroupedWeightArgs a, int size) {
-  const int n = (int)a.n, e = blockIdx.y;
+    k_grouped_join(GroupedWeightArgs a, int size, int lanes) {
+  __shared__ f4 sums[kGemmThreads];
+  const int n = (int)a.n, e = blockIdx.y, wide = kGemmThreads / lanes;
   const int lo = min(max(a.ptr[e], 0), n), hi = min(max(a.ptr[e + 1], 0), n);
   if (hi - lo <= size) return;
-  const int64_t mat = (int64_t)a.k * a.cols, all = mat + (a.grad_bias ? a.cols : 0);
-  for (int64_t i = (int64_t)blockIdx.x * kGemmThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kGemmThreads) {
-    float s = 0.f;
-    for (int64_t f = lo; f < hi; f += size) s += a.part[(2 * (f / size) + (f == lo)) * (mat + a.cols) + i];
-    if (i < mat)
-      ((T*)a.grad_w)[e * mat + i] = (T)s;
-    else
-      ((T*)a.grad_bias)[(int64_t)e * a.cols + i - mat] = (T)s;
+  const int64_t mat = (int64_t)a.k * a.cols, all = mat + (a.grad_bias ? a.cols : 0), pitch = mat + a.cols;
+  const int which = threadIdx.x / wide, parts = (hi - lo + size - 1) / size;
+  for (int64_t i0 = (int64_t)blockIdx.x * wide * 4; i0 < all; i0 += (int64_t)gridDim.x * wide * 4) {
+    const int64_t i = i0 + threadIdx.x % wide * 4;
+    f4 s = {0.f, 0.f, 0.f, 0.f};
+    if (i < all) {
+#pragma unroll 4
+      for (int p = which; p < parts; p += lanes) {
+        const int64_t f = lo + (int64_t)p * size;
+        float v[4];
+        load_chunk(a.part + (2 * (f / size) + (p == 0)) * pitch + i, (int)min(all - i, (int64_t)4), v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] += v[j];
+      }
+    }
+    for (int m = lanes >> 1; m > 0; m >>= 1) {
+      __syncthreads();
+      sums[threadIdx.x] = s;
+      __syncthreads();
+      if (which < m) s += sums[threadIdx.x + m * wide];
+    }
+    if (which == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + j < mat)
+          ((T*)a.grad_w)[e * mat + i + j] = (T)s[j];
+        else if (i + j < all)
+          ((T*)a.grad_bias)[(int64_t)e * a.cols + i + j - mat] = (T)s[j];
+      }
+    }
   }
 }
 
@@ -167,10 +281,12 @@ struct WeightShape {
   int tile, size;
   int64_t tiles;
 };
-WeightShape weight_shape(int64_t n, int n_groups, int k, int cols) {
+WeightShape weight_shape(int dtype, int64_t n, int n_groups, int k, int cols) {
   WeightShape s;
+  const auto count = [&](int t) { return (int64_t)((k + t - 1) / t) * ((cols + t - 1) / t); };
   s.tile = k > 64 && cols > 64 ? 128 : 64;
-  s.tiles = (int64_t)((k + s.tile - 1) / s.tile) * ((cols + s.tile - 1) / s.tile);
+  if (dtype == TP_BF16 && k > 128 && cols > 128 && count(256) * n_groups >= 256) s.tile = 256;
+  s.tiles = count(s.tile);
   int64_t rows = n * 3 / (2 * n_groups);
   if (s.tiles * n_groups < 512) rows = std::min(rows, n * s.tiles / 512);
   s.size = (int)std::min<int64_t>(1 << 30, std::max<int64_t>(256, (rows + 63) / 64 * 64));
@@ -179,30 +295,39 @@ WeightShape weight_shape(int64_t n, int n_groups, int k, int cols) {
 
 template <typename T>
 hipError_t weight_grad(const GroupedWeightArgs& a) {
-  const WeightShape s = weight_shape(a.n, a.n_groups, a.k, a.cols);
-  const int64_t parts = a.n / s.size + a.n_groups + 1;
-  if (parts * s.tiles > 0xffffffffLL / kGemmThreads) return hipErrorInvalidConfiguration;
-  const int nr = (a.k + s.tile - 1) / s.tile, nc = (a.cols + s.tile - 1) / s.tile;
-  const dim3 grid((unsigned)(parts * s.tiles));
-  const auto go = [&](auto b, auto w, auto even) {
-    hipLaunchKernelGGL((k_grouped_weight<T, b(), w(), even()>), grid, dim3(kGemmThreads), 0, a.stream, a, s.size, nr, nc);
-    return hipGetLastError();
-  };
-  const auto wide = [&](auto even) {
-    return s.tile == 128 ? go(std::integral_constant<int, 128>(), std::integral_constant<int, 64>(), even)
-                         : go(std::integral_constant<int, 64>(), std::integral_constant<int, 32>(), even);
-  };
-  hipError_t e = a.k % 8 == 0 && a.cols % 8 == 0 ? wide(std::true_type()) : wide(std::false_type());
+  WeightShape s = weight_shape(a.dtype, a.n, a.n_groups, a.k, a.cols);
+  constexpr int N = 16 / sizeof(T);
+  const auto aligned = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const bool fast = a.k % N == 0 && a.cols % N == 0 && a.ldx % N == 0 && a.ldg % N == 0 && aligned(a.x) && aligned(a.gy);
+  const int tile = fast ? s.tile : 64;
+  const int nr = (a.k + tile - 1) / tile, nc = (a.cols + tile - 1) / tile;
+  const int64_t blocks = (a.n / s.size + a.n_groups + 1) * nr * nc;
+  if (blocks > 0xffffffffLL / 512) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks);
+  if (!fast)
+    hipLaunchKernelGGL((k_grouped_weight<T, 64, 32, false>), grid, dim3(kGemmThreads), 0, a.stream, a, s.size, nr, nc);
+  else if (tile == 64)
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 2, 1, 1>), grid, dim3(256), 0, a.stream, a, s.size, nr, nc);
+  else if constexpr (sizeof(T) == 4)
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 2, 2, 2>), grid, dim3(256), 0, a.stream, a, s.size, nr, nc);
+  else if (tile == 128)
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 4, 2, 1>), grid, dim3(512), 0, a.stream, a, s.size, nr, nc);
+  else
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 4, 4, 2>), grid, dim3(512), 0, a.stream, a, s.size, nr, nc);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n <= s.size) return e;
-  const int64_t blocks = std::min<int64_t>(256, ((int64_t)a.k * a.cols + a.cols + kGemmThreads - 1) / kGemmThreads);
-  hipLaunchKernelGGL(k_grouped_join<T>, dim3((unsigned)blocks, a.n_groups), dim3(kGemmThreads), 0, a.stream, a, s.size);
+  int lanes = 1;                           // of the parts that one group can have
+  while (lanes < 8 && 4 * lanes < a.n / s.size) lanes <<= 1;
+  const int64_t wide = kGemmThreads / lanes * 4;
+  const int64_t joins = std::min<int64_t>(1024, ((int64_t)a.k * a.cols + a.cols + wide - 1) / wide);
+  hipLaunchKernelGGL(k_grouped_join<T>, dim3((unsigned)joins, a.n_groups), dim3(kGemmThreads), 0, a.stream, a, s.size, lanes);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t grouped_weight_workspace(int, int64_t n, int n_groups, int k, int cols) {
-  const WeightShape s = weight_shape(n, n_groups, k, cols);
+size_t grouped_weight_workspace(int dtype, int64_t n, int n_groups, int k, int cols) {
+  const WeightShape s = weight_shape(dtype, n, n_groups, k, cols);
   return n <= s.size ? 0 : 2 * ((size_t)(n / s.size) + 1) * ((size_t)k * cols + cols) * sizeof(float);
 }
 
