@@ -139,14 +139,14 @@ __global__ void __launch_bounds__(kGemmThreads)
   }
 }
 
-// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32.
-template <typename T, int WM, int WN, int MB, int NB, bool ALONG>
+// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32, D buffers.
+template <typename T, int WM, int WN, int MB, int NB, int D, bool ALONG>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
     k_grouped_fast(GroupedArgs a, int n_rows, int n_cols) {
   constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
   typedef AlongLds<T, BM, W> TA;
   typedef typename std::conditional<ALONG, AlongLds<T, BN, W>, AcrossLds<T, BN, W>>::type TB;
-  __shared__ __attribute__((aligned(16))) uint8_t a0[TA::kBytes], b0[TB::kBytes], a1[TA::kBytes], b1[TB::kBytes];
+  TPC_BUFFERS(D, TA, TB);
   __shared__ int arow[BM], crow[BM];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int rt, ct;
@@ -184,26 +184,26 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     for (int q = 0; q < TA::Q; ++q) pa[q] = (const T*)a.a + arow[TA::row(q, wave, lane)] * a.lda + TA::first(lane);
     const int steps = (a.k + S - 1) / S;
     const T* zeros = reinterpret_cast<const T*>(kZeros);
-    const auto load = [&](int t, int buffer) {
+    const auto load = [&](int t, auto buffer) {
       const int k0 = t * S, mine = k0 + TA::first(lane);
       if (k0 + S <= a.k) {
 #pragma unroll
-        for (int q = 0; q < TA::Q; ++q) fetch16(pa[q] + k0, TA::place(buffer ? a1 : a0, q, wave));
+        for (int q = 0; q < TA::Q; ++q) fetch16(pa[q] + k0, TA::place(buffers.a(buffer), q, wave));
 #pragma unroll
         for (int q = 0; q < TB::Q; ++q)
-          fetch16(pb[q] + (ALONG ? k0 : (int64_t)k0 * a.cols), TB::place(buffer ? b1 : b0, q, wave));
+          fetch16(pb[q] + (ALONG ? k0 : (int64_t)k0 * a.cols), TB::place(buffers.b(buffer), q, wave));
       } else {
 #pragma unroll
-        for (int q = 0; q < TA::Q; ++q) fetch16(mine < a.k ? pa[q] + k0 : zeros, TA::place(buffer ? a1 : a0, q, wave));
+        for (int q = 0; q < TA::Q; ++q) fetch16(mine < a.k ? pa[q] + k0 : zeros, TA::place(buffers.a(buffer), q, wave));
 #pragma unroll
         for (int q = 0; q < TB::Q; ++q)
           fetch16((ALONG ? mine : k0 + TB::row(q, wave, lane)) < a.k ? pb[q] + (ALONG ? k0 : (int64_t)k0 * a.cols) : zeros,
-                  TB::place(buffer ? b1 : b0, q, wave));
+                  TB::place(buffers.b(buffer), q, wave));
       }
     };
     const auto all = [&](auto far) {
-      walk(steps, load, [&](int buffer, int t) {
-        multiply<T, TA, TB, MB, NB, far()>(buffer ? a1 : a0, buffer ? b1 : b0, wm, wn, lane, sums);
+      walk<D, TA::Q + TB::Q>(steps, load, [&](int t, auto buffer) {
+        multiply<T, TA, TB, MB, NB, far()>(buffers.a(buffer), buffers.b(buffer), wm, wn, lane, sums);
         if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) sums.gather();
       });
       sums.gather();
@@ -219,16 +219,11 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     }
   }
   __syncthreads();
-  // the waves' own parts of the buffers
-  constexpr int kOwn = 32 * 32 * NB * sizeof(float), kA = TA::kBytes / kOwn, kB = TB::kBytes / kOwn;
-  static_assert(2 * kA + 2 * kB >= W);
-  uint8_t* own = wave < kA ? a0 + wave * kOwn
-                 : wave < kA + kB ? b0 + (wave - kA) * kOwn
-                 : wave < 2 * kA + kB ? a1 + (wave - kA - kB) * kOwn : b1 + (wave - 2 * kA - kB) * kOwn;
+  float* own = buffers.template own<32 * 32 * NB * (int)sizeof(float), W>(wave);
   const int col = col0 + 32 * NB * wn + lane % (4 * NB) * 8, left = a.cols - col;
   float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (a.bias && !none && left > 0) load8((const T*)a.bias + (int64_t)part.group * a.cols + col, left, bias);
-  hand_out<T, MB, NB>(sums, reinterpret_cast<float*>(own), lane, [&](int r, int, float* v) {
+  hand_out<T, MB, NB>(sums, own, lane, [&](int r, int, float* v) {
     const int row = crow[32 * MB * wm + r];
     if (row < 0 || left <= 0) return;
 #pragma unroll
@@ -258,13 +253,13 @@ hipError_t tiles(const GroupedArgs& a, int bm, int bn, F&& f) {
   return hipGetLastError();
 }
 
-template <typename T, int WM, int WN, int MB, int NB>
+template <typename T, int WM, int WN, int MB, int NB, int D>
 hipError_t fast(const GroupedArgs& a) {
   return tiles(a, 32 * WM * MB, 32 * WN * NB, [&](dim3 grid, int rows, int cols) {
     if (a.transposed)
-      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, true>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, true>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
     else
-      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, false>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, false>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
   });
 }
 
@@ -285,12 +280,15 @@ hipError_t product(const GroupedArgs& a) {
   const auto whole = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   if (a.k % N || a.cols % N || a.lda % N || !whole(a.a) || !whole(a.w)) return any<T>(a);
   const int64_t even = a.n / a.n_groups;
-  if (even <= 32) return fast<T, 1, 4, 1, 1>(a);
+  if (even <= 32) return fast<T, 1, 2, 1, 1, 4>(a);
   const auto count = [&](int bm, int bn) { return (a.n / bm + a.n_groups / 2) * ((a.cols + bn - 1) / bn); };
-  if constexpr (sizeof(T) == 2)
-    if (even >= 192 && count(256, 256) >= 256) return fast<T, 2, 4, 4, 2>(a);
-  if (count(128, 128) >= 256) return fast<T, 2, 2, 2, 2>(a);
-  return fast<T, 2, 2, 1, 1>(a);
+  if constexpr (sizeof(T) == 2) {
+    if (even >= 192 && count(256, 256) >= 512) return fast<T, 2, 4, 4, 2, 2>(a);
+    return fast<T, 1, 4, 2, 1, 2>(a);
+  } else {
+    if (count(128, 128) >= 256) return fast<T, 2, 2, 2, 2, 2>(a);
+    return fast<T, 2, 2, 1, 1, 2>(a);
+  }
 }
 
 }  // namespace

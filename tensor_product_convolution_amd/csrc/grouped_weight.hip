@@ -144,15 +144,15 @@ __global__ void __launch_bounds__(kGemmThreads)
   }
 }
 
-// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32.  The rows' numbers are
+// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32, D buffers.  The rows' numbers are
 // loaded a step ahead of the rows, a lane each.
-template <typename T, int WM, int WN, int MB, int NB>
+template <typename T, int WM, int WN, int MB, int NB, int D>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
     k_grouped_weight_fast(GroupedWeightArgs a, int size, int n_rows, int n_cols) {
   constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
   typedef AcrossLds<T, BM, W> TA;
   typedef AcrossLds<T, BN, W> TB;
-  __shared__ __attribute__((aligned(16))) uint8_t a0[TA::kBytes], b0[TB::kBytes], a1[TA::kBytes], b1[TB::kBytes];
+  TPC_BUFFERS(D, TA, TB);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = n_rows * n_cols, tile = blockIdx.x % tiles;
   Part part;
@@ -167,19 +167,19 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     const int place = part.first + t * S + (lane & (S - 1));
     next = a.x_div || a.g_div ? slot_at(a.rows, min(place, end - 1), n) : 0;
   };
-  const auto load = [&](int t, int buffer) {
+  const auto load = [&](int t, auto buffer) {
     const int s0 = part.first + t * S;
 #pragma unroll
     for (int q = 0; q < TA::Q; ++q) {
       const int r = TA::row(q, wave, lane), slot = __shfl(next, r, 64), row = a.x_div ? slot / a.x_div : s0 + r;
       const T* from = (const T*)a.x + row * a.ldx + min(k0 + TA::first(r, lane), a.k - TA::kPer);
-      fetch16(s0 + r < end ? from : zeros, TA::place(buffer ? a1 : a0, q, wave));
+      fetch16(s0 + r < end ? from : zeros, TA::place(buffers.a(buffer), q, wave));
     }
 #pragma unroll
     for (int q = 0; q < TB::Q; ++q) {
       const int r = TB::row(q, wave, lane), slot = __shfl(next, r, 64), row = a.g_div ? slot : s0 + r;
       const T* from = (const T*)a.gy + row * a.ldg + min(c0 + TB::first(r, lane), a.cols - TB::kPer);
-      fetch16(s0 + r < end ? from : zeros, TB::place(buffer ? b1 : b0, q, wave));
+      fetch16(s0 + r < end ? from : zeros, TB::place(buffers.b(buffer), q, wave));
     }
     numbers(t + 1);
   };
@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
 #pragma unroll
     for (int j = 0; j < NB; ++j) colsum[j] = 0.f;
     numbers(0);
-    walk(steps, load, [&](int buffer, int t) {
-      multiply<T, TA, TB, MB, NB, far(), true>(buffer ? a1 : a0, buffer ? b1 : b0, wm, wn, lane, sums, colsum, bias);
+    walk<D, TA::Q + TB::Q>(steps, load, [&](int t, auto buffer) {
+      multiply<T, TA, TB, MB, NB, far(), true>(buffers.a(buffer), buffers.b(buffer), wm, wn, lane, sums, colsum, bias);
       if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) sums.gather();
     });
     sums.gather();
@@ -202,16 +202,12 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     if (__syncthreads_or(!sums.finite())) all(std::true_type());
   }
   __syncthreads();
-  constexpr int kOwn = 32 * 32 * NB * sizeof(float), kA = TA::kBytes / kOwn, kB = TB::kBytes / kOwn;
-  static_assert(2 * kA + 2 * kB >= W);
-  uint8_t* own = wave < kA ? a0 + wave * kOwn
-                 : wave < kA + kB ? b0 + (wave - kA) * kOwn
-                 : wave < 2 * kA + kB ? a1 + (wave - kA - kB) * kOwn : b1 + (wave - 2 * kA - kB) * kOwn;
+  float* own = buffers.template own<32 * 32 * NB * (int)sizeof(float), W>(wave);
   const bool whole = part.hi - part.lo <= size;
   const int64_t mat = (int64_t)a.k * a.cols;
   float* to = whole ? nullptr : a.part + part_slot(part, size) * (mat + a.cols);
   const int col = c0 + 32 * NB * wn + lane % (4 * NB) * 8, left = a.cols - col;
-  hand_out<T, MB, NB>(sums, reinterpret_cast<float*>(own), lane, [&](int r, int, float* v) {
+  hand_out<T, MB, NB>(sums, own, lane, [&](int r, int, float* v) {
     const int row = k0 + 32 * MB * wm + r;
     if (row >= a.k || left <= 0) return;
     const int64_t at = (int64_t)row * a.cols + col;
@@ -284,12 +280,13 @@ struct WeightShape {
 WeightShape weight_shape(int dtype, int64_t n, int n_groups, int k, int cols) {
   WeightShape s;
   const auto count = [&](int t) { return (int64_t)((k + t - 1) / t) * ((cols + t - 1) / t); };
-  s.tile = k > 64 && cols > 64 ? 128 : 64;
+  s.tile = k > 64 && cols > 64 && n / 256 * count(128) >= 256 ? 128 : 64;
   if (dtype == TP_BF16 && k > 128 && cols > 128 && count(256) * n_groups >= 256) s.tile = 256;
   s.tiles = count(s.tile);
   int64_t rows = n * 3 / (2 * n_groups);
   if (s.tiles * n_groups < 512) rows = std::min(rows, n * s.tiles / 512);
-  s.size = (int)std::min<int64_t>(1 << 30, std::max<int64_t>(256, (rows + 63) / 64 * 64));
+  const int64_t least = s.tile == 64 && n < 8192 ? 128 : 256;
+  s.size = (int)std::min<int64_t>(1 << 30, std::max<int64_t>(least, (rows + 63) / 64 * 64));
   return s;
 }
 
@@ -307,13 +304,13 @@ hipError_t weight_grad(const GroupedWeightArgs& a) {
   if (!fast)
     hipLaunchKernelGGL((k_grouped_weight<T, 64, 32, false>), grid, dim3(kGemmThreads), 0, a.stream, a, s.size, nr, nc);
   else if (tile == 64)
-    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 2, 1, 1>), grid, dim3(256), 0, a.stream, a, s.size, nr, nc);
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 2, 1, 1, 2>), grid, dim3(256), 0, a.stream, a, s.size, nr, nc);
   else if constexpr (sizeof(T) == 4)
-    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 2, 2, 2>), grid, dim3(256), 0, a.stream, a, s.size, nr, nc);
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 2, 2, 2, 2>), grid, dim3(256), 0, a.stream, a, s.size, nr, nc);
   else if (tile == 128)
-    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 4, 2, 1>), grid, dim3(512), 0, a.stream, a, s.size, nr, nc);
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 4, 2, 1, 2>), grid, dim3(512), 0, a.stream, a, s.size, nr, nc);
   else
-    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 4, 4, 2>), grid, dim3(512), 0, a.stream, a, s.size, nr, nc);
+    hipLaunchKernelGGL((k_grouped_weight_fast<T, 2, 4, 4, 2, 2>), grid, dim3(512), 0, a.stream, a, s.size, nr, nc);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n <= s.size) return e;
   int lanes = 1;                           // of the parts that one group can have

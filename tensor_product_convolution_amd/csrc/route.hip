@@ -193,7 +193,7 @@ hipError_t pick_route(const RouteArgs& a, F&& f) {
 // ---- order by group -------------------------------------------------------------------
 // Entries are numbered by waves, each over a run of consecutive ones.  Group n_groups is that
 // of the entries without a group; lanes past the end have n_groups + 1.
-constexpr int kSmallThreads = 512, kSmallMost = 8192;
+constexpr int kSmallWaves = 16;
 
 __device__ __forceinline__ int entry_group(const int32_t* index, int64_t i, int64_t end, int n_groups) {
   if (i >= end) return n_groups + 1;
@@ -217,37 +217,45 @@ __device__ __forceinline__ void wave_order() {     // LDS accesses of a wave on 
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ void wave_count(const int32_t* index, int64_t first, int64_t end, int n_groups, int bits, int* cnt) {
-  const int lane = threadIdx.x & 63;
-  int g = entry_group(index, first + lane, end, n_groups);
-  for (int64_t i = first; i < end; i += 64) {
-    const int now = g;
-    g = entry_group(index, i + 64 + lane, end, n_groups);
-    const u64 m = same_group(now, bits);
-    if (now <= n_groups && (m & ((1ull << lane) - 1)) == 0) cnt[now] += __popcll(m);
-    wave_order();
+// A wave's run goes in blocks of kBlock entries, kEach a lane, loaded together.
+constexpr int kEach = 8, kBlock = 64 * kEach;
+struct Block {
+  int g[kEach];
+  u64 same[kEach];
+  __device__ __forceinline__ void load(const int32_t* index, int64_t first, int64_t end, int n_groups, int bits) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) g[j] = entry_group(index, first + 64 * j + lane, end, n_groups);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) same[j] = same_group(g[j], bits);
   }
-}
-
-__device__ __forceinline__ void wave_place(const int32_t* index, int64_t first, int64_t end, int n_groups, int bits, int* at,
-                                           int32_t* rows) {
-  const int lane = threadIdx.x & 63;
-  int g = entry_group(index, first + lane, end, n_groups);
-  for (int64_t i = first; i < end; i += 64) {
-    const int now = g;
-    g = entry_group(index, i + 64 + lane, end, n_groups);
-    const u64 m = same_group(now, bits), before = m & ((1ull << lane) - 1);
-    if (now <= n_groups) rows[at[now] + __popcll(before)] = (int32_t)(i + lane);
-    wave_order();
-    if (now <= n_groups && before == 0) at[now] += __popcll(m);
-    wave_order();
+  __device__ __forceinline__ void count(int n_groups, int* cnt) const {
+    const u64 before = (1ull << (threadIdx.x & 63)) - 1;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      if (g[j] <= n_groups && (same[j] & before) == 0) cnt[g[j]] += __popcll(same[j]);
+      wave_order();
+    }
   }
-}
+  __device__ __forceinline__ void place(int64_t first, int n_groups, int* at, int32_t* rows) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const u64 before = same[j] & ((1ull << lane) - 1);
+      const int to = g[j] <= n_groups ? at[g[j]] : 0;
+      wave_order();
+      if (g[j] <= n_groups) {
+        rows[to + __popcll(before)] = (int32_t)(first + 64 * j + lane);
+        if (before == 0) at[g[j]] = to + __popcll(same[j]);
+      }
+      wave_order();
+    }
+  }
+};
 
 // v[i] for i < n in LDS becomes the sum of those before it; every thread takes a run
-template <int THREADS>
 __device__ __forceinline__ void block_scan(int* v, int n, int* waves) {
-  const int run = (n + THREADS - 1) / THREADS, first = threadIdx.x * run, last = min(n, first + run);
+  const int run = (n + (int)blockDim.x - 1) / (int)blockDim.x, first = threadIdx.x * run, last = min(n, first + run);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int s = 0;
   for (int i = first; i < last; ++i) s += v[i];
@@ -269,22 +277,24 @@ __device__ __forceinline__ void block_scan(int* v, int n, int* waves) {
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSmallThreads)
+// one workgroup for all: a wave has one block
+__global__ void __launch_bounds__(64 * kSmallWaves)
     k_group_small(const int32_t* __restrict__ index, int n, int n_groups, int bits, int32_t* __restrict__ ptr,
                   int32_t* __restrict__ rows) {
-  constexpr int kWaves = kSmallThreads / 64;
-  extern __shared__ int lds[];             // [kWaves][n_groups + 1], [n_groups + 1]
-  __shared__ int waves[kWaves];
-  const int G = n_groups + 1, wave = threadIdx.x >> 6;
-  int* total = lds + kWaves * G;
-  for (int i = threadIdx.x; i < kWaves * G; i += kSmallThreads) lds[i] = 0;
+  extern __shared__ int lds[];             // [waves][n_groups + 1], [n_groups + 1]
+  __shared__ int sums[kSmallWaves];
+  const int G = n_groups + 1, wave = threadIdx.x >> 6, threads = blockDim.x, waves = threads >> 6;
+  int* total = lds + waves * G;
+  const int first = wave * kBlock;
+  Block block;
+  block.load(index, first, n, n_groups, bits);
+  for (int i = threadIdx.x; i < waves * G; i += threads) lds[i] = 0;
   __syncthreads();
-  const int run = ((n + kWaves - 1) / kWaves + 63) / 64 * 64, first = min(n, wave * run), end = min(n, first + run);
-  wave_count(index, first, end, n_groups, bits, lds + wave * G);
+  block.count(n_groups, lds + wave * G);
   __syncthreads();
-  for (int g = threadIdx.x; g < G; g += kSmallThreads) {
+  for (int g = threadIdx.x; g < G; g += threads) {
     int s = 0;
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < waves; ++w) {
       const int t = lds[w * G + g];
       lds[w * G + g] = s;
       s += t;
@@ -292,11 +302,12 @@ __global__ void __launch_bounds__(kSmallThreads)
     total[g] = s;
   }
   __syncthreads();
-  block_scan<kSmallThreads>(total, G, waves);
-  for (int i = threadIdx.x; i < kWaves * G; i += kSmallThreads) lds[i] += total[i % G];
-  for (int g = threadIdx.x; g < G; g += kSmallThreads) ptr[g] = total[g];
+  block_scan(total, G, sums);
+  for (int w = 0; w < waves; ++w)
+    for (int g = threadIdx.x; g < G; g += threads) lds[w * G + g] += total[g];
+  for (int g = threadIdx.x; g < G; g += threads) ptr[g] = total[g];
   __syncthreads();
-  wave_place(index, first, end, n_groups, bits, lds + wave * G, rows);
+  block.place(first, n_groups, lds + wave * G, rows);
 }
 
 // counts [n_groups + 1][units]: a wave is a unit of `run` entries
@@ -311,7 +322,12 @@ __global__ void __launch_bounds__(kThreads)
   wave_order();
   if (unit >= units) return;
   const int64_t first = (int64_t)unit * run;
-  wave_count(index, first, min(n, first + run), n_groups, bits, cnt);
+  const int64_t end = min(n, first + run);
+  for (int64_t i = first; i < end; i += kBlock) {
+    Block block;
+    block.load(index, i, end, n_groups, bits);
+    block.count(n_groups, cnt);
+  }
   for (int g = lane; g < G; g += 64) counts[(int64_t)g * units + unit] = cnt[g];
 }
 
@@ -354,7 +370,7 @@ __global__ void __launch_bounds__(kThreads)
   int* start = lds + (kThreads / 64) * G;
   for (int g = threadIdx.x; g < G; g += kThreads) start[g] = total[g];
   __syncthreads();
-  block_scan<kThreads>(start, G, waves);
+  block_scan(start, G, waves);
   if (blockIdx.x == 0)
     for (int g = threadIdx.x; g < G; g += kThreads) ptr[g] = start[g];
   if (unit >= units) return;
@@ -362,11 +378,20 @@ __global__ void __launch_bounds__(kThreads)
   for (int g = lane; g < G; g += 64) at[g] = start[g] + counts[(int64_t)g * units + unit];
   wave_order();
   const int64_t first = (int64_t)unit * run;
-  wave_place(index, first, min(n, first + run), n_groups, bits, at, rows);
+  const int64_t end = min(n, first + run);
+  for (int64_t i = first; i < end; i += kBlock) {
+    Block block;
+    block.load(index, i, end, n_groups, bits);
+    block.place(i, n_groups, at, rows);
+  }
 }
 
-// entries of a unit: a few steps of a wave, at most 2,048 units (they are scanned group by group)
-int unit_run(int64_t n) { return (int)std::max<int64_t>(512, ((n + 2047) / 2048 + 63) / 64 * 64); }
+// entries of a unit: whole blocks, at most 2,048 units (they are scanned group by group)
+int unit_run(int64_t n) { return (int)((n / 2048 + kBlock) / kBlock * kBlock); }
+// waves of the one workgroup, whose counters fit 64 KB of LDS
+int small_waves(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(kSmallWaves + 1, (n + kBlock - 1) / kBlock)); }
+size_t small_lds(int64_t n, int n_groups) { return (small_waves(n) + 1) * (size_t)(n_groups + 1) * sizeof(int); }
+bool is_small(int64_t n, int n_groups) { return small_waves(n) <= kSmallWaves && small_lds(n, n_groups) <= 65536 - 256; }
 int unit_count(int64_t n) { return (int)((n + unit_run(n) - 1) / unit_run(n)); }
 
 // ---- sums over a row's choices ------------------------------------------------------------
@@ -442,16 +467,15 @@ hipError_t route_backward(const RouteArgs& a) {
 }
 
 size_t group_workspace_bytes(int64_t n, int n_groups) {
-  return n <= kSmallMost ? 0 : ((size_t)unit_count(n) + 1) * (n_groups + 1) * sizeof(int32_t);
+  return is_small(n, n_groups) ? 0 : ((size_t)unit_count(n) + 1) * (n_groups + 1) * sizeof(int32_t);
 }
 
 hipError_t group_rows(const int32_t* index, int64_t n, int n_groups, int32_t* ptr, int32_t* rows, void* ws, hipStream_t st) {
   const int G = n_groups + 1;
   int bits = 1;
   while ((1 << bits) < n_groups + 2) ++bits;
-  if (n <= kSmallMost) {
-    const size_t lds = (kSmallThreads / 64 + 1) * (size_t)G * sizeof(int);
-    hipLaunchKernelGGL(k_group_small, dim3(1), dim3(kSmallThreads), lds, st, index, (int)n, n_groups, bits, ptr, rows);
+  if (is_small(n, n_groups)) {
+    hipLaunchKernelGGL(k_group_small, dim3(1), dim3(64 * small_waves(n)), small_lds(n, n_groups), st, index, (int)n, n_groups, bits, ptr, rows);
     return hipGetLastError();
   }
   const int run = unit_run(n), units = unit_count(n);
