@@ -177,115 +177,133 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// One pass over blocks of rows; a workgroup's part of the weight gradients stays in registers
-// until its last block.  part [gridDim.x][2][d]; a single workgroup writes the gradients itself.
-template <typename T, bool INTER, bool NORM>
+// One pass over blocks of rows, first their queries, then their keys; a workgroup's part of the weight
+// gradients stays in registers until its last block.  part [gridDim.x][2][d]; a single workgroup
+// writes the gradients itself.  Products and sums are written as the fused operations they are, so that
+// the variants round alike.  Weights and frequencies are read from LDS, by chunk: in registers they
+// leave two waves a SIMD.
+template <typename T, bool INTER, bool NORM, bool POS>
 __global__ void __launch_bounds__(kThreads)
     k_heads_bwd(HeadBwdArgs b) {
   const HeadArgs& a = b.f;
   constexpr int V = 2 * Chunk<T>::kN;
-  __shared__ float2 cs[kTrig];
-  extern __shared__ float sums[];          // [kMaxAxes][rows x heads], then [2^lg chunks of V]
-  const int lane_c = (int)threadIdx.x & ((1 << a.lg) - 1);
+  __shared__ float2 cs[kTrig];             // at the end the waves' weight gradients
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  const int n_chunks = 1 << a.lg, lane_c = (int)threadIdx.x & (n_chunks - 1), heads = a.hq + a.hk, per_axis = a.rows * heads;
+  float *gl = lds, *fl = gl + (NORM ? 2 * n_chunks * V : 0), *sums = fl + (POS ? kMaxAxes * n_chunks * V / 2 : 0);
   const Chunks<T, INTER> c(lane_c, a.d, a.pairs);
-  const int heads = a.hq + a.hk, per_axis = a.rows * heads;
-  float g[2][V], gg[2][V], f[kMaxAxes][V / 2];
+  if ((int)threadIdx.x < n_chunks) {
+    float v[V];
+    if (NORM) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        load_like<T, INTER>(i ? a.gamma_k : a.gamma_q, c, v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) gl[(i * n_chunks + lane_c) * V + j] = v[j];
+      }
+    }
+    if (POS) {
+#pragma unroll
+      for (int x = 0; x < kMaxAxes; ++x)
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j)
+          fl[(x * n_chunks + lane_c) * (V / 2) + j] = x < a.axes && j < c.pairs ? (float)a.freq[(c.pair + j) * a.axes + x] : 0.f;
+    }
+  }
+  float gg[2][V];
 #pragma unroll
   for (int j = 0; j < V; ++j) gg[0][j] = gg[1][j] = 0.f;
-  if (NORM) {
-    load_like<T, INTER>(a.gamma_q, c, g[0]);
-    load_like<T, INTER>(a.gamma_k, c, g[1]);
-  }
-  if (b.grad_pos) {
-#pragma unroll
-    for (int x = 0; x < kMaxAxes; ++x)
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) f[x][j] = x < a.axes && j < c.pairs ? (float)a.freq[(c.pair + j) * a.axes + x] : 0.f;
-  }
-  for (int64_t row0 = (int64_t)blockIdx.x * a.rows; row0 < a.n_rows; row0 += (int64_t)gridDim.x * a.rows) {
-    const int rows = (int)min((int64_t)a.rows, a.n_rows - row0);
-    const int turns = (rows * heads * (1 << a.lg) + kThreads - 1) / kThreads;
+  // the queries (KEY 0) or keys of a block of rows
+  const auto side = [&](auto key, int64_t row0, int rows) {
+    constexpr int KEY = key();
+    const int H = KEY ? a.hk : a.hq, before = KEY ? a.hq : 0, step = kThreads >> a.lg, first = (int)threadIdx.x >> a.lg;
+    const int step_row = step / H, step_head = step - step_row * H;
+    const T *src = (const T*)(KEY ? a.k : a.q), *up = (const T*)(KEY ? b.gk_up : b.gq_up);
+    const int64_t xs = KEY ? a.k_stride : a.q_stride, us = KEY ? b.gk_up_stride : b.gq_up_stride;
+    T* out = (T*)(KEY ? b.gk : b.gq);
+    const int64_t os = KEY ? b.gk_stride : b.gq_stride;
+    int row = first / H, head = first - row * H;
     RawPairs<T, INTER> x, u;
-    const auto fetch = [&](const Item& it) {
-      if (it.row >= rows) return;
-      const int64_t row = row0 + it.row;
-      if (it.head < a.hq) {
-        x.load((const T*)a.q + row * a.q_stride + it.head * a.d, c);
-        u.load((const T*)b.gq_up + row * b.gq_up_stride + it.head * a.d, c);
-      } else {
-        x.load((const T*)a.k + row * a.k_stride + (it.head - a.hq) * a.d, c);
-        u.load((const T*)b.gk_up + row * b.gk_up_stride + (it.head - a.hq) * a.d, c);
-      }
+    const auto fetch = [&](int r, int h) {
+      if (r >= rows) return;
+      x.load(src + (row0 + r) * xs + h * a.d, c);
+      u.load(up + (row0 + r) * us + h * a.d, c);
     };
-    fetch(Item(a, 0));
-    fill_angles(a, row0, rows, cs);
-    __syncthreads();
-    for (int n = 0; n < turns; ++n) {
-      const Item it(a, n);
-      const bool has = it.row < rows, key = it.head >= a.hq;
+    fetch(row, head);
+    if (KEY == 0) {
+      fill_angles(a, row0, rows, cs);
+      __syncthreads();
+    }
+    for (int n = (rows * H + step - 1) / step; n > 0; --n) {
+      const bool has = row < rows;         // the same for all threads of a head
       float v[V], h[V];
-      float s1 = 0.f, s2 = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         v[j] = has ? x.at(j) : 0.f;
         h[j] = has ? u.at(j) : 0.f;
       }
-      fetch(Item(a, n + 1));
+      const int r0 = row, h0 = head;
+      row += step_row;
+      head += step_head;
+      if (head >= H) {
+        head -= H;
+        ++row;
+      }
+      fetch(row, head);
       float2 t[V / 2];
-      cos_sin(cs + (has ? it.row : 0) * a.pairs, c, t);
+      cos_sin(cs + (has ? r0 : 0) * a.pairs, c, t);
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         const float p = h[c.first(j)], q = h[c.second(j)];
-        h[c.first(j)] = p * t[j].x + q * t[j].y;
-        h[c.second(j)] = q * t[j].x - p * t[j].y;
+        h[c.first(j)] = fmaf(p, t[j].x, q * t[j].y);
+        h[c.second(j)] = fmaf(q, t[j].x, -p * t[j].y);
       }
+      const float* g = gl + (KEY * n_chunks + lane_c) * V;
       float r = 1.f, m = 0.f;
       if (NORM) {
+        float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          s1 += v[j] * v[j];
-          s2 += h[j] * (key ? g[1][j] : g[0][j]) * v[j];
+          s1 = fmaf(v[j], v[j], s1);
+          s2 = fmaf(h[j] * g[j], v[j], s2);
         }
         r = 1.f / sqrtf(head_sum(s1, a.lg) / (float)a.d + a.eps);
         m = head_sum(s2, a.lg) * r / (float)a.d;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] *= r;
       }
-      float w[kMaxAxes] = {0.f, 0.f, 0.f};
+      if (POS) {                           // of the angles, from the pairs before they are turned
+        float w[kMaxAxes] = {0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const int p = c.first(j), q = c.second(j);
-        if (b.grad_pos) {                  // of the angle, from the pair before it is turned
-          const float yp = NORM ? v[p] * r * (key ? g[1][p] : g[0][p]) : v[p];
-          const float yq = NORM ? v[q] * r * (key ? g[1][q] : g[0][q]) : v[q];
-          const float gt = h[q] * yp - h[p] * yq;
+        for (int j = 0; j < V / 2; ++j) {
+          const int p = c.first(j), q = c.second(j);
+          const float gt = NORM ? h[q] * (v[p] * g[p]) - h[p] * (v[q] * g[q]) : h[q] * v[p] - h[p] * v[q];
 #pragma unroll
-          for (int k = 0; k < kMaxAxes; ++k) w[k] += gt * f[k][j];
+          for (int k = 0; k < kMaxAxes; ++k) w[k] += gt * fl[(k * n_chunks + lane_c) * (V / 2) + j];
         }
-      }
-      if (NORM) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float z = v[j] * r;
-          const float e = has ? h[j] * z : 0.f;
-          gg[0][j] += key ? 0.f : e;
-          gg[1][j] += key ? e : 0.f;
-          h[j] = r * (h[j] * (key ? g[1][j] : g[0][j]) - z * m);
-        }
-      }
-      if (b.grad_pos) {
 #pragma unroll
         for (int k = 0; k < kMaxAxes; ++k) {
           if (k >= a.axes) break;
           const float s = head_sum(w[k], a.lg);
-          if (has && lane_c == 0) sums[k * per_axis + it.row * heads + it.head] = s;
+          if (has && lane_c == 0) sums[k * per_axis + r0 * heads + before + h0] = s;
         }
       }
-      if (!has) continue;
-      const int64_t row = row0 + it.row;
-      store_pairs(key ? (T*)b.gk + row * b.gk_stride + (it.head - a.hq) * a.d : (T*)b.gq + row * b.gq_stride + it.head * a.d,
-                  c, h);
+      if (NORM) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          gg[KEY][j] = fmaf(h[j], v[j], gg[KEY][j]);         // both are zero where there is no head
+          h[j] = r * fmaf(-v[j], m, h[j] * g[j]);
+        }
+      }
+      if (has) store_pairs(out + (row0 + r0) * os + h0 * a.d, c, h);
     }
+  };
+  for (int64_t row0 = (int64_t)blockIdx.x * a.rows; row0 < a.n_rows; row0 += (int64_t)gridDim.x * a.rows) {
+    const int rows = (int)min((int64_t)a.rows, a.n_rows - row0);
+    side(std::integral_constant<int, 0>(), row0, rows);
+    side(std::integral_constant<int, 1>(), row0, rows);
     __syncthreads();
-    if (b.grad_pos) {
+    if (POS) {
       for (int i = threadIdx.x; i < rows * a.axes; i += kThreads) {
         const int row = i / a.axes, k = i - row * a.axes;
         float s = 0.f;
@@ -296,35 +314,36 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   if (!NORM || !b.grad_gamma_q) return;
-  // over the threads that hold the same chunk: lanes of a wave, then the waves one after the other
-  const int lane = threadIdx.x & 63, n_chunks = 1 << a.lg;
-  for (int wave = 0; wave < kThreads / 64; ++wave) {
-    if ((int)threadIdx.x >> 6 == wave) {
+  // over the threads that hold the same chunk: lanes of a wave, then the four waves
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, all = 2 * n_chunks * V;
+  float* mine = reinterpret_cast<float*>(cs);
+  static_assert(sizeof(cs) >= 4 * 2 * 2 * kHeadsMaxDim * sizeof(float));
+  __syncthreads();
+  for (int m = n_chunks; m < 64; m <<= 1) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float s = gg[i][j];
-          for (int m = n_chunks; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
-          float* to = sums + (i * n_chunks + lane_c) * V + j;
-          if (lane < n_chunks) *to = (wave ? *to : 0.f) + s;
-        }
+    for (int j = 0; j < V; ++j) {
+      gg[0][j] += __shfl_xor(gg[0][j], m, 64);
+      gg[1][j] += __shfl_xor(gg[1][j], m, 64);
     }
-    __syncthreads();
   }
+  if (lane < n_chunks) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < V; ++j) mine[wave * all + (i * n_chunks + lane_c) * V + j] = gg[i][j];
+  }
+  __syncthreads();
   float* out[2] = {b.grad_gamma_q, b.grad_gamma_k};
   if (gridDim.x > 1) {
     out[0] = b.part + (size_t)blockIdx.x * 2 * a.d;
     out[1] = out[0] + a.d;
   }
-  if ((int)threadIdx.x < n_chunks) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      store_chunk(out[i] + c.at[0], min(4, c.left[0]), sums + (i * n_chunks + lane_c) * V);
-      if (V > 8) store_chunk(out[i] + c.at[0] + 4, min(4, c.left[0] - 4), sums + (i * n_chunks + lane_c) * V + 4);
-      store_chunk(out[i] + c.at[1], min(4, c.left[1]), sums + (i * n_chunks + lane_c) * V + V / 2);
-      if (V > 8) store_chunk(out[i] + c.at[1] + 4, min(4, c.left[1] - 4), sums + (i * n_chunks + lane_c) * V + V / 2 + 4);
-    }
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    const int side_of = i / (n_chunks * V), j = i % V;
+    const Chunks<T, INTER> o(i / V % n_chunks, a.d, a.pairs);
+    const int run = j / Chunk<T>::kN, in = j % Chunk<T>::kN;
+    if (in < (run ? o.left[1] : o.left[0]))
+      out[side_of][(run ? o.at[1] : o.at[0]) + in] = (mine[i] + mine[all + i]) + (mine[2 * all + i] + mine[3 * all + i]);
   }
 }
 
@@ -341,21 +360,25 @@ __global__ void __launch_bounds__(kThreads)
   if (lane == 0) (col < d ? gq[col] : gk[col - d]) = s;
 }
 
-constexpr int kBwdBlocks = 1024;           // workgroups that walk the rows of the backward
+// workgroups that walk the rows of the backward: as many as the chip holds at once
+constexpr int kBwdBlocks = 768, kBwdBlocksF32 = 1024;
+
+// workgroups that few rows are spread over
+constexpr int kFwdFill = 1024, kBwdFill = 256;
 
 // Threads per head (their binary logarithm) and rows per workgroup: enough items for a few
 // turns of the workgroup, fewer where the rows would not fill the chip.
-void shape_of(int dtype, HeadArgs& a) {
+void shape_of(int dtype, HeadArgs& a, int64_t blocks) {
   const int n = dtype == TP_F32 ? Chunk<float>::kN : Chunk<bf16_t>::kN;
   const int chunks = (a.pairs + n - 1) / n + (a.d - 2 * a.pairs + 2 * n - 1) / (2 * n);
   a.lg = 0;
   while ((1 << a.lg) < chunks) ++a.lg;
   const int64_t most = std::max(1, std::min(kTrig / std::max(1, a.pairs), (4 * kThreads) / ((a.hq + a.hk) << a.lg)));
-  a.rows = (int)std::max<int64_t>(1, std::min<int64_t>({most, 64, (a.n_rows + 1023) / 1024}));
+  a.rows = (int)std::max<int64_t>(1, std::min<int64_t>({most, 64, (a.n_rows + blocks - 1) / blocks}));
 }
 
-int64_t bwd_blocks(const HeadArgs& a) {
-  return std::max<int64_t>(1, std::min<int64_t>(kBwdBlocks, (a.n_rows + a.rows - 1) / a.rows));
+int64_t bwd_blocks(int dtype, const HeadArgs& a) {
+  return std::max<int64_t>(1, std::min<int64_t>(dtype == TP_F32 ? kBwdBlocksF32 : kBwdBlocks, (a.n_rows + a.rows - 1) / a.rows));
 }
 
 template <typename F>
@@ -368,13 +391,13 @@ hipError_t pick(int dtype, bool interleaved, bool norm, F&& f) {
 }  // namespace
 
 size_t heads_workspace_bytes(int dtype, HeadArgs a) {
-  shape_of(dtype, a);
-  const int64_t n = bwd_blocks(a);
+  shape_of(dtype, a, kBwdFill);
+  const int64_t n = bwd_blocks(dtype, a);
   return n == 1 ? 0 : (size_t)n * 2 * a.d * sizeof(float);
 }
 
 hipError_t heads_forward(int dtype, HeadArgs a) {
-  shape_of(dtype, a);
+  shape_of(dtype, a, kFwdFill);
   const int64_t blocks = (a.n_rows + a.rows - 1) / a.rows;
   if (blocks > 0xffffffffLL / kThreads) return hipErrorInvalidConfiguration;
   return pick(dtype, a.interleaved, a.gamma_q != nullptr, [&](auto t, auto inter, auto norm) {
@@ -385,12 +408,16 @@ hipError_t heads_forward(int dtype, HeadArgs a) {
 
 hipError_t heads_backward(int dtype, HeadBwdArgs b) {
   HeadArgs& a = b.f;
-  shape_of(dtype, a);
-  const int n = (int)bwd_blocks(a);
+  shape_of(dtype, a, kBwdFill);
+  const int n = (int)bwd_blocks(dtype, a);
   hipError_t e = pick(dtype, a.interleaved, a.gamma_q != nullptr, [&](auto t, auto inter, auto norm) {
     constexpr int V = 2 * Chunk<decltype(t)>::kN;
-    const size_t floats = std::max(kMaxAxes * a.rows * (a.hq + a.hk), 2 * (V << a.lg));
-    hipLaunchKernelGGL((k_heads_bwd<decltype(t), inter(), norm()>), dim3(n), dim3(kThreads), floats * sizeof(float), a.stream, b);
+    const size_t chunks = (size_t)V << a.lg;
+    const size_t floats = (norm() ? 2 * chunks : 0) + (b.grad_pos ? kMaxAxes * (chunks / 2 + (size_t)a.rows * (a.hq + a.hk)) : 0);
+    if (b.grad_pos)
+      hipLaunchKernelGGL((k_heads_bwd<decltype(t), inter(), norm(), true>), dim3(n), dim3(kThreads), floats * sizeof(float), a.stream, b);
+    else
+      hipLaunchKernelGGL((k_heads_bwd<decltype(t), inter(), norm(), false>), dim3(n), dim3(kThreads), floats * sizeof(float), a.stream, b);
     return hipGetLastError();
   });
   if (e != hipSuccess || n == 1 || !b.grad_gamma_q) return e;
