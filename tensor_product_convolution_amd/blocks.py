@@ -5,6 +5,7 @@ Argument marshalling only, like the rest of the binding: conventions, formulas
 and errors are those of ``include/tpconv.h``.  Tensors are float32 or bfloat16;
 strided rows are taken as they are where the C entry point takes a stride.
 """
+import array
 import ctypes
 import math
 from typing import NamedTuple
@@ -12,8 +13,10 @@ from typing import NamedTuple
 import torch
 
 from . import lib
-from .layers import _INT32_MAX, _call, _check, _code, _need, _refuse, _rows, _too_large
+from .layers import _INT32_MAX, _call, _check, _code, _need, _rows, _too_large
 
+_is_tensor = lambda t: isinstance(t, torch.Tensor)
+_is_contiguous, _device_of, _address_of = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr
 _ROWS = {"source": 0, "grouped": 1}
 _ACTS = {None: 0, "silu": 1}
 _POS = {torch.float32: 0, torch.int32: 1}
@@ -361,19 +364,25 @@ class AdamW:
             self.exp_avg_unit, self.exp_avg_sq_unit = new(total // 256, torch.float32), new(total // 256, torch.float32)
         self._scalars = new(64, torch.uint8)
         self._ws = new(max(16, ws.value), torch.uint8)
-        self._ws_bytes, self._pointers = ws.value, pointers
+        self._ws_bytes = ws.value
+        # the arrays that the description points to live as long as it does; the rates are set by each step
+        self._desc = _AdamW(bits, 0, n, ctypes.addressof(self._sizes), self._table.data_ptr(), self.exp_avg.data_ptr(),
+                            self.exp_avg_sq.data_ptr(), _at(self.exp_avg_unit), _at(self.exp_avg_sq_unit), 0.0, 0.0, 0.0, 0.0, 0.0,
+                            None, 0, self._scalars.data_ptr())
 
     def step(self, grads, lr=None):
         """One step with ``grads``, contiguous tensors of the parameters' shapes, all float32 or all
         bfloat16.  Returns their norm (a float32 tensor of one value), or None without max_norm."""
         if len(grads) != self._n:
             raise ValueError(f"{len(grads)} gradients for {self._n} parameters")
-        dt, dev, where = getattr(grads[0], "dtype", None), self._dev, []
         code, _ = _code(grads[0], "grads[0]")
-        for g, shape in zip(grads, self._shapes):
-            if not (isinstance(g, torch.Tensor) and g.dtype is dt and g.shape == shape and g.is_contiguous() and g.get_device() == dev):
-                _refuse(g, f"grads[{len(where)}]", dt, shape, dev)
-            where.append(g.data_ptr())
+        dt, dev, n = grads[0].dtype, self._dev, self._n
+        # one pass over all tensors for each property: the host's time is most of a small step's
+        if not (all(map(_is_tensor, grads)) and [g.dtype for g in grads].count(dt) == n and [g.shape for g in grads] == self._shapes
+                and all(map(_is_contiguous, grads)) and list(map(_device_of, grads)).count(dev) == n):
+            for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+                _need(g, f"grads[{i}]", dt, shape, dev)
+        where = array.array("Q", map(_address_of, grads))
         lr = self.lr if lr is None else lr
         lr_at = None
         if isinstance(lr, torch.Tensor):
@@ -383,10 +392,11 @@ class AdamW:
             if not self.max_norm > 0:
                 raise ValueError("max_norm must be positive")
             norm = self._table.new_empty((), dtype=torch.float32)
-        a = _AdamW(self.bits, code, self._n, ctypes.addressof(self._sizes), self._table.data_ptr(), self.exp_avg.data_ptr(),
-                   self.exp_avg_sq.data_ptr(), _at(self.exp_avg_unit), _at(self.exp_avg_sq_unit), self.betas[0], self.betas[1],
-                   self.eps, lr, 0.0 if norm is None else self.max_norm, lr_at, self.seed, self._scalars.data_ptr())
-        _call(dev, lib().tp_adamw_step, ctypes.byref(a), self._pointers(*where), _at(norm), self._ws.data_ptr(), self._ws_bytes)
+        a = self._desc
+        a.grad_dtype, a.lr, a.lr_at, a.max_norm = code, lr, lr_at, 0.0 if norm is None else self.max_norm
+        a.beta1, a.beta2 = self.betas
+        a.eps, a.seed = self.eps, self.seed
+        _call(dev, lib().tp_adamw_step, ctypes.byref(a), where.buffer_info()[0], _at(norm), self._ws.data_ptr(), self._ws_bytes)
         return norm
 
     def moments(self):
