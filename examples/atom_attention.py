@@ -10,9 +10,12 @@ a structure, through the scalar (0e) channels of the node rows:
     energy of a structure per atom = mean over its atoms of z . readout
 
 trained on random targets with plain gradient descent; the gradient reaches every
-weight of the block and, through the convolution's backward, x and w.  Run on a GPU:
+weight of the block and, through the convolution's backward, x and w.  With ``full`` the
+block is a whole transformer's: queries and keys are normed and turned by position in front
+of the attention, a linear layer by chemical element and a feed-forward by experts stand
+behind it, and AdamW trains it all.  Run on a GPU:
 
-    python examples/atom_attention.py [steps]
+    python examples/atom_attention.py [steps] [full]
 """
 import os
 import sys
@@ -70,6 +73,67 @@ class Layer:
         return grad_f + grad_1, g
 
 
+class FullLayer(Layer):
+    """The block with norm and rotation of queries and keys, and behind it
+
+        e = z + z We[element]
+        out = e + sum over the chosen experts of weight_j silu(e W1_j + b1_j) W2_j
+    """
+
+    def __init__(self, channels, p_drop, gen, kinds=4, experts=4, chosen=2, hidden=64):
+        super().__init__(channels, p_drop, gen)
+        u, rand = channels, lambda *s: torch.randn(*s, device="cuda", generator=gen)
+        self.chosen, self.kinds = chosen, kinds
+        # wave vectors of up to 1 per Angstrom
+        self.freq = rand(DIM // 2, 3).double() * 0.4
+        self.w.update(gamma_q=torch.ones(DIM, device="cuda"), gamma_k=torch.ones(DIM, device="cuda"),
+                      element=rand(kinds, u, u) / u ** 0.5, router=rand(u, experts) / u ** 0.5,
+                      up=rand(experts, u, hidden) / u ** 0.5, up_bias=0.1 * rand(experts, hidden),
+                      down=rand(experts, hidden, u) / hidden ** 0.5)
+
+    def forward(self, f, seg, pos, step, kind):
+        w, n = self.w, len(f)
+        y, mean1, rstd1 = tpc.layer_norm_forward(f, w["gamma1"], w["beta1"])
+        q, k, v = self._split(y @ w["qkv"])
+        turn = dict(gamma_q=w["gamma_q"], gamma_k=w["gamma_k"], pos=pos, freq=self.freq)
+        qr, kr = tpc.head_norm_rotate_forward(q, k, **turn)
+        o, lse = tpc.attn_forward(qr, kr, v, seg, pos=pos, bias=w["bias"])
+        drop = tpc.Dropout(self.p_drop, seed=17, offset=step)
+        z, mean2, rstd2, h = tpc.layer_norm_residual_forward(o.view(n, -1) @ w["out"], f.contiguous(), w["gamma2"], w["beta2"], drop)
+        elements = tpc.group_rows(kind, self.kinds)
+        e = z + tpc.grouped_linear_forward(z, w["element"], elements)
+        logits = e @ w["router"]
+        weight, index = tpc.route_forward(logits, self.chosen)
+        experts = tpc.group_rows(index, logits.shape[1])
+        a, pre = tpc.grouped_linear_forward(e, w["up"], experts, bias=w["up_bias"], act="silu", y_rows="grouped", want_pre=True)
+        b = tpc.grouped_linear_forward(a, w["down"], experts, x_rows="grouped")
+        out = e + tpc.combine_forward(b, weight)
+        return out, (f, y, mean1, rstd1, q, k, v, turn, qr, kr, o, lse, drop, h, mean2, rstd2, seg, pos, z, elements, e, logits, weight,
+                     index, experts, a, pre, b)
+
+    def backward(self, grad_out, saved):
+        (f, y, mean1, rstd1, q, k, v, turn, qr, kr, o, lse, drop, h, mean2, rstd2, seg, pos, z, elements, e, logits, weight, index,
+         experts, a, pre, b) = saved
+        w, g, n = self.w, {}, len(f)
+        grad_b, grad_weight = tpc.combine_backward(grad_out, b, weight)
+        grad_pre, g["down"], _ = tpc.grouped_linear_backward(grad_b, a, w["down"], experts, x_rows="grouped", pre=pre)
+        grad_e, g["up"], g["up_bias"] = tpc.grouped_linear_backward(grad_pre, e, w["up"], experts, y_rows="grouped", want_bias=True)
+        grad_logits = tpc.route_backward(grad_weight, logits, weight, index)
+        g["router"] = e.t() @ grad_logits
+        grad_e = grad_out + grad_e + grad_logits @ w["router"].t()
+        grad_z, g["element"], _ = tpc.grouped_linear_backward(grad_e, z, w["element"], elements)
+        grad_a, grad_f, g["gamma2"], g["beta2"] = tpc.layer_norm_residual_backward(grad_e + grad_z, h, w["gamma2"], mean2, rstd2, drop)
+        g["out"] = o.view(n, -1).t() @ grad_a
+        grad_qkv = torch.empty(n, w["qkv"].shape[1], device="cuda")
+        gq, gk, gv = self._split(grad_qkv)
+        grad_qr, grad_kr, _, g["bias"] = tpc.attn_backward(qr, kr, v, seg, o, lse, (grad_a @ w["out"].t()).view(n, HEADS, DIM), pos=pos,
+                                                           bias=w["bias"], outs=(torch.empty_like(qr), torch.empty_like(kr), gv))
+        *_, g["gamma_q"], g["gamma_k"], _ = tpc.head_norm_rotate_backward(grad_qr, grad_kr, q, k, outs=(gq, gk), **turn)
+        g["qkv"] = y.t() @ grad_qkv
+        grad_1, g["gamma1"], g["beta1"] = tpc.layer_norm_backward(grad_qkv @ w["qkv"].t(), f, w["gamma1"], mean1, rstd1)
+        return grad_f + grad_1, g
+
+
 def batch(sizes, neighbours, seed):
     """Random structures: positions at 0.05 atoms per cubic Angstrom, each atom's nearest
     neighbours as edges, and one target energy per atom for each structure."""
@@ -88,8 +152,8 @@ def batch(sizes, neighbours, seed):
             cuda(r.normal(size=len(sizes)), torch.float32))
 
 
-def train(steps=20, sizes=(40, 1, 97, 64), p_drop=0.1, rate=0.02, seed=0, report=print):
-    """Losses of `steps` steps."""
+def train(steps=20, sizes=(40, 1, 97, 64), p_drop=0.1, rate=0.02, seed=0, report=print, full=False):
+    """Losses of `steps` steps; with `full` the FullLayer, trained by AdamW."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
     pos, src, dst, seg, target = batch(sizes, 12, seed)
     n, struct = pos.shape[0], torch.repeat_interleave(torch.arange(len(sizes), device="cuda"), torch.tensor(sizes, device="cuda"))
@@ -99,12 +163,19 @@ def train(steps=20, sizes=(40, 1, 97, 64), p_drop=0.1, rate=0.02, seed=0, report
     Y = tpc.sph_harm(LMAX, r)
     x = torch.randn(n, plan.xdim, device="cuda", generator=gen)
     w = torch.randn(graph.n_edges, plan.n_paths, plan.mul, device="cuda", generator=gen) / (12 * plan.n_paths) ** 0.5
-    layer = Layer(plan.mul, p_drop, gen)
+    layer = (FullLayer if full else Layer)(plan.mul, p_drop, gen)
+    more, optimiser, names = (), None, None
+    if full:
+        more = (torch.randint(0, layer.kinds, (n,), device="cuda", generator=gen, dtype=torch.int32),)
+        names = sorted(layer.w)
+        # matrices decay, norms and biases do not
+        optimiser = tpc.AdamW([w, *[layer.w[m] for m in names]], lr=rate / 4, max_norm=1.0,
+                              weight_decay=[0.01, *[0.01 if layer.w[m].dim() > 1 else 0.0 for m in names]])
     share = 1 / torch.tensor(sizes, dtype=torch.float32, device="cuda")[struct]
     losses = []
     for step in range(steps):
         rows = tpc.forward(plan, graph, x, Y, w)
-        z, saved = layer.forward(rows[:, :plan.mul], seg, pos, step)
+        z, saved = layer.forward(rows[:, :plan.mul], seg, pos, step, *more)
         energy = torch.zeros(len(sizes), device="cuda").index_add_(0, struct, share * (z @ layer.w["readout"]))
         error = energy - target
         losses.append(float((error * error).mean()))
@@ -115,6 +186,9 @@ def train(steps=20, sizes=(40, 1, 97, 64), p_drop=0.1, rate=0.02, seed=0, report
         grad_rows = torch.zeros_like(rows)
         grad_rows[:, :plan.mul] = grad_scalars
         _, _, grad_w = tpc.backward(plan, graph, x, Y, w, grad_rows, want=("w",))
+        if full:
+            optimiser.step([grad_w, *[grads[m] for m in names]])
+            continue
         for name, g in grads.items():
             layer.w[name] -= rate * g
         w -= rate * grad_w
@@ -124,4 +198,4 @@ def train(steps=20, sizes=(40, 1, 97, 64), p_drop=0.1, rate=0.02, seed=0, report
 if __name__ == "__main__":
     if not torch.cuda.is_available():
         raise SystemExit("needs a GPU")
-    train(int(sys.argv[1]) if len(sys.argv) > 1 else 20)
+    train(int(sys.argv[1]) if len(sys.argv) > 1 else 20, full="full" in sys.argv[2:])
