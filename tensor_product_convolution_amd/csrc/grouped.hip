@@ -16,7 +16,7 @@ namespace {
 // contraction and columns are multiples of 8.
 template <typename T, int BM, int BN, int WM, int WN, int S, bool ALONG, bool EVEN>
 __global__ void __launch_bounds__(kGemmThreads)
-    k_grouped(GroupedArgs a, int n_rows, int n_cols) {
+    k_grouped(GroupedArgs a, int n_cols) {
   constexpr int P = kPlanes<T>, MB = WM / 32, NB = WN / 32;
   static_assert((BM / WM) * (BN / WN) * 64 == kGemmThreads);
   typedef AlongTile<T, BM, S> TA;
@@ -27,11 +27,13 @@ __global__ void __launch_bounds__(kGemmThreads)
   __shared__ int crow[BM];
   uint16_t *la = lds, *lb = lds + TA::kElems;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int rt, ct;
-  place_tile(blockIdx.x, n_rows, n_cols, rt, ct);
-  Part part;
   const int n = (int)a.n;
-  if (!find_part(a.ptr, a.n_groups + 1, n, BM, rt, part) || part.first >= part.hi) return;
+  const Parts parts(a.ptr, a.n_groups, a.n_groups + 1, n, BM, 0);
+  if ((int)blockIdx.x >= parts.total * n_cols) return;
+  int rt, ct;
+  place_tile(place_of(blockIdx.x, parts.total * n_cols), parts.total, n_cols, rt, ct);
+  const Part part = parts.at(rt);
+  if (part.first >= part.hi) return;       // not with a valid ptr
   const int rows = min(BM, part.hi - part.first), col0 = ct * BN;
   if (tid < BM) crow[tid] = tid < rows ? row_of(a.rows, part.first + tid, a.c_div, n) : -1;
   const bool none = part.group == a.n_groups;        // slots without a group
@@ -142,18 +144,20 @@ __global__ void __launch_bounds__(kGemmThreads)
 // Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32, D buffers.
 template <typename T, int WM, int WN, int MB, int NB, int D, bool ALONG>
 __global__ void __launch_bounds__(64 * WM * WN, 2)
-    k_grouped_fast(GroupedArgs a, int n_rows, int n_cols) {
+    k_grouped_fast(GroupedArgs a, int n_cols) {
   constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
   typedef AlongLds<T, BM, W> TA;
   typedef typename std::conditional<ALONG, AlongLds<T, BN, W>, AcrossLds<T, BN, W>>::type TB;
   TPC_BUFFERS(D, TA, TB);
   __shared__ int arow[BM], crow[BM];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int rt, ct;
-  place_tile(blockIdx.x, n_rows, n_cols, rt, ct);
-  Part part;
   const int n = (int)a.n;
-  if (!find_part(a.ptr, a.n_groups + 1, n, BM, rt, part) || part.first >= part.hi) return;
+  const Parts parts(a.ptr, a.n_groups, a.n_groups + 1, n, BM, 0);
+  if ((int)blockIdx.x >= parts.total * n_cols) return;
+  int rt, ct;
+  place_tile(place_of(blockIdx.x, parts.total * n_cols), parts.total, n_cols, rt, ct);
+  const Part part = parts.at(rt);
+  if (part.first >= part.hi) return;       // not with a valid ptr
   const int rows = min(BM, part.hi - part.first), col0 = ct * BN;
   for (int i = tid; i < BM; i += 64 * W) {
     // rows past the part's end repeat its last one; nothing of them is stored
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     crow[i] = i < rows ? (a.c_div ? slot : place) : -1;
   }
   const bool none = part.group == a.n_groups;        // slots without a group
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave / WN, wn = wave % WN;
   Sums<T, MB, NB> sums;
   sums.clear();
   if (!none) {
@@ -249,28 +253,28 @@ template <typename F>
 hipError_t tiles(const GroupedArgs& a, int bm, int bn, F&& f) {
   const int64_t rows = a.n / bm + a.n_groups + 1, cols = (a.cols + bn - 1) / bn;
   if (rows * cols > 0xffffffffLL / 512) return hipErrorInvalidConfiguration;
-  f(dim3((unsigned)(rows * cols)), (int)rows, (int)cols);
+  f(dim3((unsigned)(rows * cols)), (int)cols);
   return hipGetLastError();
 }
 
 template <typename T, int WM, int WN, int MB, int NB, int D>
 hipError_t fast(const GroupedArgs& a) {
-  return tiles(a, 32 * WM * MB, 32 * WN * NB, [&](dim3 grid, int rows, int cols) {
+  return tiles(a, 32 * WM * MB, 32 * WN * NB, [&](dim3 grid, int cols) {
     if (a.transposed)
-      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, true>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, true>), grid, dim3(64 * WM * WN), 0, a.stream, a, cols);
     else
-      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, false>), grid, dim3(64 * WM * WN), 0, a.stream, a, rows, cols);
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, false>), grid, dim3(64 * WM * WN), 0, a.stream, a, cols);
   });
 }
 
 template <typename T>
 hipError_t any(const GroupedArgs& a) {
   constexpr int S = sizeof(T) == 4 ? 32 : 64;
-  return tiles(a, 64, 64, [&](dim3 grid, int rows, int cols) {
+  return tiles(a, 64, 64, [&](dim3 grid, int cols) {
     if (a.transposed)
-      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, true, false>), grid, dim3(kGemmThreads), 0, a.stream, a, rows, cols);
+      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, true, false>), grid, dim3(kGemmThreads), 0, a.stream, a, cols);
     else
-      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, false, false>), grid, dim3(kGemmThreads), 0, a.stream, a, rows, cols);
+      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, false, false>), grid, dim3(kGemmThreads), 0, a.stream, a, cols);
   });
 }
 

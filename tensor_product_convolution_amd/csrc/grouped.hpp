@@ -114,31 +114,74 @@ struct AcrossTile {
   }
 };
 
-// Part t of the groups cut into parts of `size` slots: group e's parts start at number
-// ptr[e] / size + e, which never overlap and leave at most one unused number per group, so
-// n / size + groups numbers cover any groups without the host knowing them.  Numbers grow
-// with the group, so the part's group is the count of those that start by then.  `groups` counts the one behind the last pointer (slots without a group),
-// which ends at n.  False: an unused number, but for the first of an empty group.
+// The groups cut into parts of `size` slots, numbered without gaps.  A wave counts the parts of 64 runs
+// of groups at once; the host knows n / size + groups as a bound of their number.  `groups` counts the one
+// behind the last pointer where slots without a group are parts too; `least` is 1 where an empty group
+// counts as one part.
 struct Part {
   int group, lo, hi, first;                // slots of the group, first slot of the part
 };
-__device__ __forceinline__ bool find_part(const int32_t* ptr, int groups, int n, int size, int t, Part& p) {
-  const int lane = threadIdx.x & 63;
-  const auto start = [&](int e) { return min(max(ptr[e], 0), n); };
-  int count = 0;                           // groups that start at or before part t
-#pragma unroll 4
-  for (int e = 0; e < groups; e += 64) {
-    const bool le = e + lane < groups && start(e + lane) / size + e + lane <= t;
-    count += __popcll(__ballot(le));
+struct Parts {
+  const int32_t* ptr;
+  int groups, n_groups, n, size, least, run, total;
+  int first_slot, end_slot, before;        // of this lane's run; parts of the lanes below
+  __device__ __forceinline__ int start(int e) const { return e <= n_groups ? min(max(ptr[e], 0), n) : n; }
+  __device__ __forceinline__ int count(int lo, int hi) const { return max(least, (max(hi - lo, 0) + size - 1) / size); }
+  // x plus that of the lanes `shift` below it in the same row of 16, or of the rows before
+  template <int CONTROL, int ROWS>
+  static __device__ __forceinline__ int add(int x) {
+    return x + __builtin_amdgcn_update_dpp(0, x, CONTROL, ROWS, 0xf, false);
   }
-  if (count == 0) return false;            // not a valid ptr
-  p.group = __builtin_amdgcn_readfirstlane(count - 1);
-  p.lo = start(p.group);
-  p.hi = p.group + 1 < groups ? start(p.group + 1) : n;
-  const int64_t first = (int64_t)p.lo + (int64_t)(t - (p.lo / size + p.group)) * size;
-  p.first = (int)min(first, (int64_t)n);
-  return first == p.lo || (first > p.lo && first < p.hi);
-}
+  __device__ __forceinline__ Parts(const int32_t* p, int real, int all, int slots, int each, int at_least)
+      : ptr(p), groups(all), n_groups(real), n(slots), size(each), least(at_least) {
+    const int lane = threadIdx.x & 63;
+    run = (groups + 63) >> 6;
+    int c = 0;
+    first_slot = end_slot = start(lane * run);
+    if (run == 1) {
+      end_slot = start(lane + 1);
+      c = lane < groups ? count(first_slot, end_slot) : 0;
+    } else {
+      for (int i = lane * run; i < min(groups, lane * run + run); ++i) {
+        const int hi = start(i + 1);
+        c += count(end_slot, hi);
+        end_slot = hi;
+      }
+    }
+    int sum = add<0x111, 0xf>(c);          // the running sum over the lanes: 1, 2, 4, 8 lanes back,
+    sum = add<0x112, 0xf>(sum);
+    sum = add<0x114, 0xf>(sum);
+    sum = add<0x118, 0xf>(sum);
+    sum = add<0x142, 0xa>(sum);            // then the ends of the rows of 16 before
+    sum = add<0x143, 0xc>(sum);
+    before = sum - c;
+    // a wrong ptr may count to anything: no more than the launch has, and no group that is not there
+    total = min(max(__builtin_amdgcn_readlane(sum, 63), 0), n / size + groups);
+  }
+  // part t < total
+  __device__ __forceinline__ Part at(int t) const {
+    const int owner = max(__popcll(__ballot(before <= t)) - 1, 0);
+    const int last = __builtin_amdgcn_readfirstlane(min(owner, (groups - 1) / run));
+    int left = t - __builtin_amdgcn_readlane(before, last);
+    Part p;
+    p.group = last * run;
+    p.lo = __builtin_amdgcn_readlane(first_slot, last);
+    p.hi = __builtin_amdgcn_readlane(end_slot, last);
+    if (run > 1) {
+      p.hi = start(p.group + 1);
+      for (;;) {
+        const int c = count(p.lo, p.hi);
+        if (left < c || p.group + 1 >= groups) break;
+        left -= c;
+        ++p.group;
+        p.lo = p.hi;
+        p.hi = start(p.group + 1);
+      }
+    }
+    p.first = (int)min((int64_t)p.lo + (int64_t)left * size, (int64_t)n);
+    return p;
+  }
+};
 
 // a slot by its place in group order; what is out of range is clamped
 __device__ __forceinline__ int slot_at(const int32_t* rows, int place, int n) {
@@ -151,13 +194,16 @@ __device__ __forceinline__ int row_of(const int32_t* rows, int slot, int div, in
   return (int)(div == 1 ? r : r / (uint32_t)div);
 }
 
-// Places of the tiles rows x cols in the order of the launch.  Workgroups go round the 8 dies in
-// turn; each die gets a run of consecutive tiles, 8 row tiles by all columns at a time, so that
-// what it reads of both operands stays in its L2.
-__device__ __forceinline__ void place_tile(int id, int rows, int cols, int& r, int& c) {
-  constexpr int kDies = 8, kBand = 8;
-  const int total = rows * cols, whole = total / kDies, more = total % kDies, die = id % kDies;
-  const int t = die * whole + min(die, more) + id / kDies;
+// Workgroups go round the 8 dies in turn; each die gets a run of consecutive ones of `total` tiles.
+__device__ __forceinline__ int place_of(int id, int total) {
+  constexpr int kDies = 8;
+  const int whole = total / kDies, more = total % kDies, die = id % kDies;
+  return die * whole + min(die, more) + id / kDies;
+}
+// Tile t of rows x cols: 8 row tiles by all columns at a time, so that what a die reads of both operands
+// stays in its L2.
+__device__ __forceinline__ void place_tile(int t, int rows, int cols, int& r, int& c) {
+  constexpr int kBand = 8;
   const int band = t / (kBand * cols), first = band * kBand, high = min(kBand, rows - first), in = t - first * cols;
   r = first + in % high;
   c = in / high;
@@ -320,35 +366,66 @@ struct Sums {
 template <typename T, typename TA, typename TB, int MB, int NB, bool FAR, bool BIAS = false>
 __device__ __forceinline__ void multiply(const uint8_t* ta, const uint8_t* tb, int wm, int wn, int lane, Sums<T, MB, NB>& s,
                                          float* colsum = nullptr, bool bias = false) {
+  constexpr int K = kDeep<T> / 16;
+  if constexpr (sizeof(T) == 2) {
+    // fragments are read one block row ahead of their products, which the compiler keeps in this order
+    Octet<T> a, next, b[NB], after[NB];
 #pragma unroll
-  for (int kk = 0; kk < kDeep<T> / 16; ++kk) {
-    Frag<kPlanes<T>> fb[NB];
+    for (int j = 0; j < NB; ++j) TB::read(tb, wn * NB + j, 0, lane, b[j]);
+    TA::read(ta, wm * MB, 0, lane, a);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      Octet<T> o;
-      TB::read(tb, wn * NB + j, kk, lane, o);
-      if (BIAS && bias) {
+    for (int kk = 0; kk < K; ++kk) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) colsum[j] += o.at(e);
+      for (int i = 0; i < MB; ++i) {
+        if (i + 1 < MB) {
+          TA::read(ta, wm * MB + i + 1, kk, lane, next);
+        } else if (kk + 1 < K) {
+          TA::read(ta, wm * MB, kk + 1, lane, next);
+        }
+        if (i == 0 && kk + 1 < K) {
+#pragma unroll
+          for (int j = 0; j < NB; ++j) TB::read(tb, wn * NB + j, kk + 1, lane, after[j]);
+        }
+        if (BIAS && bias && i == 0) {
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) colsum[j] += b[j].at(e);
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) s.part[i][j] = mma(operand<FAR>(b[j]), operand<FAR>(a), s.part[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        a = next;
       }
-      fb[j] = operand<FAR>(o);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) b[j] = after[j];
     }
+  } else {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      Octet<T> o;
-      TA::read(ta, wm * MB + i, kk, lane, o);
-      const Frag<kPlanes<T>> fa = operand<FAR>(o);
+    for (int kk = 0; kk < K; ++kk) {
+      Frag<kPlanes<T>> fb[NB];
 #pragma unroll
-      for (int j = 0; j < NB; ++j) s.part[i][j] = mma(fb[j], fa, s.part[i][j]);
-      // block rows in turn: 3 % over the compiler's order (8,192 x 8,192 x 8,192: 968 against 942 TFLOP/s)
-      if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < NB; ++j) {
+        Octet<T> o;
+        TB::read(tb, wn * NB + j, kk, lane, o);
+        if (BIAS && bias) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) colsum[j] += o.at(e);
+        }
+        fb[j] = operand<FAR>(o);
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        Octet<T> o;
+        TA::read(ta, wm * MB + i, kk, lane, o);
+        const Frag<kPlanes<T>> fa = operand<FAR>(o);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) s.part[i][j] = mma(fb[j], fa, s.part[i][j]);
+      }
     }
   }
 }
 
-// The loop over the steps: load(step, buffer) fetches, product(buffer, step) multiplies.  The buffers are
-// separate arrays and take turns by name, so that the compiler sees that what is fetched is not what
-// is read, and waits for nothing in between.
 // All waves meet: what this one fetched, but for the last LATE loads, is in LDS, what it read has been
 // read.  The fences are the wave's, for the compiler alone.
 template <int LATE>

@@ -29,10 +29,12 @@ __global__ void __launch_bounds__(kGemmThreads)
   __shared__ float colsum[B];
   uint16_t *la = lds, *lb = lds + Tile::kElems;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tiles = n_rows * n_cols, tile = blockIdx.x % tiles;
-  Part part;
-  const int n = (int)a.n;
-  if (!find_part(a.ptr, a.n_groups + 1, n, size, blockIdx.x / tiles, part) || part.group == a.n_groups) return;
+  const int tiles = n_rows * n_cols, n = (int)a.n;
+  const Parts parts(a.ptr, a.n_groups, a.n_groups, n, size, 1);
+  if ((int)blockIdx.x >= parts.total * tiles) return;
+  // tiles of a part on all dies: parts differ in length
+  const int tile = blockIdx.x % tiles;
+  const Part part = parts.at(blockIdx.x / tiles);
   const int k0 = tile / n_cols * B, c0 = tile % n_cols * B;
   const int end = min(part.hi, part.first + size);
   const bool bias = a.grad_bias && k0 == 0;
@@ -154,12 +156,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   typedef AcrossLds<T, BN, W> TB;
   TPC_BUFFERS(D, TA, TB);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int tiles = n_rows * n_cols, tile = blockIdx.x % tiles;
-  Part part;
-  const int n = (int)a.n;
-  if (!find_part(a.ptr, a.n_groups + 1, n, size, blockIdx.x / tiles, part) || part.group == a.n_groups) return;
+  const int tiles = n_rows * n_cols, n = (int)a.n;
+  const Parts parts(a.ptr, a.n_groups, a.n_groups, n, size, 1);
+  if ((int)blockIdx.x >= parts.total * tiles) return;
+  // tiles of a part on all dies: parts differ in length
+  const int tile = blockIdx.x % tiles;
+  const Part part = parts.at(blockIdx.x / tiles);
   const int k0 = tile / n_cols * BM, c0 = tile % n_cols * BN, end = min(part.hi, part.first + size);
-  const int wm = wave % WM, wn = wave / WM;
+  const int wm = wave / WN, wn = wave % WN;
   const bool bias = a.grad_bias && k0 == 0 && wm == 0;
   const T* zeros = reinterpret_cast<const T*>(kZeros);
   int next = 0;                            // the slot that this lane knows of the next step
