@@ -12,9 +12,8 @@ namespace tpc {
 namespace {
 
 // Rows of any length and alignment: staged through registers.  BM x BN tile of four waves, WM x WN
-// each, S contraction values a step.  ALONG: w rows run along the contraction (transposed).  EVEN:
-// contraction and columns are multiples of 8.
-template <typename T, int BM, int BN, int WM, int WN, int S, bool ALONG, bool EVEN>
+// each, S contraction values a step.  ALONG: w rows run along the contraction (transposed).
+template <typename T, int BM, int BN, int WM, int WN, int S, bool ALONG>
 __global__ void __launch_bounds__(kGemmThreads)
     k_grouped(GroupedArgs a, int n_cols) {
   constexpr int P = kPlanes<T>, MB = WM / 32, NB = WN / 32;
@@ -59,32 +58,17 @@ __global__ void __launch_bounds__(kGemmThreads)
 #pragma unroll
       for (int i = 0; i < CA; ++i) {
         const int k = k0 + (tid + i * kGemmThreads) % TA::kChunks * 8;
-        if (EVEN) {
-          ra[i].load(pa[i] + min(k, a.k - 8));
-          ra[i].keep(k < a.k);
-        } else {
-          ra[i].load(pa[i] + k, a.k - k);
-        }
+        ra[i].load(pa[i] + k, a.k - k);
       }
 #pragma unroll
       for (int i = 0; i < CB; ++i) {
         const int c = tid + i * kGemmThreads;
         if (ALONG) {
           const int k = k0 + c % TB::kChunks * 8, col = min(col0 + c / TB::kChunks, a.cols - 1);
-          if (EVEN) {
-            rb[i].load(w + (int64_t)col * a.k + min(k, a.k - 8));
-            rb[i].keep(k < a.k);
-          } else {
-            rb[i].load(w + (int64_t)col * a.k + k, a.k - k);
-          }
+          rb[i].load(w + (int64_t)col * a.k + k, a.k - k);
         } else {
           const int k = k0 + c / TB::kChunks, col = col0 + c % TB::kChunks * 8;
-          if (EVEN) {
-            rb[i].load(w + (int64_t)min(k, a.k - 1) * a.cols + min(col, a.cols - 8));
-            rb[i].keep(k < a.k);
-          } else {
-            rb[i].load(w + (int64_t)min(k, a.k - 1) * a.cols + col, k < a.k ? a.cols - col : 0);
-          }
+          rb[i].load(w + (int64_t)min(k, a.k - 1) * a.cols + col, k < a.k ? a.cols - col : 0);
         }
       }
     };
@@ -267,14 +251,14 @@ hipError_t fast(const GroupedArgs& a) {
   });
 }
 
-template <typename T>
+template <typename T, int B, int W>
 hipError_t any(const GroupedArgs& a) {
   constexpr int S = sizeof(T) == 4 ? 32 : 64;
-  return tiles(a, 64, 64, [&](dim3 grid, int cols) {
+  return tiles(a, B, B, [&](dim3 grid, int cols) {
     if (a.transposed)
-      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, true, false>), grid, dim3(kGemmThreads), 0, a.stream, a, cols);
+      hipLaunchKernelGGL((k_grouped<T, B, B, W, W, S, true>), grid, dim3(kGemmThreads), 0, a.stream, a, cols);
     else
-      hipLaunchKernelGGL((k_grouped<T, 64, 64, 32, 32, S, false, false>), grid, dim3(kGemmThreads), 0, a.stream, a, cols);
+      hipLaunchKernelGGL((k_grouped<T, B, B, W, W, S, false>), grid, dim3(kGemmThreads), 0, a.stream, a, cols);
   });
 }
 
@@ -282,10 +266,14 @@ template <typename T>
 hipError_t product(const GroupedArgs& a) {
   constexpr int N = 16 / sizeof(T);
   const auto whole = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  if (a.k % N || a.cols % N || a.lda % N || !whole(a.a) || !whole(a.w)) return any<T>(a);
   const int64_t even = a.n / a.n_groups;
-  if (even <= 32) return fast<T, 1, 2, 1, 1, 4>(a);
   const auto count = [&](int bm, int bn) { return (a.n / bm + a.n_groups / 2) * ((a.cols + bn - 1) / bn); };
+  // Of any alignment: the wider tile reads the operands half as often, but has four times fewer workgroups, and
+  // the loads through registers need many (bfloat16, 32,768 rows, 16 groups, 1,023 x 2,047: 382 against 434 us;
+  // 8,192 rows, 8 groups, 511 x 2,047: 87 against 76).
+  if (a.k % N || a.cols % N || a.lda % N || !whole(a.a) || !whole(a.w))
+    return even >= 64 && count(128, 128) >= 2048 ? any<T, 128, 64>(a) : any<T, 64, 32>(a);
+  if (even <= 32) return fast<T, 1, 2, 1, 1, 4>(a);
   if constexpr (sizeof(T) == 2) {
     if (even >= 192 && count(256, 256) >= 512) return fast<T, 2, 4, 4, 2, 2>(a);
     return fast<T, 1, 4, 2, 1, 2>(a);

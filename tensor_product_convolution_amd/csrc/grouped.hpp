@@ -24,12 +24,6 @@ template <>
 struct Octet<bf16_t> {
   RawChunk<bf16_t> v;
   __device__ __forceinline__ void load(const bf16_t* p, int left) { v.load(p, left); }
-  __device__ __forceinline__ void load(const bf16_t* p) { v.v = *reinterpret_cast<const Chunk<bf16_t>::vec*>(p); }
-  __device__ __forceinline__ void keep(bool k) {
-    u4 b = __builtin_bit_cast(u4, v.v);
-    b = k ? b : u4{0, 0, 0, 0};
-    v.v = __builtin_bit_cast(Chunk<bf16_t>::vec, b);
-  }
   __device__ __forceinline__ float at(int j) const { return v.at(j); }
   __device__ __forceinline__ void frag(Frag<1>& f) const { f.p[0] = __builtin_bit_cast(b8, v.v); }
 };
@@ -39,17 +33,6 @@ struct Octet<float> {
   __device__ __forceinline__ void load(const float* p, int left) {
     a.load(p, left);
     b.load(p + 4, left - 4);
-  }
-  __device__ __forceinline__ void load(const float* p) {
-    a.v = *reinterpret_cast<const Chunk<float>::vec*>(p);
-    b.v = *reinterpret_cast<const Chunk<float>::vec*>(p + 4);
-  }
-  __device__ __forceinline__ void keep(bool k) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a.v[j] = k ? a.v[j] : 0.f;
-      b.v[j] = k ? b.v[j] : 0.f;
-    }
   }
   __device__ __forceinline__ float at(int j) const { return j < 4 ? a.at(j) : b.at(j - 4); }
   __device__ __forceinline__ void frag(Frag<3>& f) const {

@@ -234,3 +234,45 @@ def test_stream_and_graph(tpc):
         graph.replay()
         torch.cuda.synchronize()
         assert same(held, call())
+
+
+WIDE = [  # slots, groups, in, out, kind, fan, x rows, y rows, spare values of a row: sizes that take other tiles
+    (700, 40, 72, 136, "even", 1, "source", "source", 0), (700, 40, 136, 72, "skew", 2, "source", "grouped", 8),
+    (1000, 118, 256, 128, "skew", 1, "source", "source", 0), (900, 3, 40, 264, "skew", 1, "source", "source", 8),
+    (2000, 7, 264, 200, "skew", 2, "source", "grouped", 0), (4098, 3, 512, 520, "skew", 3, "grouped", "source", 0),
+    (5000, 5, 1032, 512, "even", 1, "source", "source", 8), (16500, 3, 72, 2056, "even", 2, "source", "grouped", 0),
+    (16500, 3, 2056, 72, "skew", 1, "grouped", "source", 0), (4000, 16, 1016, 1032, "skew", 1, "source", "source", 0),
+    (16500, 2, 33, 2047, "skew", 1, "source", "source", 0), (16500, 2, 2047, 33, "skew", 2, "source", "grouped", 1),
+    (16500, 3, 1023, 2047, "skew", 1, "source", "source", 0)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", WIDE, ids=str)
+def test_grouped_tiles(tpc, dtype, case):
+    """Rows of whole 16-byte chunks, and sizes from a few rows a group to many tiles."""
+    slots, groups, i, o, kind, fan, x_rows, y_rows, spare = case
+    print(f"grouped tiles {dtype} {case}", flush=True)
+    r = np.random.default_rng(slots + i + o)
+    dt = DT[dtype]
+    index = index_of(kind, slots, groups, r)
+    g = tpc.group_rows(ints(index).view(-1, fan) if fan > 1 else ints(index), groups)
+    ptr, rows = ob.group_rows(index, groups)
+    nx = slots // fan if x_rows == "source" else slots
+    x = dev(r.normal(size=(nx, i + spare)), dt)[:, spare:]
+    w, b = dev(r.normal(size=(groups, i, o)), dt), dev(r.normal(size=(groups, o)), dt)
+    gz = dev(r.normal(size=(slots, o + spare)), dt)[:, :o]
+    X, Wt, B, G = f64(x), f64(w), f64(b), f64(gz)
+    z = ob.grouped_forward(X, Wt, ptr, rows, fan, B, x_rows, y_rows)
+    bound = (i + 16) * U * ob.grouped_forward(np.abs(X), np.abs(Wt), ptr, rows, fan, np.abs(B), x_rows, y_rows)
+    y, pre = tpc.grouped_linear_forward(x, w, g, bias=b, act="silu", x_rows=x_rows, y_rows=y_rows, want_pre=True)
+    near(pre, z, bound, "pre", dtype)
+    near(y, ob.silu(f64(pre)), 8 * U * (np.abs(f64(pre)) + 1), "y", dtype)
+    assert torch.equal(pre, tpc.grouped_linear_forward(x, w, g, bias=b, x_rows=x_rows, y_rows=y_rows))
+    back = tpc.grouped_linear_backward(gz, x, w, g, x_rows=x_rows, y_rows=y_rows, want_bias=True)
+    want = ob.grouped_backward(G, X, Wt, ptr, rows, fan, x_rows, y_rows)
+    size = abs_parts(G, X, Wt, ptr, rows, fan, x_rows, y_rows)
+    parts = (W if dtype == "bf16" else U) if fan > 1 and x_rows == "source" else 0.0
+    near(back[0], want[0], ((o + 16 + fan) * U + parts) * size[0], "grad_x", dtype)
+    near(back[1], want[1], (slots + 16) * U * size[1], "grad_w", dtype)
+    near(back[2], want[2], (slots + 16) * U * size[2], "grad_bias", dtype)
+    assert same(back, tpc.grouped_linear_backward(gz, x, w, g, x_rows=x_rows, y_rows=y_rows, want_bias=True))
