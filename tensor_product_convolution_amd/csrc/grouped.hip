@@ -125,16 +125,18 @@ __global__ void __launch_bounds__(kGemmThreads)
   }
 }
 
-// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32, D buffers.
-template <typename T, int WM, int WN, int MB, int NB, int D, bool ALONG>
-__global__ void __launch_bounds__(64 * WM * WN, 2)
+// Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32, D buffers.  KS sets of such waves
+// take the steps of the contraction in turn; their sums are joined in LDS.
+template <typename T, int WM, int WN, int MB, int NB, int D, int KS, bool ALONG>
+__global__ void __launch_bounds__(64 * WM * WN * KS, 2)
     k_grouped_fast(GroupedArgs a, int n_cols) {
   constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
   typedef AlongLds<T, BM, W> TA;
   typedef typename std::conditional<ALONG, AlongLds<T, BN, W>, AcrossLds<T, BN, W>>::type TB;
-  TPC_BUFFERS(D, TA, TB);
   __shared__ int arow[BM], crow[BM];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, id = __builtin_amdgcn_readfirstlane(tid >> 6), split = KS > 1 ? id / W : 0,
+            wave = id - split * W;
+  TPC_BUFFERS(D, TA, TB, KS, split);
   const int n = (int)a.n;
   const Parts parts(a.ptr, a.n_groups, a.n_groups + 1, n, BM, 0);
   if ((int)blockIdx.x >= parts.total * n_cols) return;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   const Part part = parts.at(rt);
   if (part.first >= part.hi) return;       // not with a valid ptr
   const int rows = min(BM, part.hi - part.first), col0 = ct * BN;
-  for (int i = tid; i < BM; i += 64 * W) {
+  for (int i = tid; i < BM; i += 64 * W * KS) {
     // rows past the part's end repeat its last one; nothing of them is stored
     const int place = part.first + min(i, rows - 1), slot = a.a_div || a.c_div ? slot_at(a.rows, place, n) : 0;
     arow[i] = a.a_div ? slot / a.a_div : place;
@@ -170,10 +172,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < TA::Q; ++q) pa[q] = (const T*)a.a + arow[TA::row(q, wave, lane)] * a.lda + TA::first(lane);
-    const int steps = (a.k + S - 1) / S;
+    const int steps = (a.k + S * KS - 1) / (S * KS);
     const T* zeros = reinterpret_cast<const T*>(kZeros);
     const auto load = [&](int t, auto buffer) {
-      const int k0 = t * S, mine = k0 + TA::first(lane);
+      const int k0 = (t * KS + split) * S, mine = k0 + TA::first(lane);
       if (k0 + S <= a.k) {
 #pragma unroll
         for (int q = 0; q < TA::Q; ++q) fetch16(pa[q] + k0, TA::place(buffers.a(buffer), q, wave));
@@ -207,6 +209,16 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     }
   }
   __syncthreads();
+  if constexpr (KS > 1) {
+    constexpr int kOwn = 64 * 16 * MB * NB;
+    static_assert(W * kOwn * sizeof(float) <= kBuffer);
+    float* sum = reinterpret_cast<float*>(p0_) + wave * kOwn + lane;
+    if (split > 0) sums.put(sum + split * (kBuffer / 4));
+    __syncthreads();
+    if (split > 0) return;
+#pragma unroll
+    for (int s = 1; s < KS; ++s) sums.add(sum + s * (kBuffer / 4));
+  }
   float* own = buffers.template own<32 * 32 * NB * (int)sizeof(float), W>(wave);
   const int col = col0 + 32 * NB * wn + lane % (4 * NB) * 8, left = a.cols - col;
   float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -241,13 +253,13 @@ hipError_t tiles(const GroupedArgs& a, int bm, int bn, F&& f) {
   return hipGetLastError();
 }
 
-template <typename T, int WM, int WN, int MB, int NB, int D>
+template <typename T, int WM, int WN, int MB, int NB, int D, int KS = 1>
 hipError_t fast(const GroupedArgs& a) {
   return tiles(a, 32 * WM * MB, 32 * WN * NB, [&](dim3 grid, int cols) {
     if (a.transposed)
-      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, true>), grid, dim3(64 * WM * WN), 0, a.stream, a, cols);
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, KS, true>), grid, dim3(64 * WM * WN * KS), 0, a.stream, a, cols);
     else
-      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, false>), grid, dim3(64 * WM * WN), 0, a.stream, a, cols);
+      hipLaunchKernelGGL((k_grouped_fast<T, WM, WN, MB, NB, D, KS, false>), grid, dim3(64 * WM * WN * KS), 0, a.stream, a, cols);
   });
 }
 
@@ -273,12 +285,23 @@ hipError_t product(const GroupedArgs& a) {
   // 8,192 rows, 8 groups, 511 x 2,047: 87 against 76).
   if (a.k % N || a.cols % N || a.lda % N || !whole(a.a) || !whole(a.w))
     return even >= 64 && count(128, 128) >= 2048 ? any<T, 128, 64>(a) : any<T, 64, 32>(a);
-  if (even <= 32) return fast<T, 1, 2, 1, 1, 4>(a);
+  // Few tiles leave most of the chip idle: four sets of waves share a tile's contraction where that is more than
+  // two steps long (float32, 256 rows, 2 groups, 2,048 x 512: 24 against 48 us; 1,536 rows, 4 groups, 256 x 256:
+  // 7.3 against 10.8; 288 such tiles, 512 x 2,048: 19 against 17).
+  const int64_t small = count(32, 64);
+  if (small <= 256 && a.k > 2 * kDeep<T>) return fast<T, 1, 2, 1, 1, 3, 4>(a);
+  // Groups of few rows are bound by their weights, which narrow tiles with four buffers bring in best (bfloat16,
+  // 32 rows, 32 groups, 2,048 x 512: 11.5 against 21 us).  So are bfloat16 tiles that are few (2,048 rows, 8
+  // groups, 2,048 x 512, 544 tiles: 17.6 against 22.4; 4,096 rows, 1,024 x 512, 1,056 tiles: 18.2 against 15).
+  if (even <= 32 || (sizeof(T) == 2 && small <= 768)) return fast<T, 1, 2, 1, 1, 4>(a);
+  // Wide tiles read less and share the splitting of float32, where there are enough to fill the chip several times
+  // (bfloat16, 65,536 rows, 8 groups, 512 x 2,048: 195 against 258 us; 8,192 rows: 43 against 35; float32, 16,384
+  // rows: 242 against 275; 4,096 rows of 512 x 1,024: 50 against 47).
   if constexpr (sizeof(T) == 2) {
     if (even >= 192 && count(256, 256) >= 512) return fast<T, 2, 4, 4, 2, 2>(a);
     return fast<T, 1, 4, 2, 1, 2>(a);
   } else {
-    if (count(128, 128) >= 256) return fast<T, 2, 2, 2, 2, 2>(a);
+    if (count(128, 128) >= 1024) return fast<T, 2, 2, 2, 2, 2>(a);
     return fast<T, 2, 2, 1, 1, 2>(a);
   }
 }

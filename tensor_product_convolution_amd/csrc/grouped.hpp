@@ -333,6 +333,29 @@ struct Sums {
     else
       return part[i][j];
   }
+  // the totals, 64 floats apart
+  __device__ __forceinline__ void put(float* to) const {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) to[64 * (16 * (i * NB + j) + r)] = total(i, j)[r];
+  }
+  __device__ __forceinline__ void add(const float* from) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float x = from[64 * (16 * (i * NB + j) + r)];
+          if constexpr (kTwo)
+            all[i][j][r] += x;
+          else
+            part[i][j][r] += x;
+        }
+  }
   __device__ __forceinline__ bool finite() const {
     bool ok = true;
 #pragma unroll
@@ -516,10 +539,13 @@ struct Buffers {
     return reinterpret_cast<float*>(wave < kEach ? p0 + wave * OWN : p1 + (wave - kEach) * OWN);
   }
 };
-#define TPC_BUFFERS(D, TA, TB)                                                                                            \
+// Each of KS `split`s of the contraction has buffers of its own.
+#define TPC_BUFFERS(D, TA, TB, KS, split)                                                                                 \
   constexpr int kBuffer = TA::kBytes + TB::kBytes;                                                                        \
-  __shared__ __attribute__((aligned(16))) uint8_t p0_[kBuffer], p1_[kBuffer], p2_[D > 2 ? kBuffer : 16], p3_[D > 3 ? kBuffer : 16]; \
-  const Buffers<D, TA::kBytes, kBuffer> buffers{p0_, p1_, p2_, p3_}
+  __shared__ __attribute__((aligned(16))) uint8_t p0_[KS * kBuffer], p1_[KS * kBuffer], p2_[D > 2 ? KS * kBuffer : 16],   \
+      p3_[D > 3 ? KS * kBuffer : 16];                                                                                     \
+  const int mine_ = (split) * kBuffer;                                                                                    \
+  const Buffers<D, TA::kBytes, kBuffer> buffers{p0_ + mine_, p1_ + mine_, p2_ + (D > 2 ? mine_ : 0), p3_ + (D > 3 ? mine_ : 0)}
 
 // eight values, loaded and stored by the type's chunks; left: values there are
 template <typename T>

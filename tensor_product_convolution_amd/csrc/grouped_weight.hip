@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   constexpr int W = WM * WN, BM = 32 * WM * MB, BN = 32 * WN * NB, S = kDeep<T>;
   typedef AcrossLds<T, BM, W> TA;
   typedef AcrossLds<T, BN, W> TB;
-  TPC_BUFFERS(D, TA, TB);
+  TPC_BUFFERS(D, TA, TB, 1, 0);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = n_rows * n_cols, n = (int)a.n;
   const Parts parts(a.ptr, a.n_groups, a.n_groups, n, size, 1);

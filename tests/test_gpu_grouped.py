@@ -243,7 +243,9 @@ WIDE = [  # slots, groups, in, out, kind, fan, x rows, y rows, spare values of a
     (5000, 5, 1032, 512, "even", 1, "source", "source", 8), (16500, 3, 72, 2056, "even", 2, "source", "grouped", 0),
     (16500, 3, 2056, 72, "skew", 1, "grouped", "source", 0), (4000, 16, 1016, 1032, "skew", 1, "source", "source", 0),
     (16500, 2, 33, 2047, "skew", 1, "source", "source", 0), (16500, 2, 2047, 33, "skew", 2, "source", "grouped", 1),
-    (16500, 3, 1023, 2047, "skew", 1, "source", "source", 0)]
+    (16500, 3, 1023, 2047, "skew", 1, "source", "source", 0),
+    (9, 2, 1032, 64, "skew", 1, "source", "source", 0), (130, 3, 264, 1000, "skew", 2, "source", "grouped", 8),
+    (17000, 3, 512, 1032, "skew", 1, "source", "source", 0), (3000, 8, 200, 512, "skew", 1, "grouped", "source", 0)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
