@@ -55,20 +55,33 @@ struct Chunks {
   static constexpr __device__ __forceinline__ int second(int j) { return INTER ? 2 * j + 1 : N + j; }
 };
 
+// The length of a run, compared anew at each use: a mask in registers for each of its values is more than there is
+// room for.
+__device__ __forceinline__ int length_of(int left) {
+  asm volatile("" : "+v"(left));
+  return left;
+}
+
 template <typename T, bool INTER>
 struct RawPairs {
   RawChunk<T> run[2];
   __device__ __forceinline__ void load(const T* head, const Chunks<T, INTER>& c) {
-    run[0].load(head + c.at[0], c.left[0]);
-    run[1].load(head + c.at[1], c.left[1]);
+    run[0].load(head + c.at[0], length_of(c.left[0]));
+    run[1].load(head + c.at[1], length_of(c.left[1]));
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < Chunk<T>::kN; ++j) run[i].v[j] = (T)0.f;
   }
   __device__ __forceinline__ float at(int j) const { return run[j / Chunk<T>::kN].at(j % Chunk<T>::kN); }
 };
 
 template <typename T, bool INTER>
 __device__ __forceinline__ void store_pairs(T* head, const Chunks<T, INTER>& c, const float* v) {
-  store_chunk(head + c.at[0], c.left[0], v);
-  store_chunk(head + c.at[1], c.left[1], v + Chunk<T>::kN);
+  store_chunk(head + c.at[0], length_of(c.left[0]), v);
+  store_chunk(head + c.at[1], length_of(c.left[1]), v + Chunk<T>::kN);
 }
 
 // float32 values laid out like a head
@@ -93,20 +106,49 @@ __device__ __forceinline__ float2 turn_of(const HeadArgs& a, int64_t row, int i)
   return make_float2(c, s);
 }
 
-__device__ __forceinline__ void fill_angles(const HeadArgs& a, int64_t row0, int rows, float2* cs) {
-  if (a.pairs == 0) return;
-  for (int i = threadIdx.x; i < rows * a.pairs; i += kThreads) cs[i] = turn_of(a, row0 + i / a.pairs, i % a.pairs);
-}
-
-template <typename T, bool INTER>
-__device__ __forceinline__ void cos_sin(const float2* cs, const Chunks<T, INTER>& c, float2* o) {
+// The angles of a block of rows, the rows' pairs filled up to whole chunks with pairs that do not turn; so is the
+// chunk behind them all, which serves the rest of a head.
+template <typename T>
+struct Angles {
+  static constexpr int N = Chunk<T>::kN;
+  float2* cs;                              // [kTrig + N]
+  int pitch, at, by;                       // of a row; this thread's chunk in row r: at + r by
+  __device__ __forceinline__ Angles(const HeadArgs& a, float2* cs, int pair) : cs(cs) {
+    pitch = (a.pairs + N - 1) / N * N;
+    at = pair < 0 ? kTrig : pair;
+    by = pair < 0 ? 0 : pitch;
+  }
+  __device__ __forceinline__ void fill(const HeadArgs& a, int64_t row0, int rows) const {
+    if (threadIdx.x < N) cs[kTrig + threadIdx.x] = make_float2(1.f, 0.f);
+    for (int i = threadIdx.x; i < rows * pitch; i += kThreads) {
+      const int row = i / pitch, pair = i - row * pitch;
+      cs[i] = pair < a.pairs ? turn_of(a, row0 + row, pair) : make_float2(1.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void get(int row, float2* o) const {
+    const float4* from = reinterpret_cast<const float4*>(cs + at + row * by);
 #pragma unroll
-  for (int j = 0; j < Chunk<T>::kN; ++j) o[j] = j < c.pairs ? cs[c.pair + j] : make_float2(1.f, 0.f);
-}
+    for (int j = 0; j < N; j += 2) {
+      const float4 t = from[j / 2];
+      o[j] = make_float2(t.x, t.y);
+      o[j + 1] = make_float2(t.z, t.w);
+    }
+  }
+};
 
-// sum over the 2^lg neighbouring threads of a head, in a fixed order
+// the value of another lane of the row of 16
+template <int CTRL>
+__device__ __forceinline__ float lane_of(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// sum over the 2^lg neighbouring threads of a head, in a fixed order: with the neighbour, the pair next to it,
+// then the mirror image in 8 and in 16 lanes, whose parts hold one sum each by then
 __device__ __forceinline__ float head_sum(float v, int lg) {
-  for (int m = 1 << lg >> 1; m > 0; m >>= 1) v += __shfl_xor(v, m, 64);
+  if (lg > 0) v += lane_of<0xb1>(v);
+  if (lg > 1) v += lane_of<0x4e>(v);
+  if (lg > 2) v += lane_of<0x141>(v);
+  if (lg > 3) v += lane_of<0x140>(v);
+  for (int m = 16; m < 1 << lg; m <<= 1) v += __shfl_xor(v, m, 64);
   return v;
 }
 
@@ -124,8 +166,10 @@ template <typename T, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads)
     k_heads_fwd(HeadArgs a) {
   constexpr int V = 2 * Chunk<T>::kN;
-  __shared__ float2 cs[kTrig];
+  __shared__ __attribute__((aligned(16))) float2 cs[kTrig + Chunk<T>::kN];
   const Chunks<T, INTER> c((int)threadIdx.x & ((1 << a.lg) - 1), a.d, a.pairs);
+  const Angles<T> angles(a, cs, c.pair);
+  const float part = 1.f / (float)a.d;
   float g[2][V];
   if (NORM) {
     load_like<T, INTER>(a.gamma_q, c, g[0]);
@@ -141,9 +185,12 @@ __global__ void __launch_bounds__(kThreads)
   RawPairs<T, INTER> x;
   {                                        // in flight while the angles are taken
     const Item it(a, 0);
-    if (it.row < rows) x.load(source(it), c);
+    if (it.row < rows)
+      x.load(source(it), c);
+    else
+      x.clear();
   }
-  fill_angles(a, row0, rows, cs);
+  angles.fill(a, row0, rows);
   __syncthreads();
   for (int n = 0; n < turns; ++n) {
     const Item it(a, n), next(a, n + 1);
@@ -152,19 +199,22 @@ __global__ void __launch_bounds__(kThreads)
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = has ? x.at(j) : 0.f;
+      v[j] = x.at(j);
       s += v[j] * v[j];
     }
-    if (next.row < rows) x.load(source(next), c);
+    if (next.row < rows)
+      x.load(source(next), c);
+    else
+      x.clear();
     if (NORM) {
-      const float r = 1.f / sqrtf(head_sum(s, a.lg) / (float)a.d + a.eps);
+      const float r = 1.f / sqrtf(head_sum(s, a.lg) * part + a.eps);
       const bool key = it.head >= a.hq;
 #pragma unroll
       for (int j = 0; j < V; ++j) v[j] = v[j] * r * (key ? g[1][j] : g[0][j]);
     }
     if (!has) continue;
     float2 t[V / 2];
-    cos_sin(cs + it.row * a.pairs, c, t);
+    angles.get(it.row, t);
 #pragma unroll
     for (int j = 0; j < V / 2; ++j) {
       const float p = v[c.first(j)], q = v[c.second(j)];
@@ -183,15 +233,17 @@ __global__ void __launch_bounds__(kThreads)
 // the variants round alike.  Weights and frequencies are read from LDS, by chunk: in registers they
 // leave two waves a SIMD.
 template <typename T, bool INTER, bool NORM, bool POS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
     k_heads_bwd(HeadBwdArgs b) {
   const HeadArgs& a = b.f;
   constexpr int V = 2 * Chunk<T>::kN;
-  __shared__ float2 cs[kTrig];             // at the end the waves' weight gradients
+  __shared__ __attribute__((aligned(16))) float2 cs[kTrig + Chunk<T>::kN];     // at the end the waves' weight gradients
   extern __shared__ __attribute__((aligned(16))) float lds[];
   const int n_chunks = 1 << a.lg, lane_c = (int)threadIdx.x & (n_chunks - 1), heads = a.hq + a.hk, per_axis = a.rows * heads;
   float *gl = lds, *fl = gl + (NORM ? 2 * n_chunks * V : 0), *sums = fl + (POS ? kMaxAxes * n_chunks * V / 2 : 0);
   const Chunks<T, INTER> c(lane_c, a.d, a.pairs);
+  const Angles<T> angles(a, cs, c.pair);
+  const float part = 1.f / (float)a.d;
   if ((int)threadIdx.x < n_chunks) {
     float v[V];
     if (NORM) {
@@ -213,25 +265,32 @@ __global__ void __launch_bounds__(kThreads)
   float gg[2][V];
 #pragma unroll
   for (int j = 0; j < V; ++j) gg[0][j] = gg[1][j] = 0.f;
-  // the queries (KEY 0) or keys of a block of rows
+  const int step = kThreads >> a.lg, first = (int)threadIdx.x >> a.lg;
+  RawPairs<T, INTER> x, u;
+  const auto fetch = [&](auto key, int64_t row, int64_t end, int head) {
+    if (row >= end) {                      // zeros where there is no head
+      x.clear();
+      u.clear();
+      return;
+    }
+    x.load((const T*)(key() ? a.k : a.q) + row * (key() ? a.k_stride : a.q_stride) + head * a.d, c);
+    u.load((const T*)(key() ? b.gk_up : b.gq_up) + row * (key() ? b.gk_up_stride : b.gq_up_stride) + head * a.d, c);
+  };
+  // what a thread begins the queries or keys of a block with
+  const auto begin = [&](auto key, int64_t row0) {
+    const int H = key() ? a.hk : a.hq, row = first / H;
+    fetch(key, row0 + row, min(row0 + a.rows, a.n_rows), first - row * H);
+  };
+  // the queries (KEY 0) or keys of a block of rows; the loads of what comes next are in flight throughout
   const auto side = [&](auto key, int64_t row0, int rows) {
     constexpr int KEY = key();
-    const int H = KEY ? a.hk : a.hq, before = KEY ? a.hq : 0, step = kThreads >> a.lg, first = (int)threadIdx.x >> a.lg;
+    const int H = KEY ? a.hk : a.hq, before = KEY ? a.hq : 0;
     const int step_row = step / H, step_head = step - step_row * H;
-    const T *src = (const T*)(KEY ? a.k : a.q), *up = (const T*)(KEY ? b.gk_up : b.gq_up);
-    const int64_t xs = KEY ? a.k_stride : a.q_stride, us = KEY ? b.gk_up_stride : b.gq_up_stride;
     T* out = (T*)(KEY ? b.gk : b.gq);
     const int64_t os = KEY ? b.gk_stride : b.gq_stride;
     int row = first / H, head = first - row * H;
-    RawPairs<T, INTER> x, u;
-    const auto fetch = [&](int r, int h) {
-      if (r >= rows) return;
-      x.load(src + (row0 + r) * xs + h * a.d, c);
-      u.load(up + (row0 + r) * us + h * a.d, c);
-    };
-    fetch(row, head);
     if (KEY == 0) {
-      fill_angles(a, row0, rows, cs);
+      angles.fill(a, row0, rows);
       __syncthreads();
     }
     for (int n = (rows * H + step - 1) / step; n > 0; --n) {
@@ -239,8 +298,8 @@ __global__ void __launch_bounds__(kThreads)
       float v[V], h[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        v[j] = has ? x.at(j) : 0.f;
-        h[j] = has ? u.at(j) : 0.f;
+        v[j] = x.at(j);
+        h[j] = u.at(j);
       }
       const int r0 = row, h0 = head;
       row += step_row;
@@ -249,9 +308,15 @@ __global__ void __launch_bounds__(kThreads)
         head -= H;
         ++row;
       }
-      fetch(row, head);
+      if (n > 1) {
+        fetch(key, row0 + row, row0 + rows, head);
+      } else if (KEY == 0) {
+        begin(std::integral_constant<int, 1>(), row0);
+      } else {
+        begin(std::integral_constant<int, 0>(), row0 + (int64_t)gridDim.x * a.rows);
+      }
       float2 t[V / 2];
-      cos_sin(cs + (has ? r0 : 0) * a.pairs, c, t);
+      angles.get(has ? r0 : 0, t);
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
         const float p = h[c.first(j)], q = h[c.second(j)];
@@ -267,8 +332,8 @@ __global__ void __launch_bounds__(kThreads)
           s1 = fmaf(v[j], v[j], s1);
           s2 = fmaf(h[j] * g[j], v[j], s2);
         }
-        r = 1.f / sqrtf(head_sum(s1, a.lg) / (float)a.d + a.eps);
-        m = head_sum(s2, a.lg) * r / (float)a.d;
+        r = 1.f / sqrtf(head_sum(s1, a.lg) * part + a.eps);
+        m = head_sum(s2, a.lg) * r * part;
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] *= r;
       }
@@ -298,6 +363,7 @@ __global__ void __launch_bounds__(kThreads)
       if (has) store_pairs(out + (row0 + r0) * os + h0 * a.d, c, h);
     }
   };
+  begin(std::integral_constant<int, 0>(), (int64_t)blockIdx.x * a.rows);
   for (int64_t row0 = (int64_t)blockIdx.x * a.rows; row0 < a.n_rows; row0 += (int64_t)gridDim.x * a.rows) {
     const int rows = (int)min((int64_t)a.rows, a.n_rows - row0);
     side(std::integral_constant<int, 0>(), row0, rows);
@@ -373,7 +439,7 @@ void shape_of(int dtype, HeadArgs& a, int64_t blocks) {
   const int chunks = (a.pairs + n - 1) / n + (a.d - 2 * a.pairs + 2 * n - 1) / (2 * n);
   a.lg = 0;
   while ((1 << a.lg) < chunks) ++a.lg;
-  const int64_t most = std::max(1, std::min(kTrig / std::max(1, a.pairs), (4 * kThreads) / ((a.hq + a.hk) << a.lg)));
+  const int64_t most = std::max(1, std::min(kTrig / std::max(1, (a.pairs + n - 1) / n * n), (4 * kThreads) / ((a.hq + a.hk) << a.lg)));
   a.rows = (int)std::max<int64_t>(1, std::min<int64_t>({most, 64, (a.n_rows + blocks - 1) / blocks}));
 }
 
