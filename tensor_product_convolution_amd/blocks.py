@@ -340,6 +340,11 @@ class AdamW:
             raise ValueError("copies and weight_decay need one entry for each parameter")
         low = [None if c is None else _need(c, f"copies[{i}]", torch.bfloat16, params[i].shape, self._dev)
                for i, c in enumerate(copies)]
+        end = 0                            # a value in two tensors would be updated twice, by whichever comes last
+        for first, last in sorted((t.data_ptr(), t.data_ptr() + t.nbytes) for t in (*params, *copies) if t is not None and t.numel()):
+            if first < end:
+                raise ValueError("a parameter or copy is there twice, or two overlap")
+            end = last
         self.params, self.copies, self.bits, self.betas, self.eps, self.max_norm = params, copies, bits, betas, eps, max_norm
         self.lr, self.seed = lr, seed
         self.numels = [p.numel() for p in params]

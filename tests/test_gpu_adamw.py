@@ -190,3 +190,15 @@ def test_another_stream(tpc):
         torch.cuda.synchronize()
         out.append((opt_p[0], *opt.state()[1:]))
     assert same(*out)
+
+
+def test_a_tensor_twice_is_refused(tpc):
+    p, none = torch.zeros(300, device="cuda"), torch.zeros(0, device="cuda")
+    tpc.AdamW([p[:100], p[100:], none, none])
+    with pytest.raises(ValueError, match="twice"):
+        tpc.AdamW([p, torch.zeros(3, device="cuda"), p])
+    with pytest.raises(ValueError, match="twice"):
+        tpc.AdamW([p[:200], p[100:]])
+    low = torch.zeros(300, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="twice"):
+        tpc.AdamW([p[:100], p[100:200]], copies=[low[:100], low[50:150]])

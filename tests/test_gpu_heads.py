@@ -170,3 +170,18 @@ def test_stream_and_graph(tpc):
         graph.replay()
         torch.cuda.synchronize()
         assert same(held, call())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shape", [(70001, 1, 1, 8, 3, 2, 0), (70001, 2, 1, 20, 7, 1, 0), (20003, 8, 2, 40, 12, 3, 0), (9001, 3, 3, 64, 32, 1, 0)],
+                         ids=str)
+def test_many_rows(tpc, dtype, interleaved, shape):
+    """More rows than the workgroups of the backward hold at once; gradients in place of the upstream ones."""
+    print(f"heads {dtype} {shape} interleaved={interleaved}", flush=True)
+    s = problem(*shape[:6], dtype, True, 0)
+    kw = dict(s["kw"], interleaved=interleaved, eps=1e-5)
+    back = tpc.head_norm_rotate_backward(s["gq"], s["gk"], s["q"], s["k"], want_pos=True, **kw)
+    check(s, interleaved, 1e-5, dtype, tpc.head_norm_rotate_forward(s["q"], s["k"], **kw), back)
+    own = tpc.head_norm_rotate_backward(s["gq"], s["gk"], s["q"], s["k"], want_pos=True, outs=(s["gq"], s["gk"]), **kw)
+    assert own[0] is s["gq"] and same(own, back)
