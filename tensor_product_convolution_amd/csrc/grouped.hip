@@ -14,7 +14,7 @@ namespace {
 // Rows of any length and alignment: staged through registers.  BM x BN tile of four waves, WM x WN
 // each, S contraction values a step.  ALONG: w rows run along the contraction (transposed).
 template <typename T, int BM, int BN, int WM, int WN, int S, bool ALONG>
-__global__ void __launch_bounds__(kGemmThreads)
+__global__ void __launch_bounds__(kGemmThreads, 2)
     k_grouped(GroupedArgs a, int n_cols) {
   constexpr int P = kPlanes<T>, MB = WM / 32, NB = WN / 32;
   static_assert((BM / WM) * (BN / WN) * 64 == kGemmThreads);
@@ -36,13 +36,8 @@ __global__ void __launch_bounds__(kGemmThreads)
   const int rows = min(BM, part.hi - part.first), col0 = ct * BN;
   if (tid < BM) crow[tid] = tid < rows ? row_of(a.rows, part.first + tid, a.c_div, n) : -1;
   const bool none = part.group == a.n_groups;        // slots without a group
-  f16v acc[MB][NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  Sums<T, MB, NB> acc;
+  acc.clear();
   const int wm = wave % (BM / WM), wn = wave / (BM / WM);
   if (!none) {
     const T* pa[CA];
@@ -97,9 +92,11 @@ __global__ void __launch_bounds__(kGemmThreads)
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-          for (int j = 0; j < NB; ++j) acc[i][j] = mma(fa[i], fb[j], acc[i][j]);
+          for (int j = 0; j < NB; ++j) acc.part[i][j] = mma(fa[i], fb[j], acc.part[i][j]);
       }
+      if ((k0 + S) % acc.kTurn == 0) acc.gather();
     }
+    acc.gather();
   }
   __syncthreads();
 #pragma unroll
@@ -113,7 +110,7 @@ __global__ void __launch_bounds__(kGemmThreads)
       for (int r = 0; r < 16; ++r) {
         const int row = crow[wm * WM + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + r % 4];
         if (row < 0) continue;
-        float v = acc[i][j][r] + bias;
+        float v = acc.total(i, j)[r] + bias;
         if (a.pre) v = none ? 0.f : v * silu_slope((float)((const T*)a.pre)[row * a.ldpre + col]);
         if (a.act) {
           const T z = (T)v;                // the activation is that of the stored value

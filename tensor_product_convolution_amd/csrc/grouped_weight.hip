@@ -19,7 +19,7 @@ __device__ __forceinline__ int64_t part_slot(const Part& p, int size) {
 
 // Rows of any length and alignment: staged through registers.
 template <typename T, int B, int W>
-__global__ void __launch_bounds__(kGemmThreads)
+__global__ void __launch_bounds__(kGemmThreads, 2)
     k_grouped_weight(GroupedWeightArgs a, int size, int n_rows, int n_cols) {
   constexpr int S = std::is_same<T, float>::value ? 32 : 64, P = kPlanes<T>, NB = W / 32;
   static_assert((B / W) * (B / W) * 64 == kGemmThreads);
@@ -38,13 +38,8 @@ __global__ void __launch_bounds__(kGemmThreads)
   const int k0 = tile / n_cols * B, c0 = tile % n_cols * B;
   const int end = min(part.hi, part.first + size);
   const bool bias = a.grad_bias && k0 == 0;
-  f16v acc[NB][NB];
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  Sums<T, NB, NB> acc;
+  acc.clear();
   float sums[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const int wm = wave % (B / W), wn = wave / (B / W), chunk = tid % Tile::kChunks, trow = tid / Tile::kChunks;
   const int kc = k0 + chunk * 8, cc = c0 + chunk * 8;
@@ -98,9 +93,11 @@ __global__ void __launch_bounds__(kGemmThreads)
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mma(fa[i], fb[j], acc[i][j]);
+        for (int j = 0; j < NB; ++j) acc.part[i][j] = mma(fa[i], fb[j], acc.part[i][j]);
     }
+    if ((s0 - part.first + S) % acc.kTurn == 0) acc.gather();
   }
+  acc.gather();
   const bool whole = part.hi - part.lo <= size;
   const int64_t mat = (int64_t)a.k * a.cols;
   float* to = whole ? nullptr : a.part + part_slot(part, size) * (mat + a.cols);
@@ -116,9 +113,9 @@ __global__ void __launch_bounds__(kGemmThreads)
         if (row >= a.k) continue;
         const int64_t at = (int64_t)row * a.cols + col;
         if (whole)
-          ((T*)a.grad_w)[part.group * mat + at] = (T)acc[i][j][r];
+          ((T*)a.grad_w)[part.group * mat + at] = (T)acc.total(i, j)[r];
         else
-          to[at] = acc[i][j][r];
+          to[at] = acc.total(i, j)[r];
       }
   }
   if (!bias) return;
@@ -182,17 +179,25 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   };
   const int steps = part.first < end ? (end - part.first + S - 1) / S : 0;
   Sums<T, MB, NB> sums;
-  float colsum[NB];
+  float colsum[NB], colall[NB];            // of the bias, in two levels like the sums
+  const auto gather = [&] {
+    sums.gather();
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      colall[j] += colsum[j];
+      colsum[j] = 0.f;
+    }
+  };
   const auto all = [&](auto far) {
     sums.clear();
 #pragma unroll
-    for (int j = 0; j < NB; ++j) colsum[j] = 0.f;
+    for (int j = 0; j < NB; ++j) colsum[j] = colall[j] = 0.f;
     numbers(0);
     walk<D, TA::Q + TB::Q>(steps, load, [&](int t, auto buffer) {
       multiply<T, TA, TB, MB, NB, far(), true>(buffers.a(buffer), buffers.b(buffer), wm, wn, lane, sums, colsum, bias);
-      if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) sums.gather();
+      if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) gather();
     });
-    sums.gather();
+    gather();
   };
   all(std::false_type());
   if constexpr (sizeof(T) == 4) {          // infinities: again, with pieces that keep them
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   if (!bias) return;
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const float s = colsum[j] + __shfl_xor(colsum[j], 32, 64);
+    const float s = colall[j] + __shfl_xor(colall[j], 32, 64);
     const int c = c0 + 32 * NB * wn + 32 * j + lane;
     if (lane >= 32 || c >= a.cols) continue;
     if (whole)
