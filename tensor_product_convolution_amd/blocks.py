@@ -15,7 +15,8 @@ import torch
 from . import lib
 from .layers import _INT32_MAX, _call, _check, _code, _need, _rows, _too_large
 
-_is_tensor = lambda t: isinstance(t, torch.Tensor)
+_TENSORS = {torch.Tensor, torch.nn.Parameter}
+_dtype_of, _shape_of = torch.Tensor.dtype.__get__, torch.Tensor.shape.__get__
 _is_contiguous, _device_of, _address_of = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr
 _ROWS = {"source": 0, "grouped": 1}
 _ACTS = {None: 0, "silu": 1}
@@ -383,8 +384,9 @@ class AdamW:
         code, _ = _code(grads[0], "grads[0]")
         dt, dev, n = grads[0].dtype, self._dev, self._n
         # one pass over all tensors for each property: the host's time is most of a small step's
-        if not (all(map(_is_tensor, grads)) and [g.dtype for g in grads].count(dt) == n and [g.shape for g in grads] == self._shapes
-                and all(map(_is_contiguous, grads)) and list(map(_device_of, grads)).count(dev) == n):
+        if not (set(map(type, grads)) <= _TENSORS and list(map(_dtype_of, grads)).count(dt) == n
+                and list(map(_shape_of, grads)) == self._shapes and all(map(_is_contiguous, grads))
+                and list(map(_device_of, grads)).count(dev) == n):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 _need(g, f"grads[{i}]", dt, shape, dev)
         where = array.array("Q", map(_address_of, grads))

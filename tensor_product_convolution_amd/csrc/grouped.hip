@@ -11,7 +11,10 @@
 namespace tpc {
 namespace {
 
-// Rows of any length and alignment: staged through registers.  BM x BN tile of four waves, WM x WN
+// Rows of any length and alignment: staged through registers.  Bound by the loads: of one step they are all that a
+// wave has in flight.  The launch bounds hold float32, with its two levels of sums, to two workgroups a compute unit
+// (20,000 rows of 33 x 2,047: 92 against 178 us).  32,768 rows of 1,023 x 2,047, 16 groups: bfloat16 345 us (400
+// TFLOP/s), float32 1,020 (134).  BM x BN tile of four waves, WM x WN
 // each, S contraction values a step.  ALONG: w rows run along the contraction (transposed).
 template <typename T, int BM, int BN, int WM, int WN, int S, bool ALONG>
 __global__ void __launch_bounds__(kGemmThreads, 2)
@@ -124,6 +127,13 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
 
 // Rows of whole 16-byte chunks: WM x WN waves, each MB x NB blocks of 32 x 32, D buffers.  KS sets of such waves
 // take the steps of the contraction in turn; their sums are joined in LDS.
+// Large groups are bound by the matrix units and what feeds them: one group of 8,192 x 8,192 x 8,192 in bfloat16 runs at
+// 1,069 TFLOP/s, transposed weights at 1,206 (a library product: 1,205); 65,536 rows of 4,096 x 1,024, 64 groups, 624 us
+// (880), of 1,024 x 4,096 with the activation 795 (690): the activation and 512 MB of results follow each tile's 16 steps and
+// nothing covers them in a workgroup that has the compute unit to itself.  float32 runs at 160 to 175 TFLOP/s (a library
+// product: 154), bound by splitting as much as by the products; at 128 x 128 (100,000 rows, 89 groups) 45 us, twice what its
+// bytes need.  Few rows are bound by their weights: 16 rows that
+// choose 20 experts of 1,024 x 4,096, 37 us at 4.5 TB/s.
 template <typename T, int WM, int WN, int MB, int NB, int D, int KS, bool ALONG>
 __global__ void __launch_bounds__(64 * WM * WN * KS, 2)
     k_grouped_fast(GroupedArgs a, int n_cols) {

@@ -10,7 +10,10 @@
 // inverted index.  The order by group is a counting sort in which a wave numbers its 64
 // entries at once: the lanes of one group find each other by a ballot per bit of the group.
 // All of it is bound by HBM for many rows and by the launches for few: up to 8,192 entries are
-// ordered by one launch, more by three.
+// ordered by one launch, more by three.  4,096 rows of 8 logits take 4.7 us either way, 32,768 of 64 7.3; the order of
+// 1,536 entries 5.4 us, of 8,192 11, of 100,000 in 89 groups 21 (8 us and less a launch, each little more than its
+// chain of loads); the sums of 32,768 rows of 2 x 1,024 in bfloat16 33 us (201 MB, 6.1 TB/s, part of it still in the
+// last cache).
 #include <algorithm>
 
 #include "internal.hpp"
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(kThreads)
   }
   float top = 0.f, all = 0.f;
   u64 won[kMaxChoices];
-#pragma unroll
+  // rolled: unrolled, 32,768 rows of 64 take 8.9 us against 6.9
+#pragma unroll 1
   for (int j = 0; j < kMaxChoices; ++j) {
     if (j >= a.k) break;
     u64 best = 0;
