@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kThreads)
 // the variants round alike.  Weights and frequencies are read from LDS, by chunk: in registers they
 // leave two waves a SIMD.
 // bfloat16 is bound by vector instructions and loads together, float32 by HBM: 100,000 rows of 16 + 4 heads of 64 with
-// the positions' gradient 200 us (768 MB, 3.8 TB/s; half the time is vector issue), without it 168, float32 302
-// (5.1 TB/s); 30,000 rows of 16 + 16 heads of 128 176 and 150 us.  Masks of `has` for each value instead of zeroed
+// the positions' gradient 191 us (768 MB, 4.0 TB/s; half the time is vector issue), without it 163, float32 299
+// (5.1 TB/s); 30,000 rows of 16 + 16 heads of 128 176 and 150 us; 1,536 of 8 + 8 of 32 9 us and 4 for the join.  Masks of `has` for each value instead of zeroed
 // loads, angles read pair by pair under a condition, and sums through LDS took 292.
 template <typename T, bool INTER, bool NORM, bool POS>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
@@ -250,22 +250,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
   const Chunks<T, INTER> c(lane_c, a.d, a.pairs);
   const Angles<T> angles(a, cs, c.pair);
   const float part = 1.f / (float)a.d;
-  if ((int)threadIdx.x < n_chunks) {
+  if (NORM && (int)threadIdx.x < 2 * n_chunks) {
     float v[V];
-    if (NORM) {
+    load_like<T, INTER>((int)threadIdx.x < n_chunks ? a.gamma_q : a.gamma_k, c, v);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        load_like<T, INTER>(i ? a.gamma_k : a.gamma_q, c, v);
-#pragma unroll
-        for (int j = 0; j < V; ++j) gl[(i * n_chunks + lane_c) * V + j] = v[j];
-      }
-    }
-    if (POS) {
-#pragma unroll
-      for (int x = 0; x < kMaxAxes; ++x)
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j)
-          fl[(x * n_chunks + lane_c) * (V / 2) + j] = x < a.axes && j < c.pairs ? (float)a.freq[(c.pair + j) * a.axes + x] : 0.f;
+    for (int j = 0; j < V; ++j) gl[threadIdx.x * V + j] = v[j];
+  }
+  if (POS) {                               // [axis][pair]: chunk c of a head has pairs from c V / 2 on
+    const int most = n_chunks * V / 2;
+    for (int i = threadIdx.x; i < kMaxAxes * most; i += kThreads) {
+      const int x = i / most, pair = i - x * most;
+      fl[i] = x < a.axes && pair < a.pairs ? (float)a.freq[(int64_t)pair * a.axes + x] : 0.f;
     }
   }
   float gg[2][V];
@@ -391,13 +386,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
   float* mine = reinterpret_cast<float*>(cs);
   static_assert(sizeof(cs) >= 4 * 2 * 2 * kHeadsMaxDim * sizeof(float));
   __syncthreads();
-  for (int m = n_chunks; m < 64; m <<= 1) {
+  const auto join = [&](auto&& other) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      gg[0][j] += __shfl_xor(gg[0][j], m, 64);
-      gg[1][j] += __shfl_xor(gg[1][j], m, 64);
+      gg[0][j] += other(gg[0][j]);
+      gg[1][j] += other(gg[1][j]);
     }
-  }
+  };
+  // turned by 1, 2, 4, 8 in the row of 16 lanes, then the rows
+  if (n_chunks <= 1) join([](float v) { return lane_of<0x121>(v); });
+  if (n_chunks <= 2) join([](float v) { return lane_of<0x122>(v); });
+  if (n_chunks <= 4) join([](float v) { return lane_of<0x124>(v); });
+  if (n_chunks <= 8) join([](float v) { return lane_of<0x128>(v); });
+  if (n_chunks <= 16) join([](float v) { return __shfl_xor(v, 16, 64); });
+  if (n_chunks <= 32) join([](float v) { return __shfl_xor(v, 32, 64); });
   if (lane < n_chunks) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -433,10 +435,12 @@ __global__ void __launch_bounds__(kThreads)
   if (lane == 0) (col < d ? gq[col] : gk[col - d]) = s;
 }
 
-// workgroups that walk the rows of the backward: as many as the chip holds at once
+// Workgroups that walk the rows of the backward: as many as the chip holds at once (100,000 rows of 8 + 8 heads of 32 with
+// 512, 768, 1,024 of them: bfloat16 107, 90, 114 us, float32 158, 132, 129).
 constexpr int kBwdBlocks = 768, kBwdBlocksF32 = 1024;
 
-// Workgroups that few rows are spread over.  The backward's each write a part of the weight gradients.
+// Workgroups that few rows are spread over (1,536 rows of 8 + 8 heads of 32, forward over 128, 1,024, 2,048: float32 5.5,
+// 4.2, 4.7 us).  The backward's each write a part of the weight gradients (over 256 and 1,024: 12.9 and 16.5).
 constexpr int kFwdFill = 1024, kBwdFill = 256;
 
 // Threads per head (their binary logarithm) and rows per workgroup: enough items for a few

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// threads of a row: 4 logits each up to 256 groups, 16 beyond
+// threads of a row: 4 logits each up to 256 groups, 16 beyond, so that a row stays in a wave
 template <typename F>
 hipError_t pick_route(const RouteArgs& a, F&& f) {
   const int vpt = a.n_groups > 256 ? 16 : 4;
@@ -392,7 +392,8 @@ __global__ void __launch_bounds__(kThreads)
 
 // entries of a unit: whole blocks, at most 2,048 units (they are scanned group by group)
 int unit_run(int64_t n) { return (int)((n / 2048 + kBlock) / kBlock * kBlock); }
-// waves of the one workgroup, whose counters fit 64 KB of LDS
+// waves of the one workgroup, whose counters fit 64 KB of LDS (1,536 entries in one launch 5.5 us, in three 10.5; 8,192 in
+// 64 groups 11.4 and 14)
 int small_waves(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(kSmallWaves + 1, (n + kBlock - 1) / kBlock)); }
 size_t small_lds(int64_t n, int n_groups) { return (small_waves(n) + 1) * (size_t)(n_groups + 1) * sizeof(int); }
 bool is_small(int64_t n, int n_groups) { return small_waves(n) <= kSmallWaves && small_lds(n, n_groups) <= 65536 - 256; }
