@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   const bool bias = a.grad_bias && k0 == 0 && wm == 0;
   const T* zeros = reinterpret_cast<const T*>(kZeros);
   int next = 0;                            // the slot that this lane knows of the next step
+  // of a step that is there: an empty group has no last slot, and without slots `rows` may be NULL
   const auto numbers = [&](int t) {
     const int place = part.first + t * S + (lane & (S - 1));
     next = a.x_div || a.g_div ? slot_at(a.rows, min(place, end - 1), n) : 0;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
     sums.clear();
 #pragma unroll
     for (int j = 0; j < NB; ++j) colsum[j] = colall[j] = 0.f;
-    numbers(0);
+    if (steps > 0) numbers(0);
     walk<D, TA::Q + TB::Q>(steps, load, [&](int t, auto buffer) {
       multiply<T, TA, TB, MB, NB, far(), true>(buffers.a(buffer), buffers.b(buffer), wm, wn, lane, sums, colsum, bias);
       if ((t + 1) % (Sums<T, MB, NB>::kTurn / S) == 0) gather();

@@ -1,0 +1,66 @@
+"""Products by group on the GPU at the ends of what is declared: groups in front that no slot chooses, no
+slots at all, against the float64 reference.
+
+Tolerances (derived): as in test_gpu_grouped.py, u = 2^-24: a float32 sum of K products is off by at
+most (K + 16) u of the sum of their absolute values; bfloat16 outputs add one rounding.
+"""
+import numpy as np
+import pytest
+
+from oracle import blocks as ob
+from tests._blocks import DT, U, dev, f64, ints, near, same, torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tpc():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import tensor_product_convolution_amd as m
+    m.lib()
+    return m
+
+
+# slots, groups, in, out: weight gradients in tiles of 64, 64 in parts, 128 and (bfloat16) 256, and rows of any alignment
+SHAPES = [(300, 5, 64, 72), (3000, 3, 136, 64), (4096, 3, 512, 512), (600, 64, 512, 520), (130, 4, 33, 65),
+          (0, 5, 64, 72), (0, 256, 136, 136), (0, 3, 33, 65)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("kind", ["last", "upper", "none"])
+def test_groups_in_front_without_slots(tpc, kind, shape, dtype):
+    slots, groups, i, o = shape
+    r = np.random.default_rng(slots + groups)
+    low = {"last": groups - 1, "upper": groups // 2, "none": groups}[kind]
+    index = r.integers(low, groups + 1, size=slots) if kind == "none" else r.integers(low, groups, size=slots)
+    dt = DT[dtype]
+    x, w, gz = dev(r.normal(size=(slots, i)), dt), dev(r.normal(size=(groups, i, o)), dt), dev(r.normal(size=(slots, o)), dt)
+    g = tpc.group_rows(ints(index), groups)
+    ptr, rows = ob.group_rows(index, groups)
+    for x_rows, y_rows in (("source", "source"), ("grouped", "source"), ("source", "grouped")):
+        print(f"groups in front {kind} {dtype} {shape} {x_rows} {y_rows}", flush=True)
+        order = dict(x_rows=x_rows, y_rows=y_rows)
+        back = tpc.grouped_linear_backward(gz, x, w, g, want_bias=True, **order)
+        want = ob.grouped_backward(f64(gz), f64(x), f64(w), ptr, rows, 1, x_rows, y_rows)
+        size = ob.grouped_backward(np.abs(f64(gz)), np.abs(f64(x)), np.abs(f64(w)), ptr, rows, 1, x_rows, y_rows)
+        for got, ref, s, k, name in zip(back, want, size, (o, slots, slots), ("grad_x", "grad_w", "grad_bias")):
+            near(got, ref, (k + 16) * U * s, name, dtype)
+        assert (back[1][:min(low, groups)] == 0).all() and (back[2][:min(low, groups)] == 0).all()
+        assert same(back, tpc.grouped_linear_backward(gz, x, w, g, want_bias=True, **order))
+
+
+def test_an_infinity_behind_groups_without_slots(tpc):
+    """The second pass for infinite operands, next to groups that have nothing to pass over."""
+    r = np.random.default_rng(3)
+    x, gz = dev(r.normal(size=(200, 64))), dev(r.random(size=(200, 64)) + 0.5)
+    g = tpc.group_rows(ints(np.where(np.arange(200) < 150, 2, 3)), 4)
+    w = dev(np.zeros((4, 64, 64)))
+    clean = tpc.grouped_linear_backward(gz, x, w, g, want_x=False)[1]
+    x[7, 5] = float("inf")
+    bad = tpc.grouped_linear_backward(gz, x, w, g, want_x=False)[1]
+    assert (bad[:2] == 0).all() and torch.equal(bad[3], clean[3]) and (bad[2, 5] == float("inf")).all()
+    keep = torch.ones(64, dtype=torch.bool, device="cuda")
+    keep[5] = False
+    near(bad[2, keep], f64(clean[2, keep]), (200 + 16) * U * 150 * 8, "rows without it")
