@@ -413,7 +413,9 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int N = Chunk<T>::kN;
   const int64_t row = (int64_t)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
   if (row >= a.n_rows) return;
-  for (int c = (threadIdx.x % lanes) * N; c < a.n_cols; c += lanes * N) {
+  // unsigned: a row may be so long that the place behind it passes 2^31
+  for (uint32_t c = threadIdx.x % lanes * N; c < (uint32_t)a.n_cols; c += lanes * N) {
+    const int left = a.n_cols - (int)c;
     float s[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] = 0.f;
@@ -422,11 +424,11 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t slot = row * a.k + j;
       const float w = a.weight ? a.weight[slot] : 1.f;
       float v[N];
-      load_chunk((const T*)a.y + slot * a.n_cols + c, a.n_cols - c, v);
+      load_chunk((const T*)a.y + slot * a.n_cols + c, left, v);
 #pragma unroll
       for (int i = 0; i < N; ++i) s[i] = fmaf(w, v[i], s[i]);
     }
-    store_chunk((T*)a.out + row * a.n_cols + c, a.n_cols - c, s);
+    store_chunk((T*)a.out + row * a.n_cols + c, left, s);
   }
 }
 
@@ -440,16 +442,17 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t row = slot / a.k;
   const float w = a.weight[slot];
   float s = 0.f;
-  for (int c = (threadIdx.x % lanes) * N; c < a.n_cols; c += lanes * N) {
+  for (uint32_t c = threadIdx.x % lanes * N; c < (uint32_t)a.n_cols; c += lanes * N) {
+    const int left = a.n_cols - (int)c;
     float g[N], v[N];
-    load_chunk((const T*)a.go + row * a.n_cols + c, a.n_cols - c, g);
-    load_chunk((const T*)a.y + slot * a.n_cols + c, a.n_cols - c, v);
+    load_chunk((const T*)a.go + row * a.n_cols + c, left, g);
+    load_chunk((const T*)a.y + slot * a.n_cols + c, left, v);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       s = fmaf(g[i], v[i], s);
       g[i] *= w;
     }
-    store_chunk((T*)a.gy + slot * a.n_cols + c, a.n_cols - c, g);
+    store_chunk((T*)a.gy + slot * a.n_cols + c, left, g);
   }
   s = lanes_sum(s, lanes);
   if (threadIdx.x % lanes == 0) a.grad_weight[slot] = s;

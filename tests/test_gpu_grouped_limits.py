@@ -64,3 +64,17 @@ def test_an_infinity_behind_groups_without_slots(tpc):
     keep = torch.ones(64, dtype=torch.bool, device="cuda")
     keep[5] = False
     near(bad[2, keep], f64(clean[2, keep]), (200 + 16) * U * 150 * 8, "rows without it")
+
+
+def test_combine_of_the_longest_rows(tpc):
+    """The place behind a row's last chunk passes 2^31.  Only the last columns hold gradients, small whole
+    numbers, so that their sum is exact."""
+    c = 2 ** 31 - 1
+    y = torch.ones(1, c, device="cuda", dtype=torch.bfloat16)
+    y[0, -3000:] = torch.arange(3000, device="cuda").remainder(5).bfloat16()
+    assert torch.equal(tpc.combine_forward(y, dev([[1.0]])), y)
+    go = torch.zeros_like(y)
+    go[0, -3000:] = torch.arange(3000, device="cuda").remainder(3).bfloat16()
+    gy, gw = tpc.combine_backward(go, y, dev([[2.0]]))
+    assert torch.equal(gy[0, -5000:], 2 * go[0, -5000:]) and not gy[0, :5000].any()
+    assert float(gw) == float((go[0, -3000:].float() * y[0, -3000:].float()).sum())
