@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 
 #include "internal.hpp"
+#include "parts.hpp"
 #include "rows.hpp"
 #include "split.hpp"
 
@@ -109,7 +110,7 @@ struct Parts {
   int groups, n_groups, n, size, least, run, total;
   int first_slot, end_slot, before;        // of this lane's run; parts of the lanes below
   __device__ __forceinline__ int start(int e) const { return e <= n_groups ? min(max(ptr[e], 0), n) : n; }
-  __device__ __forceinline__ int count(int lo, int hi) const { return max(least, (max(hi - lo, 0) + size - 1) / size); }
+  __device__ __forceinline__ int count(int lo, int hi) const { return part_count(hi - lo, size, least); }
   // x plus that of the lanes `shift` below it in the same row of 16, or of the rows before
   template <int CONTROL, int ROWS>
   static __device__ __forceinline__ int add(int x) {

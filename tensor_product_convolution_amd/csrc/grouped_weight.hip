@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
   const int tile = blockIdx.x % tiles;
   const Part part = parts.at(blockIdx.x / tiles);
   const int k0 = tile / n_cols * B, c0 = tile % n_cols * B;
-  const int end = min(part.hi, part.first + size);
+  const int end = part_end(part.first, part.hi, size);
   const bool bias = a.grad_bias && k0 == 0;
   Sums<T, NB, NB> acc;
   acc.clear();
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 2)
   // tiles of a part on all dies: parts differ in length
   const int tile = blockIdx.x % tiles;
   const Part part = parts.at(blockIdx.x / tiles);
-  const int k0 = tile / n_cols * BM, c0 = tile % n_cols * BN, end = min(part.hi, part.first + size);
+  const int k0 = tile / n_cols * BM, c0 = tile % n_cols * BN, end = part_end(part.first, part.hi, size);
   const int wm = wave / WN, wn = wave % WN;
   const bool bias = a.grad_bias && k0 == 0 && wm == 0;
   const T* zeros = reinterpret_cast<const T*>(kZeros);
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kGemmThreads)
   const int lo = start(e), hi = start(e + 1);
   if (hi - lo <= size) return;
   const int64_t mat = (int64_t)a.k * a.cols, all = mat + (a.grad_bias ? a.cols : 0), pitch = mat + a.cols;
-  const int which = threadIdx.x / wide, parts = (hi - lo + size - 1) / size;
+  const int which = threadIdx.x / wide, parts = part_count(hi - lo, size, 1);
   for (int64_t i0 = (int64_t)blockIdx.x * wide * 4; i0 < all; i0 += (int64_t)gridDim.x * wide * 4) {
     const int64_t i = i0 + threadIdx.x % wide * 4;
     f4 s = {0.f, 0.f, 0.f, 0.f};

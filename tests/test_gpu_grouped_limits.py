@@ -78,3 +78,19 @@ def test_combine_of_the_longest_rows(tpc):
     gy, gw = tpc.combine_backward(go, y, dev([[2.0]]))
     assert torch.equal(gy[0, -5000:], 2 * go[0, -5000:]) and not gy[0, :5000].any()
     assert float(gw) == float((go[0, -3000:].float() * y[0, -3000:].float()).sum())
+
+
+def test_weight_gradient_of_the_most_slots(tpc):
+    """A group of nearly 2^31 slots, whose parts end past 2^31.  Only the first and last slots hold gradients;
+    the sums are whole numbers that bfloat16 holds."""
+    n, fan = 2 ** 31 - 5000, 8
+    g = tpc.group_rows(torch.zeros(n // fan, fan, dtype=torch.int32, device="cuda"), 1)
+    assert g.ptr.tolist() == [0, n] and int(g.rows[-1]) == n - 1
+    x, w = torch.ones(n // fan, 8, device="cuda", dtype=torch.bfloat16), torch.ones(1, 8, 8, device="cuda", dtype=torch.bfloat16)
+    gz = torch.zeros(n, 8, device="cuda", dtype=torch.bfloat16)
+    gz[:64], gz[-4000:] = 1, 1
+    x[-500:, 3] = 2
+    _, gw, gb = tpc.grouped_linear_backward(gz, x, w, g, want_x=False, want_bias=True)
+    want = torch.full((1, 8, 8), 4064.0, device="cuda")
+    want[:, 3] = 8064
+    assert torch.equal(gw.float(), want) and (gb == 4064).all()
