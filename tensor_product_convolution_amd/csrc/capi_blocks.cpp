@@ -209,7 +209,7 @@ tp_status tp_head_norm_rotate_backward(const tp_heads* h, const void* grad_qo, i
     b.gk_stride = gk_stride;
     b.grad_gamma_q = grad_gamma_q;
     b.grad_gamma_k = grad_gamma_k;
-    b.grad_pos = grad_pos;
+    b.grad_pos = h->n_rows > 0 ? grad_pos : nullptr;         // without rows pos and freq may be NULL
     b.part = static_cast<float*>(ws);
     return launched(me, heads_backward(h->dtype, b));
   });
