@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
           s2 = fmaf(h[j] * g[j], v[j], s2);
         }
         r = 1.f / sqrtf(head_sum(s1, a.lg) * part + a.eps);
+        r = has ? r : 0.f;                 // eps may be 0, and zeros would be no numbers then
         m = head_sum(s2, a.lg) * r * part;
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] *= r;

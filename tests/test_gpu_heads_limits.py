@@ -7,6 +7,7 @@ import pytest
 
 from oracle import blocks as ob
 from tests._blocks import DT, U, dev, f64, ints, near, same, torch
+from tests.test_gpu_heads import check, problem
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,15 @@ def test_no_rows_and_no_frequencies(tpc, code):
                                                   torch.cuda.current_stream().cuda_stream) == 0
     torch.cuda.synchronize()
     assert (out == 0).all() and (pos == 5).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 1, 16, 8, 3, 0), (33, 4, 2, 16, 8, 3, 0), (130, 3, 5, 40, 12, 2, 0), (700, 5, 1, 24, 0, 0, 0)], ids=str)
+def test_eps_zero(tpc, dtype, shape):
+    """No head is zero, but the last turn of a workgroup has threads without a head."""
+    s = problem(*shape[:6], dtype, True, 0)
+    kw = dict(s["kw"], eps=0.0)
+    want_pos = shape[4] > 0
+    fwd = tpc.head_norm_rotate_forward(s["q"], s["k"], **kw)
+    back = tpc.head_norm_rotate_backward(s["gq"], s["gk"], s["q"], s["k"], want_pos=want_pos, **kw)
+    check(s, False, 0.0, dtype, fwd, back)
