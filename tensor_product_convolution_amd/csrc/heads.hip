@@ -108,27 +108,24 @@ __device__ __forceinline__ float2 turn_of(const HeadArgs& a, int64_t row, int i)
   return make_float2(c, s);
 }
 
-// The angles of a block of rows, the rows' pairs filled up to whole chunks with pairs that do not turn; so is the
-// chunk behind them all, which serves the rest of a head.
+// The angles of a block of rows, the rows' pairs filled up to whole chunks with pairs that do not turn.
 template <typename T>
 struct Angles {
   static constexpr int N = Chunk<T>::kN;
-  float2* cs;                              // [kTrig + N]
-  int pitch, at, by;                       // of a row; this thread's chunk in row r: at + r by
+  float2* cs;                              // [kTrig]
+  int pitch, at;                           // of a row; this thread's chunk in row r: at + r pitch, where it turns
   __device__ __forceinline__ Angles(const HeadArgs& a, float2* cs, int pair) : cs(cs) {
     pitch = (a.pairs + N - 1) / N * N;
-    at = pair < 0 ? kTrig : pair;
-    by = pair < 0 ? 0 : pitch;
+    at = pair;
   }
   __device__ __forceinline__ void fill(const HeadArgs& a, int64_t row0, int rows) const {
-    if (threadIdx.x < N) cs[kTrig + threadIdx.x] = make_float2(1.f, 0.f);
     for (int i = threadIdx.x; i < rows * pitch; i += kThreads) {
       const int row = i / pitch, pair = i - row * pitch;
       cs[i] = pair < a.pairs ? turn_of(a, row0 + row, pair) : make_float2(1.f, 0.f);
     }
   }
   __device__ __forceinline__ void get(int row, float2* o) const {
-    const float4* from = reinterpret_cast<const float4*>(cs + at + row * by);
+    const float4* from = reinterpret_cast<const float4*>(cs + at + row * pitch);
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
       const float4 t = from[j / 2];
@@ -168,7 +165,7 @@ template <typename T, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads)
     k_heads_fwd(HeadArgs a) {
   constexpr int V = 2 * Chunk<T>::kN;
-  __shared__ __attribute__((aligned(16))) float2 cs[kTrig + Chunk<T>::kN];
+  __shared__ __attribute__((aligned(16))) float2 cs[kTrig];
   const Chunks<T, INTER> c((int)threadIdx.x & ((1 << a.lg) - 1), a.d, a.pairs);
   const Angles<T> angles(a, cs, c.pair);
   const float part = 1.f / (float)a.d;
@@ -215,13 +212,15 @@ __global__ void __launch_bounds__(kThreads)
       for (int j = 0; j < V; ++j) v[j] = v[j] * r * (key ? g[1][j] : g[0][j]);
     }
     if (!has) continue;
-    float2 t[V / 2];
-    angles.get(it.row, t);
+    if (c.pair >= 0) {                     // no turn by nothing for the rest: it would pass on what is not finite
+      float2 t[V / 2];
+      angles.get(it.row, t);
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      const float p = v[c.first(j)], q = v[c.second(j)];
-      v[c.first(j)] = p * t[j].x - q * t[j].y;
-      v[c.second(j)] = p * t[j].y + q * t[j].x;
+      for (int j = 0; j < V / 2; ++j) {
+        const float p = v[c.first(j)], q = v[c.second(j)];
+        v[c.first(j)] = p * t[j].x - q * t[j].y;
+        v[c.second(j)] = p * t[j].y + q * t[j].x;
+      }
     }
     store_pairs(it.head < a.hq ? (T*)a.q_out + (row0 + it.row) * a.qo_stride + it.head * a.d
                                : (T*)a.k_out + (row0 + it.row) * a.ko_stride + (it.head - a.hq) * a.d,
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
     k_heads_bwd(HeadBwdArgs b) {
   const HeadArgs& a = b.f;
   constexpr int V = 2 * Chunk<T>::kN;
-  __shared__ __attribute__((aligned(16))) float2 cs[kTrig + Chunk<T>::kN];     // at the end the waves' weight gradients
+  __shared__ __attribute__((aligned(16))) float2 cs[kTrig];     // at the end the waves' weight gradients
   extern __shared__ __attribute__((aligned(16))) float lds[];
   const int n_chunks = 1 << a.lg, lane_c = (int)threadIdx.x & (n_chunks - 1), heads = a.hq + a.hk, per_axis = a.rows * heads;
   float *gl = lds, *fl = gl + (NORM ? 2 * n_chunks * V : 0), *sums = fl + (POS ? kMaxAxes * n_chunks * V / 2 : 0);
@@ -316,13 +315,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
       } else {
         begin(std::integral_constant<int, 0>(), row0 + (int64_t)gridDim.x * a.rows);
       }
-      float2 t[V / 2];
-      angles.get(has ? r0 : 0, t);
+      if (c.pair >= 0) {
+        float2 t[V / 2];
+        angles.get(has ? r0 : 0, t);
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float p = h[c.first(j)], q = h[c.second(j)];
-        h[c.first(j)] = fmaf(p, t[j].x, q * t[j].y);
-        h[c.second(j)] = fmaf(q, t[j].x, -p * t[j].y);
+        for (int j = 0; j < V / 2; ++j) {
+          const float p = h[c.first(j)], q = h[c.second(j)];
+          h[c.first(j)] = fmaf(p, t[j].x, q * t[j].y);
+          h[c.second(j)] = fmaf(q, t[j].x, -p * t[j].y);
+        }
       }
       const float* g = gl + (KEY * n_chunks + lane_c) * V;
       float r = 1.f, m = 0.f;
@@ -341,12 +342,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 4 : 3)
       }
       if (POS) {                           // of the angles, from the pairs before they are turned
         float w[kMaxAxes] = {0.f, 0.f, 0.f};
+        if (c.pair >= 0) {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const int p = c.first(j), q = c.second(j);
-          const float gt = NORM ? h[q] * (v[p] * g[p]) - h[p] * (v[q] * g[q]) : h[q] * v[p] - h[p] * v[q];
+          for (int j = 0; j < V / 2; ++j) {
+            const int p = c.first(j), q = c.second(j);
+            const float gt = NORM ? h[q] * (v[p] * g[p]) - h[p] * (v[q] * g[q]) : h[q] * v[p] - h[p] * v[q];
 #pragma unroll
-          for (int k = 0; k < kMaxAxes; ++k) w[k] += gt * fl[(k * n_chunks + lane_c) * (V / 2) + j];
+            for (int k = 0; k < kMaxAxes; ++k) w[k] += gt * fl[(k * n_chunks + lane_c) * (V / 2) + j];
+          }
         }
 #pragma unroll
         for (int k = 0; k < kMaxAxes; ++k) {

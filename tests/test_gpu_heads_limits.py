@@ -45,3 +45,38 @@ def test_eps_zero(tpc, dtype, shape):
     fwd = tpc.head_norm_rotate_forward(s["q"], s["k"], **kw)
     back = tpc.head_norm_rotate_backward(s["gq"], s["gk"], s["q"], s["k"], want_pos=want_pos, **kw)
     check(s, False, 0.0, dtype, fwd, back)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_bad_value_that_does_not_turn_stays_alone(tpc, dtype, interleaved, norm, bad):
+    """Values behind the turned pairs reach neither each other nor the positions' gradient, but for the
+    norm of their head."""
+    s = problem(40, 3, 2, 40, 11, 2, dtype, norm, 0)
+    kw = dict(s["kw"], interleaved=interleaved)
+    run = lambda: tpc.head_norm_rotate_forward(s["q"], s["k"], **kw)
+    back = lambda: tpc.head_norm_rotate_backward(s["gq"], s["gk"], s["q"], s["k"], want_pos=True, **kw)
+    clean, clean_back = run(), back()
+    s["gq"][7, 1, 33], s["gk"][9, 0, 22] = bad, bad
+    got = back()
+    assert torch.equal(got[4], clean_back[4])
+    if norm:
+        for g, c, at in ((got[2], clean_back[2], 33), (got[3], clean_back[3], 22)):
+            keep = torch.arange(40, device="cuda") != at
+            assert torch.equal(g[keep], c[keep]) and not torch.isfinite(g[at])
+    else:
+        for g, c, at in ((got[0], clean_back[0], (7, 1, 33)), (got[1], clean_back[1], (9, 0, 22))):
+            want = c.clone()
+            want[at] = bad
+            assert torch.equal(g.nan_to_num(nan=5e30, posinf=6e30), want.nan_to_num(nan=5e30, posinf=6e30))
+    s["q"][4, 2, 30], s["k"][5, 1, 39] = bad, bad
+    for g, c, at in zip(run(), clean, ((4, 2, 30), (5, 1, 39))):
+        want = c.clone()
+        if norm:                           # 1 / sqrt of infinity is 0
+            want[at[:2]] = 0 if bad == float("inf") else float("nan")
+            want[at] = float("nan")
+        else:
+            want[at] = bad
+        assert torch.equal(g.nan_to_num(nan=5e30, posinf=6e30), want.nan_to_num(nan=5e30, posinf=6e30))
