@@ -9,8 +9,7 @@
 // Bound by HBM: q and k are read once and written once.  A few threads hold a head, each
 // the two values of up to 4 (float32) or 8 (bfloat16) pairs, so that pairs need no exchange in
 // either layout.  The angles of a block of rows are taken once, into LDS, and
-// serve all heads: turns in 64 bits, so that far positions keep their angle, and only the
-// fraction of a turn goes on in 32.
+// serve all heads: turns in 64 bits, so that far positions keep their angle.
 // 100,000 rows of 16 + 4 heads of 64, 24 pairs, bfloat16: 115 us (512 MB, 4.5 TB/s; a large copy reaches 5.1);
 // float32 204 (5.0 TB/s).  1,536 rows of 8 + 8 heads of 32: 5 us, most of it the launch.
 #include <algorithm>
@@ -94,7 +93,7 @@ __device__ __forceinline__ void load_like(const float* w, const Chunks<T, INTER>
   for (int i = 0; i < 2 * N; i += 4) load_chunk(w + c.at[i / N] + i % N, c.left[i / N] - i % N, v + i);
 }
 
-// cos and sin of a row's angle i.  Whole turns are taken off in 64 bits.
+// cos and sin of a row's angle i: the angle in 64 bits, its functions in 32.
 __device__ __forceinline__ float2 turn_of(const HeadArgs& a, int64_t row, int i) {
   double t = 0.0;
   for (int x = 0; x < a.axes; ++x) {
@@ -103,9 +102,12 @@ __device__ __forceinline__ float2 turn_of(const HeadArgs& a, int64_t row, int i)
     t = fma(p, a.freq[(int64_t)i * a.axes + x], t);
   }
   t *= 0.15915494309189533577;             // 1 / (2 pi)
+  t -= rint(t);
+  const float f = (float)t;                // off by up to 2^-26 turns, 1.6 u of a radian: turned by the rest as well
+  const float rest = (float)(t - (double)f) * 6.2831853071795865f;
   float s, c;
-  sincospif(2.f * (float)(t - rint(t)), &s, &c);
-  return make_float2(c, s);
+  sincospif(2.f * f, &s, &c);
+  return make_float2(fmaf(-s, rest, c), fmaf(c, rest, s));
 }
 
 // The angles of a block of rows, the rows' pairs filled up to whole chunks with pairs that do not turn.

@@ -80,3 +80,26 @@ def test_a_bad_value_that_does_not_turn_stays_alone(tpc, dtype, interleaved, nor
         else:
             want[at] = bad
         assert torch.equal(g.nan_to_num(nan=5e30, posinf=6e30), want.nan_to_num(nan=5e30, posinf=6e30))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_small_sines_and_cosines(tpc, interleaved):
+    """Angles within 1.3e-3 of half and quarter turns, where a sine or cosine is small: an angle rounded to
+    float32 behind its whole turns would leave it 1e-7 off.
+
+    Tolerance (derived): sine and cosine of the rounded angle to 4 units in the last place (8 u), the
+    correction for its rounding and the sum two more: 16 u of each; the angle in 64 bits is off by 3 2^-53 of the
+    turns before it, at most 1,000: 2 pi 1,000 3 2^-53 = 2.1e-12."""
+    r = np.random.default_rng(4)
+    n = 120
+    part = np.repeat([0.5, 0.25, -0.25, 0.0], n // 4) + r.uniform(-2e-4, 2e-4, size=n)
+    turns = np.where(np.arange(n) % 2, r.integers(-1000, 1000, size=n), 0) + part
+    freq = torch.tensor(2 * np.pi * turns[:, None], device="cuda")
+    x = torch.zeros(1, 1, 2 * n, device="cuda")
+    a, b = ob.pair_places(n, interleaved)
+    x[..., torch.as_tensor(a)] = 1.0
+    pos = torch.ones(1, 1, device="cuda")
+    out = f64(tpc.head_norm_rotate_forward(x, x.clone(), pos=pos, freq=freq, interleaved=interleaved)[0])[0, 0]
+    t = f64(freq)[:, 0]
+    for got, want in ((out[a], np.cos(t)), (out[b], np.sin(t))):
+        assert (np.abs(got - want) <= 16 * U * np.abs(want) + 2.1e-12).all(), np.abs(got - want).max()
