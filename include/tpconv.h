@@ -863,7 +863,7 @@ tp_status tp_grouped_linear_forward(const tp_grouped* g, const void* x, int64_t 
 tp_status tp_grouped_linear_workspace(const tp_grouped* g, int32_t want_x, int32_t want_w, size_t* bytes);
 
 /* Backward from grad_z, the gradient of z (y's rows; of y itself without an activation):
- *   grad_x = grad_z w^T, summed over the slots of a source row (each slot's part rounded to T first);
+ *   grad_x = grad_z w^T, summed over the slots of a source row (in float32, rounded once);
  *            times silu'(pre) where pre is given: x = silu(pre), pre with x's rows (fan 1 or grouped
  *            rows), so that grad_x is the grad_z of the product in front
  *   grad_w[e] = sum over the group's slots of x^T grad_z,  grad_bias[e] = sum of grad_z

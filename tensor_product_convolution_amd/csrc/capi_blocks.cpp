@@ -109,7 +109,7 @@ tp_status check_grouped_pointers(const char* where, const tp_grouped& g, bool we
 
 bool summed(const tp_grouped& g) { return g.x_rows == TP_ROWS_SOURCE && g.fan > 1; }
 size_t grad_x_bytes(const tp_grouped& g) {
-  return summed(g) ? ((size_t)g.n_slots * g.n_in * size_of(g.dtype) + 15) / 16 * 16 : 0;
+  return summed(g) ? ((size_t)g.n_slots * g.n_in * sizeof(float) + 15) / 16 * 16 : 0;
 }
 size_t grad_w_bytes(const tp_grouped& g) { return grouped_weight_workspace(g.dtype, g.n_slots, g.n_groups, g.n_in, g.n_out); }
 
@@ -400,7 +400,8 @@ tp_status tp_grouped_linear_backward(const tp_grouped* g, const void* grad_z, in
     a.k = g->n_out;
     a.cols = g->n_in;
     a.transposed = true;
-    a.c = summed(*g) ? ws : grad_x;
+    a.c = summed(*g) ? ws : grad_x;        // the slots' parts are float32: rounded once, as their sum
+    a.wide = summed(*g);
     a.ldc = summed(*g) ? g->n_in : gx_stride;
     a.pre = pre;
     a.ldpre = pre_stride;
@@ -411,6 +412,7 @@ tp_status tp_grouped_linear_backward(const tp_grouped* g, const void* grad_z, in
     c.n_rows = n / g->fan;
     c.k = g->fan;
     c.n_cols = g->n_in;
+    c.wide = true;
     c.y = ws;
     c.out = grad_x;
     c.stream = stream;

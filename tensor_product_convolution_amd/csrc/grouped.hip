@@ -120,7 +120,10 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
           if (a.pre_out) ((T*)a.pre_out)[row * a.ldc + col] = z;
           v = silu((float)z);
         }
-        ((T*)a.c)[row * a.ldc + col] = (T)v;
+        if (ALONG && a.wide)
+          ((float*)a.c)[row * a.ldc + col] = v;
+        else
+          ((T*)a.c)[row * a.ldc + col] = (T)v;
       }
   }
 }
@@ -248,7 +251,10 @@ __global__ void __launch_bounds__(64 * WM * WN * KS, 2)
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
     }
-    store8((T*)a.c + row * a.ldc + col, left, v);
+    if (ALONG && a.wide)
+      store8((float*)a.c + row * a.ldc + col, left, v);
+    else
+      store8((T*)a.c + row * a.ldc + col, left, v);
   });
 }
 

@@ -293,6 +293,7 @@ struct CombineArgs {
   int dtype = TP_F32;
   int64_t n_rows = 0;
   int k = 0, n_cols = 0;
+  bool wide = false;                              // forward: y is float32 whatever the type
   const void *y = nullptr, *go = nullptr;
   const float* weight = nullptr;                  // null: 1
   void *out = nullptr, *gy = nullptr;
@@ -311,6 +312,7 @@ struct GroupedArgs {
   int a_div = 0, c_div = 0;
   int k = 0, cols = 0;                            // contraction, columns of c
   bool transposed = false;                        // w is [n_groups][cols][k], not [k][cols]
+  bool wide = false;                              // transposed: c is float32 whatever the type
   void *c = nullptr, *pre_out = nullptr;          // pre_out: before the activation, rows of c
   const void* pre = nullptr;                      // c is multiplied by the activation's slope here; rows of c
   int64_t ldpre = 0;

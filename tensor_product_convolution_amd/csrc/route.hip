@@ -407,7 +407,8 @@ int combine_lanes(int n_cols, int per) {
   return lanes;
 }
 
-template <typename T>
+// Y: type of y
+template <typename T, typename Y>
 __global__ void __launch_bounds__(kThreads)
     k_combine_fwd(CombineArgs a, int lanes) {
   constexpr int N = Chunk<T>::kN;
@@ -424,7 +425,8 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t slot = row * a.k + j;
       const float w = a.weight ? a.weight[slot] : 1.f;
       float v[N];
-      load_chunk((const T*)a.y + slot * a.n_cols + c, left, v);
+#pragma unroll
+      for (int i = 0; i < N; i += Chunk<Y>::kN) load_chunk((const Y*)a.y + slot * a.n_cols + c + i, left - i, v + i);
 #pragma unroll
       for (int i = 0; i < N; ++i) s[i] = fmaf(w, v[i], s[i]);
     }
@@ -501,14 +503,14 @@ hipError_t group_rows(const int32_t* index, int64_t n, int n_groups, int32_t* pt
 }
 
 hipError_t combine_forward(const CombineArgs& a) {
-  const auto go = [&](auto t) {
+  const auto go = [&](auto t, auto y) {
     const int lanes = combine_lanes(a.n_cols, Chunk<decltype(t)>::kN);
     const int64_t blocks = (a.n_rows + kThreads / lanes - 1) / (kThreads / lanes);
     if (blocks > 0xffffffffLL / kThreads) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((k_combine_fwd<decltype(t)>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, lanes);
+    hipLaunchKernelGGL((k_combine_fwd<decltype(t), decltype(y)>), dim3((unsigned)blocks), dim3(kThreads), 0, a.stream, a, lanes);
     return hipGetLastError();
   };
-  return a.dtype == TP_F32 ? go(float()) : go(bf16_t());
+  return a.dtype == TP_F32 ? go(float(), float()) : a.wide ? go(bf16_t(), float()) : go(bf16_t(), bf16_t());
 }
 
 hipError_t combine_backward(const CombineArgs& a) {

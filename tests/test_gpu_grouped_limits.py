@@ -94,3 +94,29 @@ def test_weight_gradient_of_the_most_slots(tpc):
     want = torch.full((1, 8, 8), 4064.0, device="cuda")
     want[:, 3] = 8064
     assert torch.equal(gw.float(), want) and (gb == 4064).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [(600, 5, 64, 72, 2), (3000, 7, 136, 512, 3), (4096, 4, 33, 65, 16), (64, 32, 128, 256, 4),
+                                  (70000, 3, 264, 256, 2), (33000, 2, 2056, 264, 2)], ids=str)
+def test_gradient_of_rows_of_several_slots(tpc, case, dtype):
+    """The slots' parts are summed in float32 and rounded once.  They come in pairs that all but cancel."""
+    slots, groups, i, o, fan = case
+    print(f"several slots {dtype} {case}", flush=True)
+    r = np.random.default_rng(slots + fan)
+    dt = DT[dtype]
+    index = r.integers(0, groups, size=(slots // fan, fan))
+    index[:, 1] = index[:, 0]
+    n = index.size
+    g = tpc.group_rows(ints(index), groups)
+    ptr, rows = ob.group_rows(index, groups)
+    gz = r.normal(size=(n // fan, fan, o))
+    gz[:, 1] = -gz[:, 0] + 0.01 * gz[:, 1]
+    if fan > 2:
+        gz[:, 2:] *= 0.01
+    gz, w = dev(gz.reshape(n, o), dt), dev(r.normal(size=(groups, i, o)), dt)
+    x = dev(np.zeros((n // fan, i)), dt)
+    got = tpc.grouped_linear_backward(gz, x, w, g, want_w=False)[0]
+    want = ob.grouped_backward(f64(gz), f64(x), f64(w), ptr, rows, fan, "source", "source")[0]
+    size = ob.grouped_backward(np.abs(f64(gz)), f64(x), np.abs(f64(w)), ptr, rows, fan, "source", "source")[0]
+    near(got, want, (o + 16 + fan) * U * size, "grad_x", dtype)
