@@ -854,8 +854,8 @@ typedef struct {
 } tp_grouped;
 
 /* z_s = x_row(s) w[e(s)] + bias[e(s)] (bias T [n_groups][n_out] or NULL), y = act(z).  With
- * TP_ACT_SILU, y = z / (1 + exp(-z)) of z rounded to T, and z is written to pre (NULL: not; y's rows and
- * stride).  Outputs must not overlap inputs. */
+ * TP_ACT_SILU, y = z / (1 + exp(-z)) of z rounded to T (0 below z = -87.3), and z is written to pre (NULL: not;
+ * y's rows and stride).  Outputs must not overlap inputs. */
 tp_status tp_grouped_linear_forward(const tp_grouped* g, const void* x, int64_t x_stride, const void* bias,
                                     int32_t act, void* y, int64_t y_stride, void* pre, hipStream_t stream);
 

@@ -114,11 +114,11 @@ __global__ void __launch_bounds__(kGemmThreads, 2)
         const int row = crow[wm * WM + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + r % 4];
         if (row < 0) continue;
         float v = acc.total(i, j)[r] + bias;
-        if (a.pre) v = none ? 0.f : v * silu_slope((float)((const T*)a.pre)[row * a.ldpre + col]);
+        if (a.pre) v = none ? 0.f : v * silu_slope<T>((float)((const T*)a.pre)[row * a.ldpre + col]);
         if (a.act) {
           const T z = (T)v;                // the activation is that of the stored value
           if (a.pre_out) ((T*)a.pre_out)[row * a.ldc + col] = z;
-          v = silu((float)z);
+          v = silu<T>((float)z);
         }
         if (ALONG && a.wide)
           ((float*)a.c)[row * a.ldc + col] = v;
@@ -242,14 +242,14 @@ __global__ void __launch_bounds__(64 * WM * WN * KS, 2)
       float z[8];
       load8((const T*)a.pre + row * a.ldpre + col, left, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = none ? 0.f : v[j] * silu_slope(z[j]);
+      for (int j = 0; j < 8; ++j) v[j] = none ? 0.f : v[j] * silu_slope<T>(z[j]);
     }
     if (a.act) {                           // the activation is that of the stored value
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = (float)(T)v[j];
       if (a.pre_out) store8((T*)a.pre_out + row * a.ldc + col, left, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
+      for (int j = 0; j < 8; ++j) v[j] = silu<T>(v[j]);
     }
     if (ALONG && a.wide)
       store8((float*)a.c + row * a.ldc + col, left, v);

@@ -193,15 +193,38 @@ __device__ __forceinline__ void place_tile(int t, int rows, int cols, int& r, in
   c = in / high;
 }
 
-// exp and reciprocal to a unit in the last place each: 4 u of a value, where the product in front is
-// off by more; at z = -88 and below the sigmoid is 0
-__device__ __forceinline__ float sigmoid(float z) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+// The sigmoid s of z and 1 - s, from exp(-|z|), so that both are right relatively; exp and reciprocal to a unit in the
+// last place.  float32: what the product by log2(e) loses goes on as a factor, 10 u of s in all (without it 0.75 |z| u
+// more, 57 u at -50).  Below z = -87.3 the sigmoid is 0.
+template <typename T>
+struct Sigmoid {
+  float s, rest;
+  __device__ __forceinline__ explicit Sigmoid(float z) {
+    constexpr float kLog2E = 0x1.715476p+0f, kMore = 0x1.4ae0cp-26f, kLn2 = 0.69314718f;    // log2(e) in two pieces
+    const float a = fminf(fabsf(z), 100.f), t = a * -kLog2E, lost = fmaf(a, -kMore, fmaf(a, -kLog2E, -t));
+    const float e = __builtin_amdgcn_exp2f(t) * fmaf(lost, kLn2, 1.f), q = __builtin_amdgcn_rcpf(1.f + e);
+    s = z < 0.f ? e * q : q;
+    rest = z < 0.f ? q : e * q;
+  }
+};
+// bfloat16: s to (0.75 |z| + 4) u of itself, 1 - s to 4 u of 1, far below the 2^16 u of the results' rounding; the other
+// form would be twice the instructions of the activation, which nothing covers in a large tile.
+template <>
+struct Sigmoid<bf16_t> {
+  float s, rest;
+  __device__ __forceinline__ explicit Sigmoid(float z) {
+    s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+    rest = 1.f - s;
+  }
+};
+template <typename T>
+__device__ __forceinline__ float silu(float z) {
+  return z * Sigmoid<T>(z).s;
 }
-__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
+template <typename T>
 __device__ __forceinline__ float silu_slope(float z) {
-  const float s = sigmoid(z);
-  return s * (1.f + z * (1.f - s));
+  const Sigmoid<T> g(z);
+  return g.s * (1.f + z * g.rest);
 }
 
 // ---- the fast path: operands straight to LDS --------------------------------------------

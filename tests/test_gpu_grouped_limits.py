@@ -120,3 +120,34 @@ def test_gradient_of_rows_of_several_slots(tpc, case, dtype):
     want = ob.grouped_backward(f64(gz), f64(x), f64(w), ptr, rows, fan, "source", "source")[0]
     size = ob.grouped_backward(np.abs(f64(gz)), f64(x), np.abs(f64(w)), ptr, rows, fan, "source", "source")[0]
     near(got, want, (o + 16 + fan) * U * size, "grad_x", dtype)
+
+
+@pytest.mark.parametrize("width", [1, 4])
+def test_activation_and_its_slope_are_right_relatively(tpc, width):
+    """Float32, from z = -87, below which the sigmoid's exponential underflows, to 60.
+
+    Tolerance (derived): exponential and reciprocal to a unit in the last place (2 u) each, the argument's
+    remainder, two sums and three products u each: 10 u of the value; the slope s (1 + z (1 - s)) twice
+    that of its absolute terms."""
+    r = np.random.default_rng(6)
+    n = 4000
+    z = np.r_[np.linspace(-87, 60, n - 1000), r.uniform(-4, 4, size=999), 0.0]
+    x = np.zeros((n, width))
+    x[:, 0] = z
+    x, w = dev(x), torch.eye(width, device="cuda").view(1, width, width).contiguous()
+    g = tpc.group_rows(ints(np.zeros(n)), 1)
+    y, pre = tpc.grouped_linear_forward(x, w, g, act="silu", want_pre=True)
+    z = f64(x[:, 0])
+    assert np.array_equal(f64(pre[:, 0]), z)
+    s, rest = 1 / (1 + np.exp(-z)), 1 / (1 + np.exp(z))
+    off = np.abs(f64(y[:, 0]) - z * s) / np.maximum(np.abs(z * s), 1e-37)
+    assert off.max() < 10 * U, (off.max() / U, z[off.argmax()])
+    one = torch.ones(n, width, device="cuda")
+    slope = f64(tpc.grouped_linear_backward(one, x, w, g, pre=x, want_w=False)[0][:, 0])
+    off = np.abs(slope - s * (1 + z * rest)) / (s * (1 + np.abs(z) * rest))
+    assert off.max() < 20 * U, (off.max() / U, z[off.argmax()])
+    # what is not finite: infinities of z keep their limit or are no number, as z / (1 + exp(-z)) is
+    bad = dev([[float("inf")] + [0.0] * (width - 1), [float("nan")] + [0.0] * (width - 1)])
+    if width == 1:
+        got = tpc.grouped_linear_forward(bad, w, tpc.group_rows(ints([0, 0]), 1), act="silu")
+        assert float(got[0, 0]) == float("inf") and torch.isnan(got[1, 0])
