@@ -889,7 +889,8 @@ tp_status tp_combine_backward(int32_t dtype, int64_t n_rows, int32_t k, int32_t 
  *   m = beta1 m + (1 - beta1) G,  v = beta2 v + (1 - beta2) G^2
  *   p = p (1 - lr decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
  * Where max_norm is given (+inf: only the norm is taken) and the norm is not finite, the step changes
- * nothing but *norm.  Without it a gradient that is not finite reaches its parameter and state.
+ * nothing but *norm.  Without it a gradient that is not finite reaches its parameter and state; a state of 8 bits,
+ * which has no code for it, begins anew with 0.
  *
  * States lie in arrays over all tensors, each tensor from a multiple of 256 values on, in order; what
  * lies between holds zeros.  bits 32: float32.  bits 8: one byte a value, and a float32 unit for

@@ -17,7 +17,8 @@
 // 255 (2^33).  A moment moves by a tenth or a thousandth of its distance a step, far below half
 // a code, and rounding to nearest would hold it where it is: codes are rounded up or down at random, by
 // 16 bits each of the generator's word for the value (word i % 4 of block i / 4, key seed, offset
-// t), so that the mean is right.  A second moment that is not zero keeps code 1 at least:
+// t), so that the mean is right.  A gradient that is not finite (where no norm is taken) leaves zeros: nothing of it may
+// reach the 255 others through the unit.  A second moment that is not zero keeps code 1 at least:
 // the update would be divided by nothing.  Which code is taken is decided in 64 bits.
 #include <algorithm>
 
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint2 mc = *reinterpret_cast<const uint2*>(m + state), vc = *reinterpret_cast<const uint2*>(v + state);
   const double mu = (double)m_unit[block], vu = (double)v_unit[block];
   double x[kValues], y[kValues], top_x = 0.0, top_y = 0.0;
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < kValues; ++j) {
     const double w = (double)g[j] * s.factor;
@@ -270,6 +272,17 @@ __global__ void __launch_bounds__(kThreads)
     top_x = fmax(top_x, fabs(x[j]));
     top_y = fmax(top_y, y[j]);
     p[j] = moved(p[j], (float)x[j], (float)y[j], e.decay, s, b.eps);
+    bad |= !(fabsf(g[j]) < INFINITY);
+  }
+  if (bad) {
+    top_x = top_y = 0.0;
+#pragma unroll
+    for (int j = 0; j < kValues; ++j) {
+      // no code stands for what is not finite, and its block's others go on
+      if (!(fabsf(g[j]) < INFINITY)) x[j] = y[j] = 0.0;
+      top_x = fmax(top_x, fabs(x[j]));
+      top_y = fmax(top_y, y[j]);
+    }
   }
   // rounding does not change which is the largest
   const float ux = block_max((float)(top_x * (1.0 / 1.875))), uy = block_max((float)(top_y * (1.0 / 1.875)));
