@@ -894,7 +894,7 @@ tp_status tp_combine_backward(int32_t dtype, int64_t n_rows, int32_t k, int32_t 
  *
  * States lie in arrays over all tensors, each tensor from a multiple of 256 values on, in order; what
  * lies between holds zeros.  bits 32: float32.  bits 8: one byte a value, and a float32 unit for
- * each 256: value = unit x code's value, unit = max / 1.875 (rounded to float32); code c of a second
+ * each 256: value = unit x code's value, unit = max / 1.875 (rounded to float32, at most 2^127); code c of a second
  * moment (0..255): c 2^-33 below 8, else 2^(c / 8 - 31) (1 + c % 8 / 8); of a first moment
  * bit 7 is the sign and c = code & 127: c 2^-17 below 8, else 2^(c / 8 - 15) (1 + c % 8 / 8).  A
  * value between two codes takes the upper one where its share of the way plus u / 65536 reaches
@@ -920,7 +920,7 @@ typedef struct {
   void *m, *v;               /* device: float32, or uint8 where bits is 8 */
   float *m_unit, *v_unit;    /* device, bits 8: [state_values / 256] */
   double beta1, beta2;       /* [0, 1) */
-  double eps, lr, max_norm;  /* eps, max_norm >= 0 */
+  double eps, lr, max_norm;  /* eps, max_norm >= 0; an eps below 2^-126 but for 0 counts as 2^-126 */
   const float* lr_at;        /* device: the rate is read there; NULL: lr */
   uint64_t seed;
   void* scalars;             /* device, 64 bytes, zeros before the first step; the first 8 are t */

@@ -159,7 +159,7 @@ def decode(codes, units, second):
 def encode(x, second, u):
     """(codes, units) of values x; u [0, 1) of each."""
     x = _f(x)
-    units = (np.abs(x).reshape(-1, BLOCK).max(1) / 1.875).astype(np.float32)
+    units = np.minimum(np.abs(x).reshape(-1, BLOCK).max(1) / 1.875, 2.0 ** 127).astype(np.float32)
     wide = np.repeat(_f(units), BLOCK)
     a = np.divide(np.abs(x), wide, out=np.zeros_like(x), where=wide > 0)
     v = code_values(second)

@@ -11,7 +11,7 @@
 // the norm and 230 for the step (16 bytes a value, 4.5 TB/s, vector instructions for 0.8 of it); 300,000 values in
 // 40 tensors, 32-bit states: 8 and 4 us.
 //
-// 8-bit states: 256 values share a float32 unit, the largest of them over 1.875, and each is a
+// 8-bit states: 256 values share a float32 unit, the largest of them over 1.875 (2^127 at most: all codes have a value), and each is a
 // code of unit times a small float: eight codes an octave, the lowest octave linear down to zero.
 // First moments have a sign and 127 codes (2^17 between the smallest and largest), second moments
 // 255 (2^33).  A moment moves by a tenth or a thousandth of its distance a step, far below half
@@ -170,10 +170,22 @@ struct Rates {
 
 // a parameter's step.  Square root and reciprocal to a unit in the last place: the step is of
 // lr's size, its rounding far below the parameter's
+// LOW: also where v is subnormal, which the square root's instruction need not take.
+template <bool LOW>
 __device__ __forceinline__ float moved(float p, float m, float v, float decay, const Scalars& s, float eps) {
-  const float d = __builtin_amdgcn_sqrtf(v * s.c2) + eps;
+  const bool low = LOW && v < 0x1p-96f;
+  const float root = __builtin_amdgcn_sqrtf((low ? v * 0x1p64f : v) * s.c2), d = (low ? root * 0x1p-32f : root) + eps;
   return p * (1.f - s.lr * decay) - s.lr * (m * s.c1 * __builtin_amdgcn_rcpf(d));
 }
+
+// the same with moments of any size
+__device__ __forceinline__ float moved_far(float p, double m, double v, float decay, const Scalars& s, float eps) {
+  return p * (1.f - s.lr * decay) - s.lr * (float)(m * (double)s.c1 / (sqrt(v * (double)s.c2) + (double)eps));
+}
+// Second moments outside of these are not for moved<false>(): their roots are taken in 64 bits.  Below kLeast that
+// matters only where eps is as small.
+constexpr double kLeast = 0x1p-126, kMost = 0x1p100;
+constexpr float kSmallEps = 0x1p-39f;
 
 // eight values of a gradient or parameter, by the type's chunks
 template <typename T>
@@ -209,7 +221,7 @@ __global__ void __launch_bounds__(kThreads)
     const float w = g[j] * f;
     x[j] = b1 * x[j] + r1 * w;
     y[j] = b2 * y[j] + r2 * (w * w);
-    p[j] = moved(p[j], x[j], y[j], e.decay, s, b.eps);
+    p[j] = moved<true>(p[j], x[j], y[j], e.decay, s, b.eps);
   }
   store8(m + e.offset + at, kValues, x);
   store8(v + e.offset + at, kValues, y);
@@ -271,13 +283,19 @@ __global__ void __launch_bounds__(kThreads)
     y[j] = b.beta2 * ((double)second_value(cv) * vu) + b.rest2 * (w * w);
     top_x = fmax(top_x, fabs(x[j]));
     top_y = fmax(top_y, y[j]);
-    p[j] = moved(p[j], (float)x[j], (float)y[j], e.decay, s, b.eps);
+    p[j] = moved<false>(p[j], (float)x[j], (float)y[j], e.decay, s, b.eps);
     bad |= !(fabsf(g[j]) < INFINITY);
   }
-  if (bad) {
+  const double least = b.eps < kSmallEps ? kLeast : 0.0;
+  if (least > 0.0) {
+#pragma unroll
+    for (int j = 0; j < kValues; ++j) bad |= y[j] > 0.0 && y[j] < least;
+  }
+  if (bad || top_y >= kMost) {
     top_x = top_y = 0.0;
 #pragma unroll
     for (int j = 0; j < kValues; ++j) {
+      if (j < left && y[j] > 0.0 && (y[j] < least || y[j] >= kMost)) p[j] = moved_far(e.p[at + j], x[j], y[j], e.decay, s, b.eps);
       // no code stands for what is not finite, and its block's others go on
       if (!(fabsf(g[j]) < INFINITY)) x[j] = y[j] = 0.0;
       top_x = fmax(top_x, fabs(x[j]));
@@ -285,7 +303,8 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   // rounding does not change which is the largest
-  const float ux = block_max((float)(top_x * (1.0 / 1.875))), uy = block_max((float)(top_y * (1.0 / 1.875)));
+  const float ux = fminf(block_max((float)(top_x * (1.0 / 1.875))), 0x1p127f);
+  const float uy = fminf(block_max((float)(top_y * (1.0 / 1.875))), 0x1p127f);
   const double ix = ux > 0.f ? 1.0 / (double)ux : 0.0, iy = uy > 0.f ? 1.0 / (double)uy : 0.0;
   DropArgs d;
   d.k0 = k0;
@@ -424,7 +443,9 @@ hipError_t adamw_step(const AdamArgs& a) {
     hipLaunchKernelGGL(k_adam_begin, dim3(1), dim3(kThreads), 0, a.stream, s, static_cast<const double*>(a.ws), parts, start);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const Rates b{a.beta1, a.beta2, 1.0 - a.beta1, 1.0 - a.beta2, (float)a.eps};
+  // the reciprocal's instruction need not take a subnormal eps
+  const float eps = a.eps > 0 ? std::max((float)a.eps, 0x1p-126f) : 0.f;
+  const Rates b{a.beta1, a.beta2, 1.0 - a.beta1, 1.0 - a.beta2, eps};
   return each_launch(a.n_tensors, a.sizes, [&](int first, int n, int64_t chunk, int64_t chunks) {
     Run r;
     Grads g;

@@ -43,3 +43,50 @@ def test_bad_gradients_stay_with_their_parameters(tpc, bad, dtype):
         assert same(a.state()[1:], b.state()[1:])
         assert all((m[:1000][~keep] == 0).all() for m in a.moments())
 
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_huge_gradients(tpc, bits):
+    """Squares past the largest float32: an 8-bit block's unit ends there, and its other values stay numbers."""
+    r = np.random.default_rng(8)
+    p = [dev(r.normal(size=600))]
+    opt = tpc.AdamW(p, lr=LR, betas=(B1, B2), eps=EPS, weight_decay=0.1, bits=bits, seed=5)
+    for t in range(1, 4):
+        g = r.normal(size=600)
+        g[[5, 300]] = 3e38, -1e25
+        g = [dev(g)]
+        p0, before = [x.clone() for x in p], opt.state()
+        opt.step(g)
+        assert torch.isfinite(p[0]).all()
+        if bits == 8:
+            check_step(opt, before, p0, g, p, t, [0.1], None, None, [None])
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-30, 1e-8])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_tiny_gradients_and_eps(tpc, bits, eps):
+    """Second moments that are subnormal in float32, or below it: the step is the formula's on the moments that the
+    step has (float32 ones with 32 bits), and zeros over a small eps are zeros.  An eps below 2^-126 counts as that.
+    In float32 (1 - beta2) g^2 ends at 0 where g^2 is below 2^-150 / (1 - beta2) and its own rounding, half of
+    2^-149: g below 8.7e-22; with eps 0 such a gradient is divided by nothing."""
+    r = np.random.default_rng(9)
+    n = 900
+    g = r.choice([-1.0, 1.0], size=n) * 10.0 ** r.uniform(-21.5 if bits == 32 else -30, -17, size=n)
+    g[:300] = 10.0 ** r.uniform(-12, 0, size=300)
+    if eps:
+        g[100:140] = 0
+    g, p = dev(g), dev(r.normal(size=n))
+    start = f64(p)
+    opt = tpc.AdamW([p], lr=LR, betas=(B1, B2), eps=eps, weight_decay=0.1, bits=bits)
+    opt.step([g])
+    G = f64(g)
+    if bits == 32:
+        m, v = f64(opt.exp_avg)[:n], f64(opt.exp_avg_sq)[:n]
+        assert (v[np.abs(G) > 8.7e-22] > 0).all()
+    else:
+        m, v = (1 - B1) * G, (1 - B2) * G * G
+    e = max(eps, 2.0 ** -126) if eps else 0.0
+    some = (v > 0) | (e > 0)
+    with np.errstate(divide="ignore"):
+        step = LR * (m / (1 - B1)) / (np.sqrt(v / (1 - B2)) + e)
+    assert not torch.isfinite(p[torch.tensor(~some, device="cuda")]).any()
+    near(p[torch.tensor(some, device="cuda")], (start * (1 - LR * 0.1) - step)[some], (32 * U * np.abs(step) + 4 * U * np.abs(start))[some], "p")
