@@ -321,7 +321,8 @@ class AdamW:
 
     The states of tensor i lie from ``offsets[i]`` on in ``exp_avg`` and ``exp_avg_sq`` (with bits 8 codes,
     whose units of 256 values each are ``exp_avg_unit`` and ``exp_avg_sq_unit``).  One optimiser serves
-    one stream at a time."""
+    one stream at a time.  Parameters and copies stay where they are: copy new values into them; a step after
+    their ``.data`` was set to another tensor is refused."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, max_norm=None, bits=32, copies=None,
                  seed=0):
@@ -346,6 +347,9 @@ class AdamW:
             if first < end:
                 raise ValueError("a parameter or copy is there twice, or two overlap")
             end = last
+        # the table holds addresses: of memory that stays the optimiser's even where a tensor is given other
+        self._written = [t for t in (*params, *copies) if t is not None]
+        self._places, self._held = list(map(_address_of, self._written)), [t.detach() for t in self._written]
         self.params, self.copies, self.bits, self.betas, self.eps, self.max_norm = params, copies, bits, betas, eps, max_norm
         self.lr, self.seed = lr, seed
         self.numels = [p.numel() for p in params]
@@ -389,6 +393,8 @@ class AdamW:
                 and list(map(_device_of, grads)).count(dev) == n):
             for i, (g, shape) in enumerate(zip(grads, self._shapes)):
                 _need(g, f"grads[{i}]", dt, shape, dev)
+        if list(map(_address_of, self._written)) != self._places:
+            raise ValueError("a parameter or copy has moved since the optimiser was made (its .data was set)")
         where = array.array("Q", map(_address_of, grads))
         lr = self.lr if lr is None else lr
         lr_at = None

@@ -90,3 +90,26 @@ def test_tiny_gradients_and_eps(tpc, bits, eps):
         step = LR * (m / (1 - B1)) / (np.sqrt(v / (1 - B2)) + e)
     assert not torch.isfinite(p[torch.tensor(~some, device="cuda")]).any()
     near(p[torch.tensor(some, device="cuda")], (start * (1 - LR * 0.1) - step)[some], (32 * U * np.abs(step) + 4 * U * np.abs(start))[some], "p")
+
+
+def test_a_parameter_that_has_moved_is_refused(tpc):
+    """The addresses are the optimiser's from its start: it writes nothing where a parameter was before."""
+    p, low = [torch.nn.Parameter(torch.ones(300, device="cuda")) for _ in range(2)], torch.zeros(300, device="cuda", dtype=torch.bfloat16)
+    opt = tpc.AdamW(p, copies=[None, low])
+    g = [torch.ones(300, device="cuda") for _ in p]
+    opt.step(g)
+    p[0].data.copy_(torch.zeros(300))      # other values in the same place are what it goes on from
+    opt.step(g)
+    assert float(p[0][0]) < 0 < float(p[1][0]) < 1
+    was, t = p[1].data, opt.state()[0]
+    p[1].data = was.clone()
+    keep = was.clone()
+    with pytest.raises(ValueError, match="moved"):
+        opt.step(g)
+    assert torch.equal(was, keep) and torch.equal(p[1], keep) and opt.state()[0] == t == 2
+    p[1].data = was
+    opt.step(g)
+    assert float(p[1][0]) < float(keep[0])
+    low.data = low.clone()
+    with pytest.raises(ValueError, match="moved"):
+        opt.step(g)
