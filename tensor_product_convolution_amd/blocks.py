@@ -382,7 +382,7 @@ class AdamW:
 
     def step(self, grads, lr=None):
         """One step with ``grads``, contiguous tensors of the parameters' shapes, all float32 or all
-        bfloat16.  Returns their norm (a float32 tensor of one value), or None without max_norm."""
+        bfloat16 (None is refused: a step moves every parameter).  Returns their norm (a float32 tensor of one value), or None without max_norm."""
         if len(grads) != self._n:
             raise ValueError(f"{len(grads)} gradients for {self._n} parameters")
         code, _ = _code(grads[0], "grads[0]")
@@ -410,6 +410,7 @@ class AdamW:
         a.beta1, a.beta2 = self.betas
         a.eps, a.seed = self.eps, self.seed
         _call(dev, lib().tp_adamw_step, ctypes.byref(a), where.buffer_info()[0], _at(norm), self._ws.data_ptr(), self._ws_bytes)
+        torch.autograd.graph.increment_version(self._written)  # a graph that saved one of them is not right any more
         return norm
 
     def moments(self):

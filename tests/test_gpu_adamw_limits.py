@@ -113,3 +113,16 @@ def test_a_parameter_that_has_moved_is_refused(tpc):
     low.data = low.clone()
     with pytest.raises(ValueError, match="moved"):
         opt.step(g)
+
+
+def test_autograd_knows_of_a_step(tpc):
+    """A graph that saved a parameter before the step is refused its backward, as after any other write in place."""
+    p, low = torch.nn.Parameter(torch.ones(30, device="cuda")), torch.zeros(30, device="cuda", dtype=torch.bfloat16)
+    opt = tpc.AdamW([p], copies=[low])
+    (p * p).sum().backward()
+    loss, versions = (p * p).sum(), (p._version, low._version)
+    opt.step([p.grad])
+    assert p._version > versions[0] and low._version > versions[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    (p * p).sum().backward()
