@@ -126,3 +126,44 @@ def test_autograd_knows_of_a_step(tpc):
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
     (p * p).sum().backward()
+
+
+def mean_of_200_steps(c, start, step):
+    """Of the moments over where they belong, less 1, of values that are not the largest of their blocks."""
+    n, t = len(c), 200
+    others = np.arange(n) % 256 != 0
+    held = ob.decode(*start[:2], False), ob.decode(*start[2:], True)
+    want = c + (held[0] - c) * B1 ** t, c * c + (held[1] - c * c) * B2 ** t
+    for i in range(t):
+        got = step(i)
+    return [float((g / w)[others].mean()) - 1 for g, w in zip(got, want)]
+
+
+def slow_moments():
+    """A value in each block that stays where it is and holds the unit, and others whose moments start at half and a
+    quarter of where they go."""
+    n = 256 * 80
+    c = (10.0 ** np.random.default_rng(2).uniform(-1.5, -0.2, size=n)).astype(np.float32).astype(np.float64)
+    c[::256] = 1.0
+    part = np.where(np.arange(n) % 256 != 0, 0.5, 1.0)
+    return c, (*ob.encode(part * c, False, 0.5), *ob.encode((part * c) ** 2, True, 0.5))
+
+
+# Derived: a rounding's standard deviation is at most half a code's distance, a sixteenth of the value.  Second moments keep
+# each of the 200, 200^(1/2) / 16 in all, first moments 1 / (1 - 0.9^2)^(1/2) / 16; five times that over 20,400 values.
+SPREAD = 5 / 16 / 20400 ** 0.5 / (1 - B1 ** 2) ** 0.5, 5 / 16 * (200 / 20400) ** 0.5
+
+
+def test_moments_move_by_less_than_half_a_code(tpc):
+    c, start = slow_moments()
+    opt = tpc.AdamW([dev(np.zeros(len(c)))], lr=0.0, betas=(B1, B2), weight_decay=0.0, bits=8, seed=11)
+    opt.load(1000, *[torch.tensor(t, device="cuda") for t in (start[0], start[2], start[1], start[3])])
+    g = [dev(c)]
+
+    def step(i):
+        opt.step(g)
+        return [f64(m) for m in opt.moments()] if i == 199 else None
+
+    off = mean_of_200_steps(c, start, step)
+    print(off, SPREAD)
+    assert abs(off[0]) < SPREAD[0] and abs(off[1]) < SPREAD[1]
