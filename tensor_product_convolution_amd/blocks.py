@@ -61,7 +61,7 @@ def rotary_frequencies(n_pairs, axes=1, base=1e4, stretch=1.0, trained=None, few
     head_norm_rotate_forward: pair i turns with axis i % axes.
 
     stretch: the length to serve over the length trained for; all frequencies are divided by it.
-    With ``trained`` (that length) only the slow ones are: a pair that makes more than ``many``
+    With ``trained`` (that length) only the slow ones are, by parts (Peng, Quesnelle, Fan and Shippole, 2023): a pair that makes more than ``many``
     turns over it keeps its frequency, one with fewer than ``few`` is divided by ``stretch``, those
     between go over linearly in the number of turns."""
     if n_pairs < 0 or axes < 1 or not stretch > 0 or not base > 0:
@@ -315,7 +315,7 @@ class AdamW:
     weight_decay: one number, or one for each tensor.  max_norm: the gradients are scaled down to this
     2-norm over all of them (None: not; float("inf"): the norm is only returned), and a step whose
     norm is not finite changes nothing.  bits: 32, or 8 for states of one byte a value (rounded at
-    random, from ``seed`` and the step's number).  copies: bfloat16 tensors (or None) that get the new
+    random, from ``seed`` and the step's number; without max_norm a gradient that is not finite leaves zeros there).  copies: bfloat16 tensors (or None) that get the new
     parameters too.  lr: a number, or a float32 tensor of one value on the GPU, read by every step: the
     way to change it under a captured graph.
 

