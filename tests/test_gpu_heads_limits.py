@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import blocks as ob
-from tests._blocks import DT, U, dev, f64, ints, near, same, torch
+from tests._blocks import U, f64, torch
 from tests.test_gpu_heads import check, problem
 
 pytestmark = pytest.mark.gpu
